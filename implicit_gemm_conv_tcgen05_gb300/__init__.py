@@ -20,6 +20,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
 HEADER = os.path.join(_ROOT, "include", "igc.h")
 DEBUG_HEADER = os.path.join(_ROOT, "include", "igc_debug.h")
+FFN_HEADER = os.path.join(_ROOT, "include", "igc_ffn.h")
 
 IGC_OK = 0
 IGC_ERR_INVALID_ARG = 1
@@ -31,6 +32,11 @@ IGC_ERR_WORKSPACE = 6
 IGC_F32 = 0
 IGC_F16 = 1
 IGC_BF16 = 2
+IGC_ACT_NONE = 0
+IGC_ACT_RELU = 1
+IGC_ACT_GELU = 2
+IGC_ACT_GELU_TANH = 3
+IGC_ACT_SILU = 4
 
 _lock = threading.Lock()
 _lib = None
@@ -110,6 +116,28 @@ def lib() -> ctypes.CDLL:
             L.igc_plan_gemm.restype = i32
             L.igc_debug_wait_timeout_probe.argtypes = [vp]
             L.igc_debug_wait_timeout_probe.restype = i32
+            f32 = ctypes.c_float
+            L.linear_act.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i32, i32, vp, i64,
+                                     vp, i64, vp, i64, i32, vp]
+            L.linear_act.restype = i32
+            L.linear_act_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i64,
+                                              vp, i64, vp, i64, vp, i64, i32, vp, i32, vp, sz, vp]
+            L.linear_act_backward.restype = i32
+            L.gated_ffn.argtypes = [i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp, i32, i32,
+                                    vp, vp, i64, vp, i64, vp]
+            L.gated_ffn.restype = i32
+            L.gated_ffn_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, vp, i64, i32, vp,
+                                             i64, vp, vp, i64, vp, i64, vp, vp, i64, i32, vp, vp,
+                                             i32, vp, sz, vp]
+            L.gated_ffn_backward.restype = i32
+            for name in ("linear_act_backward_workspace_size",
+                         "gated_ffn_backward_workspace_size"):
+                getattr(L, name).argtypes = [i64, i64, i64]
+                getattr(L, name).restype = sz
+            L.grad_norm_clip.argtypes = [i64, vp, vp, vp, vp, f32, f32, vp, vp, sz, vp]
+            L.grad_norm_clip.restype = i32
+            L.grad_norm_clip_workspace_size.argtypes = [i64]
+            L.grad_norm_clip_workspace_size.restype = sz
             L.igc_version.argtypes = []
             L.igc_version.restype = ctypes.c_char_p
             _lib = L
@@ -497,3 +525,339 @@ def conv2d_nhwc_s8_zp(x, w, zX, zW=0, zW_k=None, y32=None, y8=None, scale=0.0, s
                                  _stream(stream))
     _check(rc, "conv2d_nhwc_s8_zp")
     return y32, y8
+
+
+# ---------------------------------------------------------------------------
+# feed-forward operators (include/igc_ffn.h)
+# ---------------------------------------------------------------------------
+
+_ACTS = {"none": IGC_ACT_NONE, "relu": IGC_ACT_RELU, "gelu": IGC_ACT_GELU,
+         "gelu_tanh": IGC_ACT_GELU_TANH, "silu": IGC_ACT_SILU}
+_dtype_codes = {}
+
+
+def _dtype_code(dtype):
+    """IGC_F32 / IGC_F16 / IGC_BF16 of a torch dtype, None for any other."""
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float32: IGC_F32, torch.float16: IGC_F16,
+                             torch.bfloat16: IGC_BF16})
+    return _dtype_codes.get(dtype)
+
+
+def _operand_code(t, name):
+    code = _dtype_code(t.dtype)
+    if code is None or code == IGC_F32:
+        raise TypeError(f"{name} has dtype {t.dtype}: fp16 or bf16 is needed")
+    return code
+
+
+def _act_code(act):
+    try:
+        return _ACTS[act]
+    except KeyError:
+        raise ValueError(f"act is {act!r}: one of {', '.join(_ACTS)}") from None
+
+
+def _mat(t, name, dtypes, rows, cols):
+    """Row stride (in elements) of a rows x cols matrix: unit inner stride, rows that
+    do not overlap (so no broadcast view), one of `dtypes`.  A single row has no
+    stride of its own: it gets one that suits TMA."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    s0, s1 = t.stride()
+    if (s1 != 1 and cols > 1) or (s0 < cols and rows > 1):
+        raise ValueError(f"{name} must be row-major with unit inner stride and rows apart")
+    return s0 if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _vec_code(v, name, dtypes, n):
+    """dtype code of an optional vector of n elements (IGC_F32 for none)."""
+    if v is None:
+        return IGC_F32
+    if v.dtype not in dtypes or v.dim() != 1 or v.shape[0] != n or not v.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of length {n} and type "
+                         f"{' or '.join(str(d) for d in dtypes)}")
+    return _dtype_code(v.dtype)
+
+
+def _two_dims(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape
+
+
+def _one_device(*pairs):
+    """Checks that all tensors given are on one CUDA device, and makes it current."""
+    dev = None
+    for name, t in pairs:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name} is on another device")
+    import torch
+    if dev is not None and torch.cuda.current_device() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+
+
+def _new(shape, dtype, device, stream):
+    """An uninitialised tensor that is safe to use on `stream` (None: the current one):
+    memory that the caching allocator hands out belongs to the stream it was asked on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(workspace, need, device, stream):
+    import torch
+    if workspace is None:
+        return _new(max(need, 1), torch.uint8, device, stream)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return workspace
+
+
+def linear_act(X, W, bias=None, act="none", residual=None, Y=None, Z=None, stream=None):
+    """Y = act(X W^T + bias) + residual; X (M,K), W (N,K), residual and Z (M,N) of one
+    type (fp16 or bf16), Y (M,N) of that type or fp32, bias (N) of that type or fp32.
+    Z, if given, receives the pre-activation for linear_act_backward.  residual may be
+    Y itself.  Returns Y (allocated if None)."""
+    import torch
+    dt = _operand_code(X, "X")
+    code = _act_code(act)
+    M, K = _two_dims(X, "X")
+    N = _two_dims(W, "W")[0]
+    own = (X.dtype,)
+    either = (X.dtype, torch.float32)
+    ldx, ldw = _mat(X, "X", own, M, K), _mat(W, "W", own, N, K)
+    ldr = _mat(residual, "residual", own, M, N) if residual is not None else 0
+    ldz = _mat(Z, "Z", own, M, N) if Z is not None else 0
+    ldy = _mat(Y, "Y", either, M, N) if Y is not None else 0
+    bt = _vec_code(bias, "bias", either, N)
+    _one_device(("X", X), ("W", W), ("bias", bias), ("residual", residual), ("Y", Y), ("Z", Z))
+    if Y is None:
+        Y = _new((M, N), X.dtype, X.device, stream)
+        ldy = N
+    rc = lib().linear_act(M, N, K, dt, X.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(bias), bt, code,
+                          _ptr(residual), ldr, _ptr(Z), ldz, Y.data_ptr(), ldy,
+                          _dtype_code(Y.dtype), _stream(stream))
+    _check(rc, "linear_act")
+    return Y
+
+
+def linear_act_backward_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().linear_act_backward_workspace_size(M, N, K))
+
+
+def linear_act_backward(dY, X, W, act="none", Z=None, dX=None, dW=None, dbias=None,
+                        workspace=None, stream=None):
+    """Gradients of linear_act from dY (M,N) and the pre-activation Z (M,N) that it kept
+    (not needed without an activation): dX (M,K), dW (N,K), dbias (N).  The ones given
+    are computed (X is needed for dW, W for dX; the other may be None); with none
+    given, dX and dW are allocated.  dW and dbias may be fp32.  Returns (dX, dW, dbias)."""
+    import torch
+    dt = _operand_code(dY, "dY")
+    code = _act_code(act)
+    M, N = _two_dims(dY, "dY")
+    if dX is None and dW is None and dbias is None:
+        if X is None or W is None:
+            raise ValueError("X and W are needed for dX and dW")
+        dX = _new(X.shape, dY.dtype, dY.device, stream)
+        dW = _new(W.shape, dY.dtype, dY.device, stream)
+    if (dX is not None and W is None) or (dW is not None and X is None):
+        raise ValueError("dX needs W and dW needs X")
+    if code != IGC_ACT_NONE and Z is None:
+        raise ValueError("Z, the pre-activation, is needed with an activation")
+    k_of = W if W is not None else X
+    K = _two_dims(k_of, "W" if W is not None else "X")[1] if k_of is not None else 0
+    own = (dY.dtype,)
+    either = (dY.dtype, torch.float32)
+    lddy = _mat(dY, "dY", own, M, N)
+    ldz = _mat(Z, "Z", own, M, N) if Z is not None else 0
+    ldx = _mat(X, "X", own, M, K) if X is not None else 0
+    ldw = _mat(W, "W", own, N, K) if W is not None else 0
+    lddx = _mat(dX, "dX", own, M, K) if dX is not None else 0
+    lddw = _mat(dW, "dW", either, N, K) if dW is not None else 0
+    bt = _vec_code(dbias, "dbias", either, N)
+    _one_device(("dY", dY), ("X", X), ("W", W), ("Z", Z), ("dX", dX), ("dW", dW),
+                ("dbias", dbias), ("workspace", workspace))
+    ws = _workspace(workspace, linear_act_backward_workspace_size(M, N, K), dY.device, stream)
+    rc = lib().linear_act_backward(M, N, K, dt, dY.data_ptr(), lddy, _ptr(Z), ldz, code, _ptr(X),
+                                   ldx, _ptr(W), ldw, _ptr(dX), lddx, _ptr(dW), lddw,
+                                   _dtype_code(dW.dtype) if dW is not None else IGC_F32,
+                                   _ptr(dbias), bt, ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(rc, "linear_act_backward")
+    return dX, dW, dbias
+
+
+def gated_ffn(X, Wg, Wu, bg=None, bu=None, act="silu", H=None, G=None, U=None, stream=None):
+    """H = act(X Wg^T + bg) * (X Wu^T + bu); X (M,K), Wg and Wu (F,K) with one row stride
+    (two matrices, or the halves of a (2F,K) one), H (M,F), all of one type (fp16 or
+    bf16); bg and bu (F) of that type or fp32.  G and U, if given, receive the two
+    pre-activations for gated_ffn_backward.  Returns H (allocated if None)."""
+    import torch
+    dt = _operand_code(X, "X")
+    code = _act_code(act)
+    M, K = _two_dims(X, "X")
+    F = _two_dims(Wg, "Wg")[0]
+    own = (X.dtype,)
+    ldx = _mat(X, "X", own, M, K)
+    ldw = _mat(Wg, "Wg", own, F, K)
+    if _mat(Wu, "Wu", own, F, K) != ldw:
+        raise ValueError("Wg and Wu must have one row stride")
+    if (G is None) != (U is None):
+        raise ValueError("G and U go together")
+    ldh = _mat(H, "H", own, M, F) if H is not None else 0
+    ldgu = 0
+    if G is not None:
+        ldgu = _mat(G, "G", own, M, F)
+        if _mat(U, "U", own, M, F) != ldgu:
+            raise ValueError("G and U must have one row stride")
+    either = (X.dtype, torch.float32)
+    bt = _vec_code(bg, "bg", either, F)
+    but = _vec_code(bu, "bu", either, F)
+    if bg is not None and bu is not None and bt != but:
+        raise ValueError("bg and bu must have one type")
+    _one_device(("X", X), ("Wg", Wg), ("Wu", Wu), ("bg", bg), ("bu", bu), ("H", H), ("G", G),
+                ("U", U))
+    if H is None:
+        H = _new((M, F), X.dtype, X.device, stream)
+        ldh = F
+    rc = lib().gated_ffn(M, F, K, dt, X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw,
+                         _ptr(bg), _ptr(bu), bt if bg is not None else but, code, _ptr(G),
+                         _ptr(U), ldgu, H.data_ptr(), ldh, _stream(stream))
+    _check(rc, "gated_ffn")
+    return H
+
+
+def gated_ffn_backward_workspace_size(M: int, F: int, K: int) -> int:
+    return int(lib().gated_ffn_backward_workspace_size(M, F, K))
+
+
+def gated_ffn_backward(dH, G, U, X, Wg, Wu, act="silu", dX=None, dWg=None, dWu=None, dbg=None,
+                       dbu=None, workspace=None, stream=None):
+    """Gradients of gated_ffn from dH (M,F) and the pre-activations G and U (M,F) that it
+    kept: dX (M,K), dWg and dWu (F,K), dbg and dbu (F).  The ones given are computed
+    (the pairs go together; X is needed for the weights', Wg and Wu for dX); with none
+    given, dX, dWg and dWu are allocated.  The weights' and biases' may be fp32.
+    Returns (dX, dWg, dWu, dbg, dbu)."""
+    import torch
+    dt = _operand_code(dH, "dH")
+    code = _act_code(act)
+    M, F = _two_dims(dH, "dH")
+    if (Wg is None) != (Wu is None) or (dWg is None) != (dWu is None) or \
+            (dbg is None) != (dbu is None):
+        raise ValueError("Wg and Wu, dWg and dWu, and dbg and dbu go together")
+    if dX is None and dWg is None and dbg is None:
+        if X is None or Wg is None:
+            raise ValueError("X, Wg and Wu are needed for dX, dWg and dWu")
+        dX = _new(X.shape, dH.dtype, dH.device, stream)
+        dWg = _new(Wg.shape, dH.dtype, dH.device, stream)
+        dWu = _new(Wg.shape, dH.dtype, dH.device, stream)
+    if (dX is not None and Wg is None) or (dWg is not None and X is None):
+        raise ValueError("dX needs Wg and Wu, dWg and dWu need X")
+    k_of = Wg if Wg is not None else X
+    K = _two_dims(k_of, "Wg" if Wg is not None else "X")[1] if k_of is not None else 0
+    own = (dH.dtype,)
+    either = (dH.dtype, torch.float32)
+    lddh = _mat(dH, "dH", own, M, F)
+    ldgu = _mat(G, "G", own, M, F)
+    if _mat(U, "U", own, M, F) != ldgu:
+        raise ValueError("G and U must have one row stride")
+    ldx = _mat(X, "X", own, M, K) if X is not None else 0
+    ldw = 0
+    if Wg is not None:
+        ldw = _mat(Wg, "Wg", own, F, K)
+        if _mat(Wu, "Wu", own, F, K) != ldw:
+            raise ValueError("Wg and Wu must have one row stride")
+    lddx = _mat(dX, "dX", own, M, K) if dX is not None else 0
+    lddw = 0
+    if dWg is not None:
+        lddw = _mat(dWg, "dWg", either, F, K)
+        if _mat(dWu, "dWu", (dWg.dtype,), F, K) != lddw:
+            raise ValueError("dWg and dWu must have one row stride")
+    bt = _vec_code(dbg, "dbg", either, F)
+    if _vec_code(dbu, "dbu", either, F) != bt:
+        raise ValueError("dbg and dbu must have one type")
+    _one_device(("dH", dH), ("G", G), ("U", U), ("X", X), ("Wg", Wg), ("Wu", Wu), ("dX", dX),
+                ("dWg", dWg), ("dWu", dWu), ("dbg", dbg), ("dbu", dbu), ("workspace", workspace))
+    ws = _workspace(workspace, gated_ffn_backward_workspace_size(M, F, K), dH.device, stream)
+    rc = lib().gated_ffn_backward(M, F, K, dt, dH.data_ptr(), lddh, G.data_ptr(), U.data_ptr(),
+                                  ldgu, code, _ptr(X), ldx, _ptr(Wg), _ptr(Wu), ldw, _ptr(dX),
+                                  lddx, _ptr(dWg), _ptr(dWu), lddw,
+                                  _dtype_code(dWg.dtype) if dWg is not None else IGC_F32,
+                                  _ptr(dbg), _ptr(dbu), bt, ws.data_ptr(), ws.numel(),
+                                  _stream(stream))
+    _check(rc, "gated_ffn_backward")
+    return dX, dWg, dWu, dbg, dbu
+
+
+def grad_norm_clip_workspace_size(count: int) -> int:
+    return int(lib().grad_norm_clip_workspace_size(int(count)))
+
+
+def grad_norm_clip(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None, stream=None):
+    """Clips the global 2-norm of `grads` (a sequence of contiguous fp32, fp16 or bf16
+    tensors, types may differ): each becomes g * min(1, max_norm / (norm + eps)), in place
+    or in `out` (tensors of the same sizes and types).  out=False: the norm alone.
+    Returns the norm, a one-element fp32 CUDA tensor (`norm`, or allocated); nothing
+    waits for the GPU."""
+    import torch
+    grads = list(grads)
+    if out is None:
+        outs = grads
+    elif out is False:
+        outs = None
+    else:
+        outs = list(out)
+        if len(outs) != len(grads):
+            raise ValueError("out must have as many tensors as grads")
+    codes, sizes, ptrs = [], [], []
+    for g in grads:
+        code = _dtype_code(g.dtype)
+        if code is None:
+            raise TypeError(f"a gradient has dtype {g.dtype}")
+        if not g.is_contiguous():
+            raise ValueError("gradients must be contiguous")
+        if not g.is_cuda:
+            raise ValueError("gradients must be CUDA tensors")
+        codes.append(code)
+        sizes.append(g.numel())
+        ptrs.append(g.data_ptr())
+    out_ptrs = ptrs
+    if outs is not None and outs is not grads:
+        out_ptrs = []
+        for o, g in zip(outs, grads):
+            if o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous() or \
+                    not o.is_cuda:
+                raise ValueError("out must match grads in type and size, contiguous, on CUDA")
+            out_ptrs.append(o.data_ptr())
+    if norm is not None and (norm.dtype != torch.float32 or norm.numel() != 1 or
+                             not norm.is_cuda):
+        raise ValueError("norm must be a one-element fp32 CUDA tensor")
+    n = len(grads)
+    device = grads[0].device if n else (norm.device if norm is not None else "cuda")
+    if any(g.device != device for g in grads[1:]):
+        raise ValueError("gradients must be on one device")
+    if norm is None:
+        norm = _new((), torch.float32, device, stream)
+    _one_device(("grads", grads[0] if n else None), ("norm", norm), ("workspace", workspace))
+    ws = _workspace(workspace, grad_norm_clip_workspace_size(n), device, stream)
+    vps, i64s, i32s = ctypes.c_void_p * n, ctypes.c_int64 * n, ctypes.c_int32 * n
+    rc = lib().grad_norm_clip(n, vps(*ptrs), i64s(*sizes), i32s(*codes),
+                              None if outs is None else vps(*out_ptrs), float(max_norm),
+                              float(eps), norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                              _stream(stream))
+    _check(rc, "grad_norm_clip")
+    return norm

@@ -1,0 +1,261 @@
+// The pass through the activation of the feed-forward backward passes, with the bias
+// gradients, and the forward pass of an empty contraction.
+//
+//   linear:  dZ = dY act'(Z)                    db  = column sums of dZ
+//   gated:   dU = dH act(G), dG = dH U act'(G)  dbg, dbu = column sums of dG, dU
+//
+// One pass over memory: a thread keeps 8 adjacent columns (one 16-byte access per
+// matrix and row) and walks down the rows of its chunk, so the column sums stay in its
+// registers (fp32) and cost no second read.  The 8 warps of a block take every eighth
+// row; their sums meet in shared memory, one row of partial sums per chunk goes to the
+// workspace, and a second kernel adds the chunks in order (no atomics).
+#include "ffn_act.cuh"
+#include "ffn_host.h"
+#include "sm100_ptx.cuh"
+
+namespace igc {
+
+namespace {
+
+constexpr int kCols = 256;      // columns of a block: 32 lanes x 8
+constexpr int kRowLanes = 8;    // warps of a block
+constexpr int kMaxChunks = 256;
+
+struct DactParams {
+  int M, N;
+  int rows_per_chunk;
+  int bf16, act;
+  const uint16_t* dO;
+  const uint16_t* Z;
+  const uint16_t* U;
+  long long ldo, ldz, ldu;
+  int o_vec, z_vec, u_vec;
+  uint16_t* D0;
+  uint16_t* D1;
+  long long ldd;
+  float* partial0;
+  float* partial1;
+};
+
+// 8 elements of a row from column n (zeros past N).
+__device__ __forceinline__ void load8(const uint16_t* row, int n, int N, bool vec, bool bf16,
+                                      float (&v)[8]) {
+  if (vec && n + 8 <= N) {
+    const uint4 q = *reinterpret_cast<const uint4*>(row + n);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack16(w[i], bf16);
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = n + i < N ? load16(row, n + i, bf16) : 0.0f;
+  }
+}
+
+// The workspace rows are padded to a multiple of 8 columns: always whole.
+__device__ __forceinline__ void save8(uint16_t* row, int n, bool bf16, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(row + n) =
+      make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16), pack16(v[4], v[5], bf16),
+                 pack16(v[6], v[7], bf16));
+}
+
+// Adds the block's 8 warps' column sums and writes them to the chunk's row of partial sums.
+__device__ __forceinline__ void block_sums(float (&red)[kRowLanes][kCols], const float (&s)[8],
+                                           float* partial, int N) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[warp][lane * 8 + i] = s[i];
+  __syncthreads();
+  const int n = blockIdx.x * kCols + threadIdx.x;
+  if (n < N) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowLanes; ++w) t += red[w][threadIdx.x];
+    partial[static_cast<long long>(blockIdx.y) * N + n] = t;
+  }
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kRowLanes * 32) dact_kernel(const DactParams p) {
+  __shared__ float red[kRowLanes][kCols];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n = blockIdx.x * kCols + lane * 8;
+  const long long r0 = static_cast<long long>(blockIdx.y) * p.rows_per_chunk;
+  const long long r1 = min(static_cast<long long>(p.M), r0 + p.rows_per_chunk);
+  const bool bf16 = p.bf16 != 0;
+  float s0[8] = {}, s1[8] = {};
+  if (n < p.N) {
+    with_act(p.act, [&](auto a) {
+      constexpr int kAct = decltype(a)::value;
+#pragma unroll 2
+      for (long long r = r0 + warp; r < r1; r += kRowLanes) {
+        float o[8], z[8];
+        load8(p.dO + r * p.ldo, n, p.N, p.o_vec, bf16, o);
+        if (kGated || kAct != IGC_ACT_NONE) load8(p.Z + r * p.ldz, n, p.N, p.z_vec, bf16, z);
+        if constexpr (kGated) {
+          float u[8];
+          load8(p.U + r * p.ldu, n, p.N, p.u_vec, bf16, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float f, d;
+            act_grad_f32<kAct>(z[i], f, d);
+            z[i] = o[i] * u[i] * d;  // dG
+            u[i] = o[i] * f;         // dU
+            s0[i] += z[i];
+            s1[i] += u[i];
+          }
+          if (p.D0 != nullptr) {
+            save8(p.D0 + r * p.ldd, n, bf16, z);
+            save8(p.D1 + r * p.ldd, n, bf16, u);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (kAct != IGC_ACT_NONE) {
+              float f, d;
+              act_grad_f32<kAct>(z[i], f, d);
+              o[i] *= d;
+            }
+            s0[i] += o[i];
+          }
+          if (p.D0 != nullptr) save8(p.D0 + r * p.ldd, n, bf16, o);
+        }
+      }
+    });
+  }
+  if (p.partial0 != nullptr) block_sums(red, s0, p.partial0, p.N);
+  if (kGated && p.partial1 != nullptr) block_sums(red, s1, p.partial1, p.N);
+}
+
+// out[n] = sum over chunks of partial[chunk][n]; blockIdx.y: which vector.
+__global__ void __launch_bounds__(256) sum_chunks_kernel(const float* partial0,
+                                                         const float* partial1, int chunks, int N,
+                                                         void* out0, void* out1, int f32,
+                                                         int bf16) {
+  __shared__ float red[8][32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const float* partial = blockIdx.y ? partial1 : partial0;
+  void* out = blockIdx.y ? out1 : out0;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n = blockIdx.x * 32 + lane;
+  float t = 0.0f;
+  if (n < N)
+    for (int c = warp; c < chunks; c += 8) t += partial[static_cast<long long>(c) * N + n];
+  red[warp][lane] = t;
+  __syncthreads();
+  if (warp != 0 || n >= N) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) t += red[w][lane];
+  if (f32)
+    static_cast<float*>(out)[n] = t;
+  else
+    store16(out, n, t, bf16);
+}
+
+// ---------------------------------------------------------------------------
+// forward pass over a contraction of length zero: Z = bias
+// ---------------------------------------------------------------------------
+struct BiasOnlyParams {
+  int M, N;
+  int bf16, act, gated;
+  const void* bias0;
+  const void* bias1;
+  int bias_f32;
+  const void* R;
+  long long ldr;
+  void* out[3];
+  long long ld[3];
+  int f32_0;
+};
+
+__global__ void __launch_bounds__(256) bias_only_kernel(const BiasOnlyParams p) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long total = static_cast<long long>(p.M) * p.N;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  const bool bf16 = p.bf16 != 0;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += step) {
+    const long long m = i / p.N;
+    const int n = static_cast<int>(i - m * p.N);
+    const float z = load_vec(p.bias0, n, p.bias_f32, bf16);
+    float y = z;
+    with_act(p.act, [&](auto a) { y = act_f32<decltype(a)::value>(z); });
+    if (p.out[1] != nullptr) store16(p.out[1], m * p.ld[1] + n, z, bf16);
+    if (p.gated) {
+      const float u = load_vec(p.bias1, n, p.bias_f32, bf16);
+      y *= u;
+      if (p.out[2] != nullptr) store16(p.out[2], m * p.ld[2] + n, u, bf16);
+    } else if (p.R != nullptr) {
+      y += load16(p.R, m * p.ldr + n, bf16);
+    }
+    if (p.f32_0)
+      static_cast<float*>(p.out[0])[m * p.ld[0] + n] = y;
+    else
+      store16(p.out[0], m * p.ld[0] + n, y, bf16);
+  }
+}
+
+}  // namespace
+
+// Chunks of rows: enough blocks to fill the GPU several times over, at least 32 rows each.
+int64_t dact_chunks(int64_t M, int64_t N) {
+  const int64_t col_blocks = (N + kCols - 1) / kCols;
+  const int64_t most = (M + 31) / 32;
+  int64_t want = col_blocks > 0 ? (2432 + col_blocks - 1) / col_blocks : 1;
+  if (want > kMaxChunks) want = kMaxChunks;
+  if (want > most) want = most;
+  return want < 1 ? 1 : want;
+}
+
+int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream) {
+  DactParams p = {};
+  p.M = static_cast<int>(a.M), p.N = static_cast<int>(a.N);
+  const int64_t chunks = dact_chunks(a.M, a.N);
+  p.rows_per_chunk = static_cast<int>((a.M + chunks - 1) / chunks);
+  p.bf16 = a.dtype == IGC_BF16, p.act = a.act;
+  p.dO = static_cast<const uint16_t*>(a.dO.ptr), p.ldo = a.dO.ld;
+  p.Z = static_cast<const uint16_t*>(a.Z.ptr), p.ldz = a.Z.ld;
+  p.U = static_cast<const uint16_t*>(a.U.ptr), p.ldu = a.U.ld;
+  p.o_vec = operand_ok(a.dO.ptr, a.dO.ld);
+  p.z_vec = operand_ok(a.Z.ptr, a.Z.ld);
+  p.u_vec = operand_ok(a.U.ptr, a.U.ld);
+  p.D0 = static_cast<uint16_t*>(a.D0), p.D1 = static_cast<uint16_t*>(a.D1);
+  p.ldd = a.ldd;
+  if (a.db0 != nullptr) {
+    p.partial0 = a.partial;
+    p.partial1 = gated ? a.partial + chunks * a.N : nullptr;
+  }
+  const dim3 grid(static_cast<unsigned>((a.N + kCols - 1) / kCols), static_cast<unsigned>(chunks));
+  int rc = gated ? launch_pdl(dact_kernel<true>, grid, dim3(kRowLanes * 32), 0, stream, p)
+                 : launch_pdl(dact_kernel<false>, grid, dim3(kRowLanes * 32), 0, stream, p);
+  if (rc != IGC_OK || a.db0 == nullptr) return rc;
+  return launch_pdl(sum_chunks_kernel,
+                    dim3(static_cast<unsigned>((a.N + 31) / 32), gated ? 2 : 1), dim3(256), 0,
+                    stream, p.partial0, p.partial1, static_cast<int>(chunks), p.N, a.db0, a.db1,
+                    a.db_dtype == IGC_F32 ? 1 : 0, p.bf16);
+}
+
+int ffn_bias_only(const PointwiseArgs& a, bool gated, cudaStream_t stream) {
+  BiasOnlyParams p = {};
+  p.M = static_cast<int>(a.M), p.N = static_cast<int>(a.N);
+  p.bf16 = a.dtype == IGC_BF16, p.act = a.act, p.gated = gated;
+  p.bias0 = a.bias[0], p.bias1 = a.bias[1], p.bias_f32 = a.bias_dtype == IGC_F32;
+  p.R = a.R.ptr, p.ldr = a.R.ld;
+  for (int i = 0; i < 3; ++i) {
+    p.out[i] = const_cast<void*>(a.out[i].ptr);
+    p.ld[i] = a.out[i].ld;
+  }
+  p.f32_0 = a.out[0].dtype == IGC_F32;
+  const long long blocks = (static_cast<long long>(p.M) * p.N + 255) / 256;
+  return launch_pdl(bias_only_kernel, dim3(static_cast<unsigned>(blocks < 4864 ? blocks : 4864)),
+                    dim3(256), 0, stream, p);
+}
+
+}  // namespace igc

@@ -1,0 +1,66 @@
+// Host-side pieces shared by the feed-forward entry points (not part of the ABI).
+#pragma once
+
+#include "igc_ffn.h"
+#include "igc_host.h"
+
+namespace igc {
+
+inline size_t elem_size(int dtype) { return dtype == IGC_F32 ? 4 : 2; }
+inline bool is_operand_type(int dtype) { return dtype == IGC_F16 || dtype == IGC_BF16; }
+inline bool fits32(int64_t v) { return v <= 0x7fffffff; }
+inline CUtensorMapDataType map_type(int dtype) {
+  return dtype == IGC_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                          : (dtype == IGC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+}
+inline bool rows_aligned(const void* p, int64_t ld, size_t esize, size_t to) {
+  return reinterpret_cast<uintptr_t>(p) % to == 0 && static_cast<uint64_t>(ld) * esize % to == 0;
+}
+
+// An M x N 16-bit operand that TMA reads.
+inline bool operand_ok(const void* p, int64_t ld) { return rows_aligned(p, ld, 2, 16); }
+
+// A matrix of the interface: pointer, row stride, element type.
+struct Mat {
+  const void* ptr = nullptr;
+  int64_t ld = 0;
+  int dtype = IGC_F32;
+};
+
+// dX = sum_s D[s] W[s]: D[s] M x N, W[s] N x K, dX M x K (ffn_gradx.cu)
+int ffn_grad_x(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
+               const Mat* D, const Mat* W, const Mat& dX, cudaStream_t stream);
+// dW[s] = D[s]^T X: X M x K, dW[s] N x K (ffn_gradw.cu)
+int ffn_grad_w(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
+               const Mat* D, const Mat& X, const Mat* dW, cudaStream_t stream);
+
+// Forward passes over the fp32 pre-activations of a contraction of length zero
+// (the biases alone), and the backward passes over stored pre-activations (ffn_dact.cu).
+struct PointwiseArgs {
+  int64_t M = 0, N = 0;
+  int dtype = IGC_BF16, act = IGC_ACT_NONE;
+  const void* bias[2] = {};
+  int bias_dtype = IGC_F32;
+  Mat R, out[3];
+};
+int ffn_bias_only(const PointwiseArgs& a, bool gated, cudaStream_t stream);
+
+// Backward through the activation: D0 = dO act'(Z) (linear), or D0 = dG and D1 = dU
+// (gated, Z = G).  D0 / D1 may be null (not stored); db0 / db1 null: not summed.
+struct DactArgs {
+  int64_t M = 0, N = 0;
+  int dtype = IGC_BF16, act = IGC_ACT_NONE;
+  Mat dO, Z, U;
+  void* D0 = nullptr;
+  void* D1 = nullptr;
+  int64_t ldd = 0;  // row stride of D0 and D1: a multiple of 8; both 16-byte aligned
+  void* db0 = nullptr;
+  void* db1 = nullptr;
+  int db_dtype = IGC_F32;
+  float* partial = nullptr;  // dact_chunks(M, N) x N floats per summed vector
+};
+int64_t dact_chunks(int64_t M, int64_t N);
+int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream);
+
+}  // namespace igc

@@ -1,0 +1,190 @@
+"""Host-side checks of the feed-forward operators that need no GPU: declared and exported
+entry points, refusals of the C entries before any device call, refusals of the binding,
+workspace sizes."""
+
+import ctypes
+
+import pytest
+import torch
+
+import implicit_gemm_conv_tcgen05_gb300 as igc
+
+INVALID, MISALIGNED, WORKSPACE, OK = (igc.IGC_ERR_INVALID_ARG, igc.IGC_ERR_MISALIGNED,
+                                      igc.IGC_ERR_WORKSPACE, igc.IGC_OK)
+P = ctypes.c_void_p(4096)
+ODD = ctypes.c_void_p(4098)
+
+
+def test_header_declares_the_operators_and_the_library_exports_them():
+    names = {"linear_act", "linear_act_backward", "linear_act_backward_workspace_size", "gated_ffn",
+             "gated_ffn_backward", "gated_ffn_backward_workspace_size", "grad_norm_clip",
+             "grad_norm_clip_workspace_size"}
+    assert set(igc.declared_functions(igc.FFN_HEADER)) == names
+    for n in names:
+        assert ctypes.cast(getattr(igc.lib(), n), ctypes.c_void_p).value
+
+
+def linear(M=4, N=8, K=16, dt=1, X=P, ldx=16, W=P, ldw=16, b=None, bt=0, act=0, R=None, ldr=8,
+           Z=None, ldz=8, Y=P, ldy=8, yt=1):
+    return igc.lib().linear_act(M, N, K, dt, X, ldx, W, ldw, b, bt, act, R, ldr, Z, ldz, Y, ldy,
+                                yt, None)
+
+
+def test_linear_act_refusals():
+    for bad in (dict(M=-1), dict(N=-1), dict(K=-1), dict(dt=0), dict(dt=3), dict(yt=2),
+                dict(b=P, bt=2), dict(act=5), dict(act=-1), dict(Y=None), dict(ldy=7),
+                dict(R=P, ldr=7), dict(Z=P, ldz=7), dict(X=None), dict(W=None), dict(ldx=15),
+                dict(ldw=15)):
+        assert linear(**bad) == INVALID, bad
+    for bad in (dict(X=ODD), dict(W=ODD), dict(ldx=17), dict(ldw=20)):
+        assert linear(**bad) == MISALIGNED, bad
+    assert linear(M=1 << 31) == igc.IGC_ERR_UNSUPPORTED
+    assert linear(M=0, X=None, Y=None) == OK and linear(N=0, W=None, Y=None) == OK
+
+
+def linear_bwd(M=4, N=8, K=16, dt=2, dY=P, lddy=8, Z=None, ldz=8, act=0, X=P, ldx=16, W=P, ldw=16,
+               dX=P, lddx=16, dW=P, lddw=16, dwt=2, db=None, dbt=0, ws=None, n=0):
+    return igc.lib().linear_act_backward(M, N, K, dt, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX,
+                                         lddx, dW, lddw, dwt, db, dbt, ws, n, None)
+
+
+def test_linear_act_backward_refusals():
+    for bad in (dict(M=-1), dict(dt=0), dict(act=9), dict(dwt=1), dict(db=P, dbt=1), dict(lddx=15),
+                dict(lddw=15), dict(dY=None), dict(lddy=7), dict(act=2), dict(act=2, Z=P, ldz=7),
+                dict(X=None), dict(W=None), dict(ldx=15), dict(ldw=15)):
+        assert linear_bwd(**bad) == INVALID, bad
+    for bad in (dict(X=ODD), dict(W=ODD), dict(ldx=17), dict(ldw=20)):
+        assert linear_bwd(**bad) == MISALIGNED, bad
+    # nothing asked for, or nothing to compute: no operand is looked at
+    assert linear_bwd(dX=None, dW=None, dY=None, X=None, W=None) == OK
+    assert linear_bwd(M=0, dW=None, dY=None) == OK
+
+
+def gated(M=4, F=8, K=16, dt=1, X=P, ldx=16, Wg=P, Wu=P, ldw=16, bg=None, bu=None, bt=0, act=4,
+          G=None, U=None, ldgu=8, H=P, ldh=8):
+    return igc.lib().gated_ffn(M, F, K, dt, X, ldx, Wg, Wu, ldw, bg, bu, bt, act, G, U, ldgu, H, ldh,
+                               None)
+
+
+def test_gated_ffn_refusals():
+    for bad in (dict(M=-1), dict(F=-1), dict(K=-1), dict(dt=0), dict(bg=P, bt=2), dict(bu=P, bt=2),
+                dict(act=5), dict(H=None), dict(ldh=7), dict(G=P), dict(U=P),
+                dict(G=P, U=P, ldgu=7), dict(X=None), dict(Wg=None), dict(Wu=None), dict(ldx=15),
+                dict(ldw=15)):
+        assert gated(**bad) == INVALID, bad
+    for bad in (dict(X=ODD), dict(Wg=ODD), dict(Wu=ODD), dict(ldx=17), dict(ldw=20)):
+        assert gated(**bad) == MISALIGNED, bad
+    assert gated(M=0, H=None) == OK and gated(F=0, H=None) == OK
+
+
+def gated_bwd(M=4, F=8, K=16, dt=2, dH=P, lddh=8, G=P, U=P, ldgu=8, act=4, X=P, ldx=16, Wg=P, Wu=P,
+              ldw=16, dX=P, lddx=16, dWg=P, dWu=P, lddw=16, dwt=2, dbg=None, dbu=None, dbt=0,
+              ws=None, n=0):
+    return igc.lib().gated_ffn_backward(M, F, K, dt, dH, lddh, G, U, ldgu, act, X, ldx, Wg, Wu, ldw,
+                                        dX, lddx, dWg, dWu, lddw, dwt, dbg, dbu, dbt, ws, n, None)
+
+
+def test_gated_ffn_backward_refusals():
+    for bad in (dict(M=-1), dict(dt=0), dict(act=9), dict(dWg=None), dict(dWu=None), dict(dbg=P),
+                dict(dbu=P), dict(dwt=1), dict(dbg=P, dbu=P, dbt=1), dict(lddx=15), dict(lddw=15),
+                dict(dH=None), dict(lddh=7), dict(G=None), dict(U=None), dict(ldgu=7), dict(X=None),
+                dict(Wg=None), dict(Wu=None), dict(ldx=15), dict(ldw=15)):
+        assert gated_bwd(**bad) == INVALID, bad
+    for bad in (dict(X=ODD), dict(Wg=ODD), dict(Wu=ODD), dict(ldx=17), dict(ldw=20)):
+        assert gated_bwd(**bad) == MISALIGNED, bad
+
+
+def clip(n=2, grads=(4096, 8192), sizes=(5, 7), types=(0, 1), out=None, max_norm=1.0, eps=0.0,
+         norm=P, ws=P, nbytes=1 << 20):
+    g = (ctypes.c_void_p * max(len(grads), 1))(*grads)
+    s = (ctypes.c_int64 * max(len(sizes), 1))(*sizes)
+    t = (ctypes.c_int32 * max(len(types), 1))(*types)
+    o = None if out is None else (ctypes.c_void_p * len(out))(*out)
+    return igc.lib().grad_norm_clip(n, g, s, t, o, max_norm, eps, norm, ws, nbytes, None)
+
+
+def test_grad_norm_clip_refusals():
+    for bad in (dict(n=-1), dict(norm=None), dict(max_norm=-1.0), dict(max_norm=float("nan")),
+                dict(eps=-1.0), dict(eps=float("nan")), dict(sizes=(5, -7)), dict(types=(0, 3)),
+                dict(grads=(4096, None)), dict(out=(None, 4096))):
+        assert clip(**bad) == INVALID, bad
+    assert igc.lib().grad_norm_clip(1, None, None, None, None, 1.0, 0.0, P, P, 1 << 20,
+                                    None) == INVALID
+    for bad in (dict(grads=(4098, 8192)), dict(grads=(4096, 8193)), dict(out=(4097, 8192))):
+        assert clip(**bad) == MISALIGNED, bad
+
+
+def test_workspace_sizes():
+    def up(v):
+        return -(-v // 256) * 256
+
+    # dZ with rows padded to 8 columns, then one row of partial sums per chunk of rows
+    assert igc.linear_act_backward_workspace_size(3, 5, 7) == up(3 * 8 * 2) + up(5 * 4)
+    assert igc.gated_ffn_backward_workspace_size(3, 5, 7) == 2 * up(3 * 8 * 2) + up(2 * 5 * 4)
+    assert igc.linear_act_backward_workspace_size(-1, 5, 7) == 0
+    assert igc.gated_ffn_backward_workspace_size(1, -5, 7) == 0
+    assert igc.grad_norm_clip_workspace_size(-1) == 0
+    one = igc.grad_norm_clip_workspace_size(1)
+    assert one == igc.grad_norm_clip_workspace_size(0) == igc.grad_norm_clip_workspace_size(1024)
+    assert igc.grad_norm_clip_workspace_size(1025) == 2 * one
+
+
+def t(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def test_binding_refusals():
+    X, W = t(4, 16), t(8, 16)
+    with pytest.raises(TypeError, match="X has dtype"):
+        igc.linear_act(X.float(), W)
+    with pytest.raises(TypeError, match="W has dtype"):
+        igc.linear_act(X, W.half())
+    with pytest.raises(ValueError, match="W has shape"):
+        igc.linear_act(X, t(8, 15))
+    with pytest.raises(ValueError, match="act is"):
+        igc.linear_act(X, W, act="tanh")
+    with pytest.raises(ValueError, match="bias must be"):
+        igc.linear_act(X, W, bias=t(9))
+    with pytest.raises(ValueError, match="bias must be"):
+        igc.linear_act(X, W, bias=t(8, dtype=torch.float64))
+    with pytest.raises(ValueError, match="rows apart"):      # a broadcast view has no rows
+        igc.linear_act(X, W, residual=t(1, 8).expand(4, 8))
+    with pytest.raises(ValueError, match="unit inner stride"):
+        igc.linear_act(t(16, 4).t(), W)
+    with pytest.raises(ValueError, match="Y has shape"):
+        igc.linear_act(X, W, Y=t(4, 9))
+    with pytest.raises(ValueError, match="X must be a matrix"):
+        igc.linear_act(t(16), W)
+    with pytest.raises(ValueError, match="CUDA"):
+        igc.linear_act(X, W)
+    dY = t(4, 8)
+    with pytest.raises(ValueError, match="pre-activation"):
+        igc.linear_act_backward(dY, X, W, act="gelu", dX=t(4, 16))
+    with pytest.raises(ValueError, match="dX needs W"):
+        igc.linear_act_backward(dY, X, None, dX=t(4, 16))
+    with pytest.raises(ValueError, match="rows apart"):
+        igc.linear_act_backward(t(1, 8).expand(4, 8), X, W, dX=t(4, 16))
+    with pytest.raises(TypeError, match="dX has dtype"):
+        igc.linear_act_backward(dY, X, W, dX=t(4, 16, dtype=torch.float32))
+    with pytest.raises(ValueError, match="CUDA"):
+        igc.linear_act_backward(dY, X, W, dX=t(4, 16))
+    with pytest.raises(ValueError, match="one row stride"):
+        igc.gated_ffn(X, W, t(8, 24)[:, :16])
+    with pytest.raises(ValueError, match="go together"):
+        igc.gated_ffn(X, W, W, G=t(4, 8))
+    with pytest.raises(ValueError, match="one type"):
+        igc.gated_ffn(X, W, W, bg=t(8), bu=t(8, dtype=torch.float32))
+    with pytest.raises(ValueError, match="CUDA"):
+        igc.gated_ffn(X, W, W)
+    with pytest.raises(ValueError, match="go together"):
+        igc.gated_ffn_backward(dY, dY, dY, X, W, W, dWg=t(8, 16))
+    with pytest.raises(ValueError, match="CUDA"):
+        igc.gated_ffn_backward(dY, dY, dY, X, W, W, dX=t(4, 16))
+    with pytest.raises(TypeError, match="a gradient has dtype"):
+        igc.grad_norm_clip([t(4, dtype=torch.float64)], 1.0)
+    with pytest.raises(ValueError, match="contiguous"):
+        igc.grad_norm_clip([t(4, 8).t()], 1.0)
+    with pytest.raises(ValueError, match="CUDA"):
+        igc.grad_norm_clip([t(4)], 1.0)
+    with pytest.raises(ValueError, match="as many"):
+        igc.grad_norm_clip([t(4)], 1.0, out=[])
