@@ -11,6 +11,7 @@ missing and cannot be built, importing the binding's functions raises.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -138,6 +139,9 @@ def lib() -> ctypes.CDLL:
             L.grad_norm_clip.restype = i32
             L.grad_norm_clip_workspace_size.argtypes = [i64]
             L.grad_norm_clip_workspace_size.restype = sz
+            L.igc_plan_ffn.argtypes = [i32, i64, i64, i64, i32, i32,
+                                       ctypes.POINTER(ctypes.c_int32)]
+            L.igc_plan_ffn.restype = i32
             L.igc_version.argtypes = []
             L.igc_version.restype = ctypes.c_char_p
             _lib = L
@@ -803,6 +807,18 @@ def gated_ffn_backward(dH, G, U, X, Wg, Wu, act="silu", dX=None, dWg=None, dWu=N
     return dX, dWg, dWu, dbg, dbu
 
 
+PLAN_FFN_LINEAR, PLAN_FFN_GATED, PLAN_FFN_GRAD_X, PLAN_FFN_GRAD_W = 0, 1, 2, 3
+_PLAN_FFN_FIELDS = ("small", "rows", "row_blocks", "split", "small_ns", "tiles_ns")
+
+
+def igc_plan_ffn(op: int, M: int, N: int, K: int, count: int = 1, sms: int = 152) -> dict:
+    """The schedule that a feed-forward product runs with (see include/igc_ffn.h)."""
+    out = (ctypes.c_int32 * 6)()
+    _check(lib().igc_plan_ffn(int(op), int(M), int(N), int(K), int(count), int(sms), out),
+           "igc_plan_ffn")
+    return dict(zip(_PLAN_FFN_FIELDS, (int(v) for v in out)))
+
+
 def grad_norm_clip_workspace_size(count: int) -> int:
     return int(lib().grad_norm_clip_workspace_size(int(count)))
 
@@ -814,50 +830,43 @@ def grad_norm_clip(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=Non
     Returns the norm, a one-element fp32 CUDA tensor (`norm`, or allocated); nothing
     waits for the GPU."""
     import torch
+    T = torch.Tensor
     grads = list(grads)
-    if out is None:
-        outs = grads
-    elif out is False:
-        outs = None
+    n = len(grads)
+    if out is None or out is False:
+        every = grads
     else:
-        outs = list(out)
-        if len(outs) != len(grads):
+        every = grads + list(out)
+        if len(every) != 2 * n:
             raise ValueError("out must have as many tensors as grads")
-    codes, sizes, ptrs = [], [], []
-    for g in grads:
-        code = _dtype_code(g.dtype)
-        if code is None:
-            raise TypeError(f"a gradient has dtype {g.dtype}")
-        if not g.is_contiguous():
-            raise ValueError("gradients must be contiguous")
-        if not g.is_cuda:
-            raise ValueError("gradients must be CUDA tensors")
-        codes.append(code)
-        sizes.append(g.numel())
-        ptrs.append(g.data_ptr())
-    out_ptrs = ptrs
-    if outs is not None and outs is not grads:
-        out_ptrs = []
-        for o, g in zip(outs, grads):
-            if o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous() or \
-                    not o.is_cuda:
-                raise ValueError("out must match grads in type and size, contiguous, on CUDA")
-            out_ptrs.append(o.data_ptr())
+    dtypes = [g.dtype for g in every]
+    codes = [_dtype_code(t) for t in dtypes[:n]]
+    if None in codes:
+        raise TypeError(f"a gradient has dtype {dtypes[codes.index(None)]}")
+    sizes = list(map(T.numel, every))
+    if not all(map(T.is_contiguous, every)):
+        raise ValueError("gradients and out must be contiguous")
+    devices = set(map(T.get_device, every))
+    if -1 in devices:
+        raise ValueError("gradients and out must be CUDA tensors")
+    if len(devices) > 1:
+        raise ValueError("gradients and out must be on one device")
+    if len(every) > n and (dtypes[:n] != dtypes[n:] or sizes[:n] != sizes[n:]):
+        raise ValueError("out must match grads in type and size")
+    ptrs = array.array("Q", map(T.data_ptr, every))
+    g_ptr = ptrs.buffer_info()[0]
+    o_ptr = None if out is False else (g_ptr if out is None else g_ptr + 8 * n)
+    sizes, codes = array.array("q", sizes[:n]), array.array("i", codes)
     if norm is not None and (norm.dtype != torch.float32 or norm.numel() != 1 or
                              not norm.is_cuda):
         raise ValueError("norm must be a one-element fp32 CUDA tensor")
-    n = len(grads)
     device = grads[0].device if n else (norm.device if norm is not None else "cuda")
-    if any(g.device != device for g in grads[1:]):
-        raise ValueError("gradients must be on one device")
     if norm is None:
         norm = _new((), torch.float32, device, stream)
     _one_device(("grads", grads[0] if n else None), ("norm", norm), ("workspace", workspace))
     ws = _workspace(workspace, grad_norm_clip_workspace_size(n), device, stream)
-    vps, i64s, i32s = ctypes.c_void_p * n, ctypes.c_int64 * n, ctypes.c_int32 * n
-    rc = lib().grad_norm_clip(n, vps(*ptrs), i64s(*sizes), i32s(*codes),
-                              None if outs is None else vps(*out_ptrs), float(max_norm),
-                              float(eps), norm.data_ptr(), ws.data_ptr(), ws.numel(),
-                              _stream(stream))
+    rc = lib().grad_norm_clip(n, g_ptr, sizes.buffer_info()[0], codes.buffer_info()[0], o_ptr,
+                              float(max_norm), float(eps), norm.data_ptr(), ws.data_ptr(),
+                              ws.numel(), _stream(stream))
     _check(rc, "grad_norm_clip")
     return norm

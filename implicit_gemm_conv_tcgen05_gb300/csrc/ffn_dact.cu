@@ -78,58 +78,121 @@ __device__ __forceinline__ void block_sums(float (&red)[kRowLanes][kCols], const
   }
 }
 
-template <bool kGated>
-__global__ void __launch_bounds__(kRowLanes * 32) dact_kernel(const DactParams p) {
-  __shared__ float red[kRowLanes][kCols];
+// One row's 8 columns: o, z (and u) come in as dO, Z (U) and leave as D0 (z when gated,
+// else o) and D1 (u).
+template <bool kGated, int kAct>
+__device__ __forceinline__ void dact8(float (&o)[8], float (&z)[8], float (&u)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f, d;
+    act_grad_f32<kAct>(z[i], f, d);
+    if constexpr (kGated) {
+      z[i] = o[i] * u[i] * d;  // dG
+      u[i] = o[i] * f;         // dU
+    } else {
+      o[i] *= d;               // dZ
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack8(uint4 q, bool bf16, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack16(w[i], bf16);
+    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+  }
+}
+
+// Bound by memory where it reads 16-byte vectors: kUnroll rows' loads are issued before
+// the first is used, so that an SM keeps some 70 KB in flight.
+template <bool kGated, int kAct, bool kSum>
+__device__ __forceinline__ void dact_rows(const DactParams& p, int n, long long r0, long long r1,
+                                          float (&s0)[8], float (&s1)[8]) {
+  constexpr int kUnroll = 2;
+  constexpr bool kNeedZ = kGated || kAct != IGC_ACT_NONE;
+  const int warp = threadIdx.x / 32;
+  const bool bf16 = p.bf16 != 0;
+  auto finish = [&](long long r, float(&o)[8], float(&z)[8], float(&u)[8]) {
+    if constexpr (kNeedZ) dact8<kGated, kAct>(o, z, u);
+    float(&d0)[8] = kGated ? z : o;
+    if constexpr (kSum) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s0[i] += d0[i];
+        if constexpr (kGated) s1[i] += u[i];
+      }
+    }
+    if (p.D0 != nullptr) {
+      save8(p.D0 + r * p.ldd, n, bf16, d0);
+      if constexpr (kGated) save8(p.D1 + r * p.ldd, n, bf16, u);
+    }
+  };
+  const bool fast = n + 8 <= p.N && p.o_vec && (!kNeedZ || p.z_vec) && (!kGated || p.u_vec);
+  if (fast) {
+    for (long long r = r0 + warp; r < r1; r += kUnroll * kRowLanes) {
+      uint4 qo[kUnroll], qz[kUnroll], qu[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const long long rj = r + j * kRowLanes;
+        if (rj >= r1) continue;
+        qo[j] = *reinterpret_cast<const uint4*>(p.dO + rj * p.ldo + n);
+        if constexpr (kNeedZ) qz[j] = *reinterpret_cast<const uint4*>(p.Z + rj * p.ldz + n);
+        if constexpr (kGated) qu[j] = *reinterpret_cast<const uint4*>(p.U + rj * p.ldu + n);
+      }
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const long long rj = r + j * kRowLanes;
+        if (rj >= r1) continue;
+        float o[8], z[8], u[8];
+        unpack8(qo[j], bf16, o);
+        if constexpr (kNeedZ) unpack8(qz[j], bf16, z);
+        if constexpr (kGated) unpack8(qu[j], bf16, u);
+        finish(rj, o, z, u);
+      }
+    }
+  } else {
+    for (long long r = r0 + warp; r < r1; r += kRowLanes) {
+      float o[8], z[8], u[8];
+      load8(p.dO + r * p.ldo, n, p.N, p.o_vec, bf16, o);
+      if constexpr (kNeedZ) load8(p.Z + r * p.ldz, n, p.N, p.z_vec, bf16, z);
+      if constexpr (kGated) load8(p.U + r * p.ldu, n, p.N, p.u_vec, bf16, u);
+      finish(r, o, z, u);
+    }
+  }
+}
+
+template <bool kGated, int kAct, bool kSum>
+__global__ void __launch_bounds__(kRowLanes * 32, 3) dact_kernel(const DactParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int n = blockIdx.x * kCols + lane * 8;
+  const int n = blockIdx.x * kCols + (threadIdx.x % 32) * 8;
   const long long r0 = static_cast<long long>(blockIdx.y) * p.rows_per_chunk;
   const long long r1 = min(static_cast<long long>(p.M), r0 + p.rows_per_chunk);
-  const bool bf16 = p.bf16 != 0;
   float s0[8] = {}, s1[8] = {};
-  if (n < p.N) {
-    with_act(p.act, [&](auto a) {
-      constexpr int kAct = decltype(a)::value;
-#pragma unroll 2
-      for (long long r = r0 + warp; r < r1; r += kRowLanes) {
-        float o[8], z[8];
-        load8(p.dO + r * p.ldo, n, p.N, p.o_vec, bf16, o);
-        if (kGated || kAct != IGC_ACT_NONE) load8(p.Z + r * p.ldz, n, p.N, p.z_vec, bf16, z);
-        if constexpr (kGated) {
-          float u[8];
-          load8(p.U + r * p.ldu, n, p.N, p.u_vec, bf16, u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float f, d;
-            act_grad_f32<kAct>(z[i], f, d);
-            z[i] = o[i] * u[i] * d;  // dG
-            u[i] = o[i] * f;         // dU
-            s0[i] += z[i];
-            s1[i] += u[i];
-          }
-          if (p.D0 != nullptr) {
-            save8(p.D0 + r * p.ldd, n, bf16, z);
-            save8(p.D1 + r * p.ldd, n, bf16, u);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if constexpr (kAct != IGC_ACT_NONE) {
-              float f, d;
-              act_grad_f32<kAct>(z[i], f, d);
-              o[i] *= d;
-            }
-            s0[i] += o[i];
-          }
-          if (p.D0 != nullptr) save8(p.D0 + r * p.ldd, n, bf16, o);
-        }
-      }
-    });
+  if (n < p.N) dact_rows<kGated, kAct, kSum>(p, n, r0, r1, s0, s1);
+  if constexpr (kSum) {
+    __shared__ float red[kRowLanes][kCols];
+    block_sums(red, s0, p.partial0, p.N);
+    if constexpr (kGated) block_sums(red, s1, p.partial1, p.N);
   }
-  if (p.partial0 != nullptr) block_sums(red, s0, p.partial0, p.N);
-  if (kGated && p.partial1 != nullptr) block_sums(red, s1, p.partial1, p.N);
+}
+
+template <bool kGated, bool kSum>
+int launch_dact(const DactParams& p, dim3 grid, cudaStream_t stream) {
+  const dim3 block(kRowLanes * 32);
+  switch (p.act) {
+    case IGC_ACT_RELU:
+      return launch_pdl(dact_kernel<kGated, IGC_ACT_RELU, kSum>, grid, block, 0, stream, p);
+    case IGC_ACT_GELU:
+      return launch_pdl(dact_kernel<kGated, IGC_ACT_GELU, kSum>, grid, block, 0, stream, p);
+    case IGC_ACT_GELU_TANH:
+      return launch_pdl(dact_kernel<kGated, IGC_ACT_GELU_TANH, kSum>, grid, block, 0, stream, p);
+    case IGC_ACT_SILU:
+      return launch_pdl(dact_kernel<kGated, IGC_ACT_SILU, kSum>, grid, block, 0, stream, p);
+    default:
+      return launch_pdl(dact_kernel<kGated, IGC_ACT_NONE, kSum>, grid, block, 0, stream, p);
+  }
 }
 
 // out[n] = sum over chunks of partial[chunk][n]; blockIdx.y: which vector.
@@ -204,10 +267,11 @@ __global__ void __launch_bounds__(256) bias_only_kernel(const BiasOnlyParams p) 
 
 }  // namespace
 
-// Chunks of rows: enough blocks to fill the GPU several times over, at least 32 rows each.
+// Chunks of rows: enough blocks to fill the GPU several times over, at least a row for
+// each of a block's warps.
 int64_t dact_chunks(int64_t M, int64_t N) {
   const int64_t col_blocks = (N + kCols - 1) / kCols;
-  const int64_t most = (M + 31) / 32;
+  const int64_t most = (M + kRowLanes - 1) / kRowLanes;
   int64_t want = col_blocks > 0 ? (2432 + col_blocks - 1) / col_blocks : 1;
   if (want > kMaxChunks) want = kMaxChunks;
   if (want > most) want = most;
@@ -233,8 +297,11 @@ int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream) {
     p.partial1 = gated ? a.partial + chunks * a.N : nullptr;
   }
   const dim3 grid(static_cast<unsigned>((a.N + kCols - 1) / kCols), static_cast<unsigned>(chunks));
-  int rc = gated ? launch_pdl(dact_kernel<true>, grid, dim3(kRowLanes * 32), 0, stream, p)
-                 : launch_pdl(dact_kernel<false>, grid, dim3(kRowLanes * 32), 0, stream, p);
+  const bool sum = a.db0 != nullptr;
+  const int rc = gated ? (sum ? launch_dact<true, true>(p, grid, stream)
+                              : launch_dact<true, false>(p, grid, stream))
+                       : (sum ? launch_dact<false, true>(p, grid, stream)
+                              : launch_dact<false, false>(p, grid, stream));
   if (rc != IGC_OK || a.db0 == nullptr) return rc;
   return launch_pdl(sum_chunks_kernel,
                     dim3(static_cast<unsigned>((a.N + 31) / 32), gated ? 2 : 1), dim3(256), 0,

@@ -6,11 +6,12 @@ namespace igc {
 
 int ffn_grad_x(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
                const Mat* D, const Mat* W, const Mat& dX, cudaStream_t stream) {
-  FfnParams p = {};
-  p.M = static_cast<int>(M), p.N = static_cast<int>(K);
-  p.kb_seg = static_cast<int>((N + kFfnKS - 1) / kFfnKS);
-  p.segs = count, p.srcs = 1;
-  return ffn_launch<FfnOp::GradX>(dev, dtype, count, D, M, N, count, W, N, K, &dX, 1, p, stream);
+  FfnProblem q;
+  q.M = M, q.N = K, q.K = N, q.dtype = dtype;
+  q.segs = q.count_a = q.count_b = count;
+  for (int i = 0; i < count; ++i) q.A[i] = D[i], q.B[i] = W[i];
+  q.out[0] = dX;
+  return ffn_launch<FfnOp::GradX>(dev, q, stream);
 }
 
 }  // namespace igc

@@ -1,18 +1,15 @@
 // Launches of the feed-forward GEMM kernels: tile width, schedule, tensor maps.
 #pragma once
 
+#include <algorithm>
 #include <mutex>
 
 #include "ffn_host.h"
-#include "ffn_skinny.cuh"
+#include "ffn_small.cuh"
 #include "ffn_tc.cuh"
 #include "launch.cuh"
 
 namespace igc {
-
-// Largest number of rows of X that the swapped (decode) kernel takes; above it the
-// 256-row tiles are used.
-constexpr int kSkinnyMaxM = 128;
 
 struct FfnOperands {
   CUtensorMap a[2], b[2];
@@ -130,24 +127,52 @@ inline void ffn_set_out(FfnParams& p, CUtensorMap* maps, int i, const Mat& m) {
 }
 
 // Tensor map of a rows x cols operand: K-major boxes are 64 k x box_rows rows;
-// MN-major boxes are 64 outputs x one stage of k.
+// MN-major boxes are 64 outputs x box_rows k.
 inline int ffn_operand_map(CUtensorMap* map, int dtype, const Mat& m, int64_t rows, int64_t cols,
-                           bool mn_major, int box_rows) {
+                           int box_rows) {
   return encode_tiled_2d_fresh(map, map_type(dtype), m.ptr, static_cast<uint64_t>(cols),
                                static_cast<uint64_t>(rows), static_cast<uint64_t>(m.ld) * 2, BK,
-                               static_cast<uint32_t>(mn_major ? kFfnKS : box_rows));
+                               static_cast<uint32_t>(box_rows));
 }
 
-// Chooses the tile width, encodes the operand maps and launches.  A[i] is a_rows x
-// a_cols, B[i] b_rows x b_cols; p holds M, N, kb_seg, segs, srcs and the epilogue.
+// A product of the feed-forward operators: out[m, n] = sum over segments and k of
+// A[m, k] B[n, k] (A the output's rows, B its columns; either may be stored with the
+// output index contiguous, see ffn_tc.cuh), and what the epilogue takes.
+struct FfnProblem {
+  int64_t M = 0, N = 0, K = 0;  // one output matrix, one contraction segment
+  int dtype = IGC_BF16;
+  int segs = 1, srcs = 1;
+  Mat A[2], B[2];               // count_a / count_b of them
+  int count_a = 1, count_b = 1;
+  Mat out[3];
+  int act = IGC_ACT_NONE;
+  const void* bias[2] = {};
+  int bias_dtype = IGC_F32;
+  Mat R;
+};
+
+// Stored extents of operand i: MN-major operands have k as their rows.
+inline int ffn_map_a(CUtensorMap* map, const FfnProblem& q, int i, bool mn, int box_rows) {
+  return mn ? ffn_operand_map(map, q.dtype, q.A[i], q.K, q.M, box_rows)
+            : ffn_operand_map(map, q.dtype, q.A[i], q.M, q.K, box_rows);
+}
+inline int ffn_map_b(CUtensorMap* map, const FfnProblem& q, int i, bool mn, int box_rows) {
+  return mn ? ffn_operand_map(map, q.dtype, q.B[i], q.K, q.N, box_rows)
+            : ffn_operand_map(map, q.dtype, q.B[i], q.N, q.K, box_rows);
+}
+
+// 256-row tiles: chooses the tile width, encodes the maps and launches.
 template <FfnOp kOp>
-int ffn_launch(const DeviceInfo& dev, int dtype, int count_a, const Mat* A, int64_t a_rows,
-               int64_t a_cols, int count_b, const Mat* B, int64_t b_rows, int64_t b_cols,
-               const Mat* outs, int n_outs, FfnParams p, cudaStream_t stream) {
-  int clusters = 0;
-  int rc = ffn_kernel_setup<kOp, 256>(dev, &clusters);
-  if (rc != IGC_OK) return rc;
-  p.bf16 = dtype == IGC_BF16;
+int ffn_launch_tiles(const DeviceInfo& dev, const FfnProblem& q, int clusters,
+                     cudaStream_t stream) {
+  FfnParams p = {};
+  p.M = static_cast<int>(q.M), p.N = static_cast<int>(q.N);
+  p.kb_seg = static_cast<int>((q.K + kFfnKS - 1) / kFfnKS);
+  p.segs = q.segs, p.srcs = q.srcs;
+  p.bf16 = q.dtype == IGC_BF16;
+  p.act = q.act;
+  p.bias0 = q.bias[0], p.bias1 = q.bias[1], p.bias_f32 = q.bias_dtype == IGC_F32;
+  p.R = q.R.ptr, p.ldr = q.R.ld, p.r_vec = rows_aligned(q.R.ptr, q.R.ld, 2, 16);
   const long long tm = (static_cast<long long>(p.M) + BM - 1) / BM * p.srcs;
   const int wide = FfnCfg<kOp, 256>::kOutN, narrow = FfnCfg<kOp, 128>::kOutN;
   int bn = ffn_cost(tm, p.N, wide, true, kBnEff[0], clusters) <=
@@ -156,78 +181,183 @@ int ffn_launch(const DeviceInfo& dev, int dtype, int count_a, const Mat* A, int6
                : 128;
   bn = tile_width_override() == 128 || tile_width_override() == 256 ? tile_width_override() : bn;
   FfnOperands ops = {};
-  for (int i = 0; i < count_a; ++i) {
-    rc = ffn_operand_map(&ops.a[i], dtype, A[i], a_rows, a_cols, ffn_a_mn(kOp), BM_CTA);
-    if (rc != IGC_OK) return rc;
-  }
-  for (int i = 0; i < count_b; ++i) {
-    rc = ffn_operand_map(&ops.b[i], dtype, B[i], b_rows, b_cols, ffn_b_mn(kOp), bn / 4);
-    if (rc != IGC_OK) return rc;
-  }
+  int rc = IGC_OK;
+  for (int i = 0; i < q.count_a && rc == IGC_OK; ++i)
+    rc = ffn_map_a(&ops.a[i], q, i, ffn_a_mn(kOp), ffn_a_mn(kOp) ? kFfnKS : BM_CTA);
+  for (int i = 0; i < q.count_b && rc == IGC_OK; ++i)
+    rc = ffn_map_b(&ops.b[i], q, i, ffn_b_mn(kOp), ffn_b_mn(kOp) ? kFfnKS : bn / 4);
+  if (rc != IGC_OK) return rc;
   CUtensorMap out_maps[3] = {};
-  for (int i = 0; i < n_outs; ++i) ffn_set_out(p, out_maps, i, outs[i]);
+  for (int i = 0; i < 3; ++i) ffn_set_out(p, out_maps, i, q.out[i]);
   return bn == 256 ? ffn_launch_bn<kOp, 256>(dev, ops, out_maps, p, stream)
                    : ffn_launch_bn<kOp, 128>(dev, ops, out_maps, p, stream);
 }
 
 // ---------------------------------------------------------------------------
-// few rows of X: the swapped kernel
+// small outputs: 128-column blocks shared by clusters that split k
 // ---------------------------------------------------------------------------
-constexpr size_t kSkinnySmem = 110 * 1024;  // two CTAs on an SM
+constexpr size_t kSmallSmemTwo = 110 * 1024;  // two CTAs on an SM
+constexpr size_t kSmallSmemOne = 224 * 1024;
 
-template <bool kGated>
-int ffn_launch_skinny(const DeviceInfo& dev, int dtype, int64_t K, const Mat& X, const Mat* W,
-                      SkinnyParams p, const Mat* outs, int n_outs, cudaStream_t stream) {
+// Estimated times in microseconds, for choosing between schedules (measured on GB300: a
+// CTA takes in about 65 bytes a nanosecond through TMA, two on an SM 95 together, one with
+// twice the stages 85; an SM reads about 40 from the shared memory of the other CTAs of
+// its cluster; DRAM gives 6600 once enough CTAs stream; a launch and a CTA's set-up, first
+// loads and last stores take about 3.5 us).
+constexpr double kUsFixed = 3.5, kCtaRate = 65e3, kTwoCtaRate = 95e3, kDeepCtaRate = 85e3,
+                 kDsmemPerSm = 40e3, kDramRate = 6.6e6, kDramPerCta = 48e3;
+
+// Bytes of the operands, each read once.
+template <FfnOp kOp>
+double operand_bytes(const FfnProblem& q) {
+  return 2.0 * q.segs * static_cast<double>(q.K) *
+         (static_cast<double>(q.N) * (kOp == FfnOp::Gated ? 2 : 1) +
+          static_cast<double>(q.M) * q.srcs);
+}
+
+struct SmallPlan {
+  int m_blocks = 1, mt = 16, split = 1;
+  double us = 1e30;
+};
+
+inline size_t small_stage_bytes(int mt) { return kSkWBytes + static_cast<size_t>(mt) * BK * 2; }
+inline size_t small_part_bytes(int mt) { return static_cast<size_t>(mt) * kSkRows * 4; }
+// Whether two CTAs with blocks of mt output rows fit on an SM with at least three stages each.
+inline bool small_two_fit(int mt) {
+  return small_part_bytes(mt) <= kSmallSmemTwo - 1024 &&
+         3 * small_stage_bytes(mt) <= kSmallSmemTwo - 1024;
+}
+
+// The number of output rows of a block and of CTAs that share one: the cheapest of the
+// combinations.  Fewer rows and more CTAs mean more SMs at work on shorter parts, but W
+// is read once per block of rows and each CTA's partial sums cross the cluster.
+template <FfnOp kOp>
+SmallPlan small_plan(const FfnProblem& q, int sms) {
+  constexpr int kOutT = kOp == FfnOp::Gated ? kSkRows / 2 : kSkRows;
+  constexpr int kRowStep = ffn_a_mn(kOp) ? 64 : 16;
+  const int atoms = static_cast<int>((q.K + BK - 1) / BK) * q.segs;
+  const double unique = operand_bytes<kOp>(q);
+  SmallPlan best;
+  int last_mt = 0;
+  for (int rows = kSkMaxMt; rows >= 32; rows -= 32) {
+    const int64_t mb = (q.M + rows - 1) / rows;
+    const int mt = static_cast<int>(((q.M + mb - 1) / mb + kRowStep - 1) / kRowStep * kRowStep);
+    if (mt == last_mt || mt > kSkMaxMt || mb > 1 << 20) continue;
+    last_mt = mt;
+    const double blocks = static_cast<double>((q.N + kOutT - 1) / kOutT) *
+                          static_cast<double>(mb) * q.srcs;
+    for (int split = 1; split <= kSkMaxSplit && (split == 1 || atoms >= 2 * split); split *= 2) {
+      const bool two = small_two_fit(mt);
+      // clusters of 4 and 8 do not pack the SMs fully
+      const double packed = split == 8 ? (two ? 0.85 : 0.8) : (split == 4 ? 0.9 : 1.0);
+      const double slots = (two ? 2.0 : 1.0) * sms * packed;
+      const double ctas = blocks * split;
+      const double waves = ctas <= slots ? 1.0 : static_cast<double>(static_cast<long long>(
+                                                     (ctas + slots - 1) / slots));
+      const bool pairs = two && ctas > 0.9 * sms;  // two CTAs on an SM
+      const double rate = pairs ? kTwoCtaRate / 2 : (two ? kCtaRate : kDeepCtaRate);
+      const double load =
+          static_cast<double>((atoms + split - 1) / split) * BK * 2.0 * (kSkRows + mt) / rate;
+      const double join =
+          static_cast<double>(small_part_bytes(mt)) /
+              (split > 1 ? (pairs ? kDsmemPerSm / 2 : kDsmemPerSm) : rate) +
+          (split > 1 ? 0.3 : 0.0);
+      const double dram =
+          unique / std::min(kDramRate, std::min(ctas, slots) * kDramPerCta);
+      const double busy = std::max(waves * load, dram);
+      const double us = kUsFixed + busy + waves * join;
+      if (us < best.us) {
+        best.m_blocks = static_cast<int>(mb);
+        best.mt = mt;
+        best.split = split;
+        best.us = us;
+      }
+    }
+  }
+  return best;
+}
+
+// The same estimate for the 256-row tiles: rounds of the schedule, each 128-deep stage as
+// long as its MMAs or its operands' way into an SM: about 165 bytes a nanosecond (the
+// large boxes of this kernel), half of that where rows do not start on 128-byte lines.
+template <FfnOp kOp>
+double tiles_us(const FfnProblem& q, int clusters) {
+  const int out_n = FfnCfg<kOp, 256>::kOutN;
+  const long long tiles = (q.M + BM - 1) / BM * q.srcs * ((q.N + out_n - 1) / out_n);
+  const long long full = tiles / clusters, rem = tiles % clusters;
+  bool lines = true;
+  for (int i = 0; i < q.count_a; ++i) lines = lines && rows_aligned(q.A[i].ptr, q.A[i].ld, 2, 128);
+  for (int i = 0; i < q.count_b; ++i) lines = lines && rows_aligned(q.B[i].ptr, q.B[i].ld, 2, 128);
+  const double rate = lines ? 165e3 : 82e3;
+  const double whole = std::max(0.53, 65536 / rate), half = std::max(0.27, 49152 / rate);
+  const double stages = static_cast<double>((q.K + kFfnKS - 1) / kFfnKS) * q.segs;
+  const bool halves = rem > 0 && 2 * rem <= clusters;
+  const double busy = stages * (static_cast<double>(full) * whole +
+                                (rem == 0 ? 0.0 : (halves ? half : whole)));
+  // streaming from DRAM takes CTAs: about 35 bytes a nanosecond each
+  const double pairs = full > 0 ? clusters : static_cast<double>(halves ? 2 * rem : rem);
+  const double dram = operand_bytes<kOp>(q) / std::min(kDramRate, 2.0 * pairs * 35e3);
+  return kUsFixed + 1.0 + std::max(busy, dram);
+}
+
+template <FfnOp kOp>
+int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const SmallPlan& plan,
+                     cudaStream_t stream) {
   static std::once_flag once[64];
   static int rcs[64];
-  auto kern = igc_ffn_skinny_kernel<kGated>;
+  auto kern = igc_ffn_small_kernel<kOp>;
   std::call_once(once[dev.device], [&] {
     rcs[dev.device] =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSkinnySmem)) == cudaSuccess
-            ? IGC_OK
-            : IGC_ERR_CUDA;
+        dev.smem_optin < kSmallSmemOne + 1024
+            ? IGC_ERR_UNSUPPORTED
+            : (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kSmallSmemOne)) == cudaSuccess
+                   ? IGC_OK
+                   : IGC_ERR_CUDA);
   });
   if (rcs[dev.device] != IGC_OK) return rcs[dev.device];
 
-  const int out_t = kGated ? kSkRows / 2 : kSkRows;
-  const long long blocks = (static_cast<long long>(p.N) + out_t - 1) / out_t;
-  p.mt = (p.M + 15) / 16 * 16;
+  constexpr int kOutT = kOp == FfnOp::Gated ? kSkRows / 2 : kSkRows;
+  SmallParams p = {};
+  p.M = static_cast<int>(q.M), p.N = static_cast<int>(q.N);
+  p.m_blocks = plan.m_blocks;
+  p.mt = plan.mt;
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>(p.mt)) p.tmem_cols *= 2;
-  p.atoms = static_cast<int>((K + BK - 1) / BK);
-  // CTAs per block: as many as keep the grid within two CTAs per SM and leave each
-  // at least four 64-k steps
-  p.split = 1;
-  while (p.split < kSkMaxSplit && 2 * p.split * blocks <= 2LL * dev.sm_count &&
-         p.atoms >= 8 * p.split)
-    p.split *= 2;
+  p.atoms_seg = static_cast<int>((q.K + BK - 1) / BK);
+  p.atoms = p.atoms_seg * q.segs;
+  const long long blocks = (q.N + kOutT - 1) / kOutT * p.m_blocks * q.srcs;
+  p.split = plan.split;
   p.per_cta = (p.atoms + p.split - 1) / p.split;
   if (blocks * p.split > 0x7fffffffLL) return IGC_ERR_UNSUPPORTED;
-  const size_t stage = kSkWBytes + static_cast<size_t>(p.mt) * BK * 2;
-  const size_t part = static_cast<size_t>(p.mt) * kSkRows * 4;
-  size_t stages = (kSkinnySmem - 1024) / stage;
+  const size_t stage = small_stage_bytes(p.mt), part = small_part_bytes(p.mt);
+  const size_t budget = (small_two_fit(p.mt) ? kSmallSmemTwo : kSmallSmemOne) - 1024;
+  size_t stages = budget / stage;
   if (stages > kSkMaxStages) stages = kSkMaxStages;
   if (stages > static_cast<size_t>(p.per_cta)) stages = static_cast<size_t>(p.per_cta);
   p.stages = static_cast<int>(stages);
   const size_t ring = stages * stage;
-  p.bf16 = dtype == IGC_BF16;
+  p.bf16 = q.dtype == IGC_BF16;
+  p.act = q.act;
+  p.bias0 = q.bias[0], p.bias1 = q.bias[1], p.bias_f32 = q.bias_dtype == IGC_F32;
+  p.R = q.R.ptr, p.ldr = q.R.ld, p.r_vec = rows_aligned(q.R.ptr, q.R.ld, 2, 8);
   p.wait_limit_ns = wait_limit_ns();
   p.status = status_word();
-  for (int i = 0; i < n_outs; ++i) {
-    p.out[i] = const_cast<void*>(outs[i].ptr);
-    p.ld[i] = outs[i].ld;
-    p.f32[i] = outs[i].dtype == IGC_F32;
-    p.vec[i] = rows_aligned(outs[i].ptr, outs[i].ld, elem_size(outs[i].dtype),
-                            4 * elem_size(outs[i].dtype));
+  for (int i = 0; i < 3; ++i) {
+    const size_t es = elem_size(q.out[i].dtype);
+    p.out[i] = const_cast<void*>(q.out[i].ptr);
+    p.ld[i] = q.out[i].ld;
+    p.f32[i] = q.out[i].dtype == IGC_F32;
+    p.vec[i] = rows_aligned(q.out[i].ptr, q.out[i].ld, es, 4 * es);
   }
-  CUtensorMap mx, mw[2];
-  int rc = ffn_operand_map(&mx, dtype, X, p.M, K, false, p.mt);
+  // the kernel's A operand is the problem's B (the output's columns) and the other way round
+  CUtensorMap ma[2] = {}, mb[2] = {};
+  int rc = IGC_OK;
+  for (int i = 0; i < q.count_b && rc == IGC_OK; ++i)
+    rc = ffn_map_b(&ma[i], q, i, ffn_b_mn(kOp), ffn_b_mn(kOp) ? BK : kOutT);
+  for (int i = 0; i < q.count_a && rc == IGC_OK; ++i)
+    rc = ffn_map_a(&mb[i], q, i, ffn_a_mn(kOp), ffn_a_mn(kOp) ? BK : p.mt);
   if (rc != IGC_OK) return rc;
-  for (int i = 0; i < 2; ++i) {
-    rc = ffn_operand_map(&mw[i], dtype, W[kGated ? i : 0], p.N, K, false, out_t);
-    if (rc != IGC_OK) return rc;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks * p.split), 1, 1);
   cfg.blockDim = dim3(kSkThreads, 1, 1);
@@ -242,11 +372,41 @@ int ffn_launch_skinny(const DeviceInfo& dev, int dtype, int64_t K, const Mat& X,
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kern, mx, mw[0], mw[1], p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, ma[0], ma[1], mb[0], mb[1], p) != cudaSuccess) {
     (void)cudaGetLastError();
     return IGC_ERR_CUDA;
   }
   return IGC_OK;
+}
+
+// Which of the two kernels runs a problem: the one with the shorter estimate, unless the
+// calling thread forced a tile width (igc_set_tile_width).
+template <FfnOp kOp>
+bool ffn_takes_small(const FfnProblem& q, const SmallPlan& plan, int clusters) {
+  return plan.us < tiles_us<kOp>(q, clusters) && tile_width_override() == 0;
+}
+
+template <FfnOp kOp>
+int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, cudaStream_t stream) {
+  int clusters = 0;
+  const int rc = ffn_kernel_setup<kOp, 256>(dev, &clusters);
+  if (rc != IGC_OK) return rc;
+  const SmallPlan plan = small_plan<kOp>(q, dev.sm_count);
+  return ffn_takes_small<kOp>(q, plan, clusters) ? ffn_launch_small<kOp>(dev, q, plan, stream)
+                                                 : ffn_launch_tiles<kOp>(dev, q, clusters, stream);
+}
+
+// igc_plan_ffn for one product (see igc_ffn.h).
+template <FfnOp kOp>
+void ffn_plan(const FfnProblem& q, int sms, int32_t* out) {
+  const SmallPlan plan = small_plan<kOp>(q, sms);
+  const bool small = ffn_takes_small<kOp>(q, plan, sms / 2);
+  out[0] = small;
+  out[1] = small ? plan.mt : BM;
+  out[2] = small ? plan.m_blocks : static_cast<int32_t>((q.M + BM - 1) / BM);
+  out[3] = small ? plan.split : 1;
+  out[4] = static_cast<int32_t>(plan.us * 1000);
+  out[5] = static_cast<int32_t>(tiles_us<kOp>(q, sms / 2) * 1000);
 }
 
 }  // namespace igc

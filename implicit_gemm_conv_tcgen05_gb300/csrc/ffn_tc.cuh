@@ -241,37 +241,65 @@ __device__ __forceinline__ void ffn_store_box32(const FfnOut& o, const CUtensorM
   }
 }
 
-// v += bias of columns n0 .. n0+31 (a column per lane, broadcast by shuffles).
-__device__ __forceinline__ void ffn_add_bias(const FfnParams& p, const void* bias, int n0, int lane,
-                                             float (&v)[32]) {
-  if (bias == nullptr) return;
-  const int n = n0 + lane;
-  const float b = n < p.N ? load_vec(bias, n, p.bias_f32, p.bf16) : 0.0f;
+// What a box's epilogue reads besides the accumulator, fetched before the accumulator is
+// waited for: the biases of columns n0 + lane and n0 + 32 + lane (broadcast by shuffles
+// later) and, where 16-byte loads can take it whole, this lane's row of the residual.
+struct FfnFetched {
+  float bias0[2], bias1[2];
+  uint4 res[8];
+  bool res_ok;
+};
+
+template <FfnOp kOp>
+__device__ __forceinline__ void ffn_fetch(const FfnParams& p, int m, int n0, int lane,
+                                          FfnFetched& f) {
+  if constexpr (kOp == FfnOp::Linear || kOp == FfnOp::Gated) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int n = n0 + 32 * c + lane;
+      f.bias0[c] = n < p.N ? load_vec(p.bias0, n, p.bias_f32, p.bf16) : 0.0f;
+      if constexpr (kOp == FfnOp::Gated)
+        f.bias1[c] = n < p.N ? load_vec(p.bias1, n, p.bias_f32, p.bf16) : 0.0f;
+    }
+  }
+  if constexpr (kOp == FfnOp::Linear) {
+    f.res_ok = p.R != nullptr && p.r_vec && m < p.M && n0 + kFfnBox <= p.N;
+    if (f.res_ok) {
+      const uint4* r = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(p.R) + static_cast<long long>(m) * p.ldr + n0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f.res[k] = r[k];
+    }
+  }
+}
+
+__device__ __forceinline__ void ffn_add_bias(float b, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
 }
 
-// v += R[m, n0 .. n0+31].
-__device__ __forceinline__ void ffn_add_residual(const FfnParams& p, int m, int n0,
-                                                 float (&v)[32]) {
-  if (p.R == nullptr || m >= p.M) return;
-  const uint16_t* row = static_cast<const uint16_t*>(p.R) + static_cast<long long>(m) * p.ldr + n0;
+// v += R[m, n0 + 32 c .. + 31].
+__device__ __forceinline__ void ffn_add_residual(const FfnParams& p, const FfnFetched& f, int m,
+                                                 int n0, int c, float (&v)[32]) {
+  if (f.res_ok) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (p.r_vec && n0 + 8 * k + 8 <= p.N) {
-      const uint4 q = reinterpret_cast<const uint4*>(row)[k];
+    for (int k = 0; k < 4; ++k) {
+      const uint4 q = f.res[4 * c + k];
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack16(w[i], p.bf16);
-        v[8 * k + 2 * i] += f.x;
-        v[8 * k + 2 * i + 1] += f.y;
+        const float2 e = unpack16(w[i], p.bf16);
+        v[8 * k + 2 * i] += e.x;
+        v[8 * k + 2 * i + 1] += e.y;
       }
-    } else {
-#pragma unroll
-      for (int i = 8 * k; i < 8 * k + 8; ++i)
-        if (n0 + i < p.N) v[i] += load16(row, i, p.bf16);
     }
+  } else if (p.R != nullptr && m < p.M) {
+    const int n = n0 + 32 * c;
+    const uint16_t* row =
+        static_cast<const uint16_t*>(p.R) + static_cast<long long>(m) * p.ldr + n;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n + i < p.N) v[i] += load16(row, i, p.bf16);
   }
 }
 
@@ -293,8 +321,8 @@ __device__ __forceinline__ void ffn_tmem_load(uint32_t taddr, float (&v)[32]) {
 template <FfnOp kOp>
 __device__ __forceinline__ void ffn_epilogue_box(const FfnParams& p, const CUtensorMap* tmO0,
                                                  const CUtensorMap* tmO1, const CUtensorMap* tmO2,
-                                                 const Stager& st, uint32_t acc, int u_off, int m,
-                                                 int n0, int src, int lane) {
+                                                 const Stager& st, uint32_t acc, int u_off,
+                                                 const FfnFetched& f, int m, int n0, int src) {
   const bool bf16 = p.bf16 != 0;
   if constexpr (kOp == FfnOp::Gated) {
     uint32_t h[32], gk[32], uk[32];
@@ -303,8 +331,8 @@ __device__ __forceinline__ void ffn_epilogue_box(const FfnParams& p, const CUten
       float g[32], u[32];
       ffn_tmem_load(acc + 32 * c, g);
       ffn_tmem_load(acc + u_off + 32 * c, u);
-      ffn_add_bias(p, p.bias0, n0 + 32 * c, lane, g);
-      ffn_add_bias(p, p.bias1, n0 + 32 * c, lane, u);
+      if (p.bias0 != nullptr) ffn_add_bias(f.bias0[c], g);
+      if (p.bias1 != nullptr) ffn_add_bias(f.bias1[c], u);
       if (p.out[1].ptr != nullptr) {
         ffn_pack(g, gk + 16 * c, bf16);
         ffn_pack(u, uk + 16 * c, bf16);
@@ -331,13 +359,13 @@ __device__ __forceinline__ void ffn_epilogue_box(const FfnParams& p, const CUten
       float v[32];
       ffn_tmem_load(acc + 32 * c, v);
       if constexpr (kOp == FfnOp::Linear) {
-        ffn_add_bias(p, p.bias0, n, lane, v);
+        if (p.bias0 != nullptr) ffn_add_bias(f.bias0[c], v);
         if (p.out[1].ptr != nullptr) ffn_pack(v, z + 16 * c, bf16);
         with_act(p.act, [&](auto a) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = act_f32<decltype(a)::value>(v[i]);
         });
-        ffn_add_residual(p, m, n, v);
+        ffn_add_residual(p, f, m, n0, c, v);
       }
       if (o.f32)
         ffn_store_box32(o, map, st, m, n, v);
@@ -537,17 +565,21 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       const FfnUnit w = ffn_unit<kOp, BN>(p, u);
       const int src = kOp == FfnOp::GradW ? w.mb / p.tiles_m : 0;
       st.row0 = (w.mb - src * p.tiles_m) * BM + static_cast<int>(rank) * BM_CTA + quad * 32;
+      FfnFetched f;
+      ffn_fetch<kOp>(p, st.row0 + lane, w.n0 + first_box * kFfnBox, lane, f);
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, lim, abort_flag, p.status,
                                               kSiteEpiFull)))
         goto epi_done;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                              static_cast<uint32_t>(acc) * BN;
-      for (int b = first_box; b < w.cols / kFfnBox; b += 2)
-        if (w.n0 + b * kFfnBox < p.N)
-          ffn_epilogue_box<kOp>(p, &tmO0, &tmO1, &tmO2, st,
-                                taddr + static_cast<uint32_t>(b * kFfnBox), w.cols,
-                                st.row0 + lane, w.n0 + b * kFfnBox, src, lane);
+      for (int b = first_box; b < w.cols / kFfnBox && w.n0 + b * kFfnBox < p.N; b += 2) {
+        if (b != first_box)
+          ffn_fetch<kOp>(p, st.row0 + lane, w.n0 + b * kFfnBox, lane, f);
+        ffn_epilogue_box<kOp>(p, &tmO0, &tmO1, &tmO2, st,
+                              taddr + static_cast<uint32_t>(b * kFfnBox), w.cols, f,
+                              st.row0 + lane, w.n0 + b * kFfnBox, src);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(tempty_lead + static_cast<uint32_t>(acc) * 8u);

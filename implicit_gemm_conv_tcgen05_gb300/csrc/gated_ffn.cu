@@ -34,19 +34,11 @@ extern "C" int gated_ffn(int64_t M, int64_t F, int64_t K, int dtype, const void*
     for (int i = 0; i < 3; ++i) a.out[i] = outs[i];
     return ffn_bias_only(a, true, stream);
   }
-  const Mat x{X, ldx, dtype}, w[2] = {{Wg, ldw, dtype}, {Wu, ldw, dtype}};
-  if (M <= kSkinnyMaxM) {
-    SkinnyParams p = {};
-    p.M = static_cast<int>(M), p.N = static_cast<int>(F);
-    p.act = act;
-    p.bias0 = bg, p.bias1 = bu, p.bias_f32 = bias_dtype == IGC_F32;
-    return ffn_launch_skinny<true>(dev, dtype, K, x, w, p, outs, 3, stream);
-  }
-  FfnParams p = {};
-  p.M = static_cast<int>(M), p.N = static_cast<int>(F);
-  p.kb_seg = static_cast<int>((K + kFfnKS - 1) / kFfnKS);
-  p.segs = 1, p.srcs = 1;
-  p.act = act;
-  p.bias0 = bg, p.bias1 = bu, p.bias_f32 = bias_dtype == IGC_F32;
-  return ffn_launch<FfnOp::Gated>(dev, dtype, 1, &x, M, K, 2, w, F, K, outs, 3, p, stream);
+  FfnProblem q;
+  q.M = M, q.N = F, q.K = K, q.dtype = dtype;
+  q.A[0] = {X, ldx, dtype};
+  q.B[0] = {Wg, ldw, dtype}, q.B[1] = {Wu, ldw, dtype}, q.count_b = 2;
+  for (int i = 0; i < 3; ++i) q.out[i] = outs[i];
+  q.act = act, q.bias[0] = bg, q.bias[1] = bu, q.bias_dtype = bias_dtype;
+  return ffn_launch<FfnOp::Gated>(dev, q, stream);
 }

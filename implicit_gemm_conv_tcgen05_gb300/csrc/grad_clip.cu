@@ -2,14 +2,16 @@
 //
 // Bound by memory: every gradient is read for the norm and, scaled, read again and
 // written.  Two kernels.  The first deals chunks of all tensors over a fixed number of
-// blocks; a thread adds squares in fp32 over a chunk and chunks in fp64, a block writes
-// one partial sum.  In the second every block adds the partial sums itself, in the same
-// order (a few thousand doubles from L2, instead of a third launch between the two),
-// and scales its chunks.  It walks them backwards: the chunks that the first kernel read
-// last are still in L2.  No atomics, so the norm is the same every time.
+// blocks, a run of neighbouring chunks to each; a thread adds squares in fp32 over a
+// chunk and chunks in fp64, a block writes one partial sum.  In the second every block
+// adds the partial sums itself, in the same order (a few hundred doubles from L2, instead
+// of a third launch between the two), and scales its chunks.  It walks them backwards:
+// the chunks that the first kernel read last are still in L2.  No atomics, so the norm is
+// the same every time.
 //
-// The list of tensors travels in the kernel's parameters (up to 32764 bytes): nothing is
-// copied to the device, and the host arrays are free once the call returns.
+// The list of tensors travels in the kernel's parameters (up to 32764 bytes), with the
+// tensor at which each block starts: nothing is copied to the device, no block searches
+// the list, and the host arrays are free once the call returns.
 #include "ffn_act.cuh"
 #include "ffn_host.h"
 #include "sm100_ptx.cuh"
@@ -19,11 +21,11 @@ namespace igc {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kBlocksPerSm = 4;
-constexpr int kMaxBlocks = 1024;      // partial sums of one launch
+constexpr int kBlocksPerSm = 3;
+constexpr int kMaxBlocks = 512;       // partial sums of one launch
 constexpr int kTable = 1024;          // tensors of one launch
 constexpr int kSmallTable = 64;
-constexpr long long kMinChunk = 4096, kMaxChunk = 65536;  // elements
+constexpr long long kMinChunk = 2048, kMaxChunk = 32768, kChunkStep = 1024;  // elements
 
 template <int NT>
 struct Table {
@@ -31,36 +33,23 @@ struct Table {
   void* out[NT];
   long long n[NT];
   int first[NT + 1];  // first chunk of each tensor; first[count] = all chunks
+  unsigned short start[kMaxBlocks];  // tensor of each block's first chunk
   unsigned char dtype[NT];
-  int count;
+  int count, blocks;
   int chunk;
 };
 static_assert(sizeof(Table<kTable>) + 64 <= 32764, "kernel parameter limit");
 
-// Tensor that holds chunk c: the last one whose first chunk is at most c.
-template <int NT>
-__device__ __forceinline__ int tensor_of(const Table<NT>& t, int c) {
-  int lo = 0, hi = t.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (t.first[mid] <= c)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
+// First chunk of block b: the chunks are dealt in runs that differ by at most one.
+__host__ __device__ inline int first_chunk(int chunks, int blocks, int b) {
+  return static_cast<int>(static_cast<long long>(chunks) * b / blocks);
 }
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
+// Sum over the lanes of a warp, in every lane.
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-  __syncthreads();
-  double s = 0.0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += red[w];
-  __syncthreads();
-  return s;
+  return v;
 }
 
 __device__ __forceinline__ float load_elem(const void* p, long long i, int dtype) {
@@ -171,15 +160,16 @@ __device__ __forceinline__ void chunk_scale(const void* p, void* o, long long n,
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     norm_kernel(const __grid_constant__ Table<NT> t, double* partial) {
-  __shared__ double red[kThreads / 32];
+  __shared__ double red[kThreads];
+  const int c1 = first_chunk(t.first[t.count], t.blocks, blockIdx.x + 1);
+  int i = t.start[blockIdx.x];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int chunks = t.first[t.count];
   double sum = 0.0;
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
+  for (int c = first_chunk(t.first[t.count], t.blocks, blockIdx.x); c < c1; ++c) {
+    while (c >= t.first[i + 1]) ++i;
     const long long at = static_cast<long long>(c - t.first[i]) * t.chunk;
     const long long n = min(static_cast<long long>(t.chunk), t.n[i] - at);
     const int d = t.dtype[i];
@@ -188,26 +178,42 @@ __global__ void __launch_bounds__(kThreads, 2)
                         : (d == IGC_BF16 ? chunk_squares<IGC_BF16>(p, n)
                                          : chunk_squares<IGC_F16>(p, n));
   }
-  sum = block_sum(sum, red);
+  // one warp adds the threads' sums: fp64 additions are slow (about two a clock on an SM)
+  red[threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) sum += red[w * 32 + threadIdx.x];
+  sum = warp_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     scale_kernel(const __grid_constant__ Table<NT> t, const double* partial, int n_partial,
                  float max_norm, float eps, float* norm_out) {
-  __shared__ double red[kThreads / 32];
+  __shared__ float shared_norm;
+  const int chunks = t.first[t.count];
+  const int c0 = first_chunk(chunks, t.blocks, blockIdx.x);
+  const int c1 = first_chunk(chunks, t.blocks, blockIdx.x + 1);
+  int i = t.start[blockIdx.x];
+  while (i < t.count && t.first[i + 1] < c1) ++i;  // the tensor of the last chunk
   grid_dependency_wait();
   grid_dependents_launch();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < n_partial; i += kThreads) sum += partial[i];
-  const float norm = static_cast<float>(sqrt(block_sum(sum, red)));
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < n_partial; k += 32) sum += partial[k];
+    sum = warp_sum(sum);
+    if (threadIdx.x == 0) shared_norm = static_cast<float>(sqrt(sum));
+  }
+  __syncthreads();
+  const float norm = shared_norm;
   if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float ratio = max_norm / (norm + eps);
   const float coef = ratio > 1.0f ? 1.0f : ratio;  // (NaN stays NaN)
-  const int chunks = t.first[t.count];
-  for (int c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-    const int i = tensor_of(t, c);
+  for (int c = c1 - 1; c >= c0; --c) {
+    while (c < t.first[i]) --i;
     if (coef == 1.0f && t.out[i] == t.g[i]) continue;  // in place, times one
     const long long at = static_cast<long long>(c - t.first[i]) * t.chunk;
     const long long n = min(static_cast<long long>(t.chunk), t.n[i] - at);
@@ -224,11 +230,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// The tensors [t0, t1) of a call as a table; its number of chunks, or -1 if there are
-// more than an int holds.
+// The tensors [t0, t1) of a call as a table for at most `most` blocks; its number of
+// chunks, or -1 if there are more than an int holds.
 template <int NT>
 long long fill(Table<NT>& t, int64_t t0, int64_t t1, const void* const* grads,
-               const int64_t* sizes, const int32_t* dtypes, void* const* out, long long chunk) {
+               const int64_t* sizes, const int32_t* dtypes, void* const* out, long long chunk,
+               int most) {
   t.count = static_cast<int>(t1 - t0);
   t.chunk = static_cast<int>(chunk);
   long long at = 0;
@@ -243,6 +250,13 @@ long long fill(Table<NT>& t, int64_t t0, int64_t t1, const void* const* grads,
     if (at > 0x7ffffff0LL) return -1;
   }
   t.first[t.count] = static_cast<int>(at);
+  t.blocks = static_cast<int>(at < most ? (at < 1 ? 1 : at) : most);
+  int k = 0;
+  for (int b = 0; b < t.blocks; ++b) {
+    const int c = first_chunk(static_cast<int>(at), t.blocks, b);
+    while (k + 1 < t.count && c >= t.first[k + 1]) ++k;
+    t.start[b] = static_cast<unsigned short>(k);
+  }
   return at;
 }
 
@@ -255,40 +269,36 @@ int run(const DeviceInfo& dev, int64_t count, const void* const* grads, const in
   if (most > kMaxBlocks) most = kMaxBlocks;
   long long total = 0;
   for (int64_t i = 0; i < count; ++i) total += sizes[i];
-  // chunks: about eight per block, within the limits
-  long long chunk = kMinChunk;
-  while (chunk < kMaxChunk && chunk * most * 8 < total) chunk *= 2;
+  // Chunk: one per block where that suffices (with room for the tensors' ragged ends), and
+  // at most 32768 elements, so that a long list is dealt evenly.
+  long long chunk = (total + total / 4) / most;
+  chunk = (chunk + kChunkStep - 1) / kChunkStep * kChunkStep;
+  chunk = chunk < kMinChunk ? kMinChunk : (chunk > kMaxChunk ? kMaxChunk : chunk);
 
   Table<NT> t;
   const int64_t groups = count == 0 ? 1 : (count + NT - 1) / NT;
   int n_partial = 0;
   for (int64_t g = 0; g < groups; ++g) {
     const int64_t t1 = (g + 1) * NT < count ? (g + 1) * NT : count;
-    const long long chunks = fill(t, g * NT, t1, grads, sizes, dtypes, out, chunk);
+    const long long chunks = fill(t, g * NT, t1, grads, sizes, dtypes, out, chunk, most);
     if (chunks < 0) return IGC_ERR_UNSUPPORTED;
     if (chunks == 0) continue;
-    const int blocks = static_cast<int>(chunks < most ? chunks : most);
-    const int rc = launch_pdl(norm_kernel<NT>, dim3(blocks), dim3(kThreads), 0, stream, t,
+    const int rc = launch_pdl(norm_kernel<NT>, dim3(t.blocks), dim3(kThreads), 0, stream, t,
                               partial + n_partial);
     if (rc != IGC_OK) return rc;
-    n_partial += blocks;
+    n_partial += t.blocks;
   }
-  for (int64_t g = 0; g < groups; ++g) {
-    const int64_t t1 = (g + 1) * NT < count ? (g + 1) * NT : count;
-    long long chunks = 0;
-    if (out != nullptr) {
-      chunks = fill(t, g * NT, t1, grads, sizes, dtypes, out, chunk);
-    } else {
-      t.count = 0;
-      t.first[0] = 0;
-    }
-    if (chunks == 0 && g > 0) continue;  // the first one also writes the norm
-    const int blocks = static_cast<int>(chunks < 1 ? 1 : (chunks < most ? chunks : most));
-    const int rc = launch_pdl(scale_kernel<NT>, dim3(blocks), dim3(kThreads), 0, stream, t,
+  // the norm alone: one block of an empty table
+  const int64_t scaled = out != nullptr ? count : 0;
+  for (int64_t g = 0; g < (scaled == 0 ? 1 : groups); ++g) {
+    const int64_t t1 = (g + 1) * NT < scaled ? (g + 1) * NT : scaled;
+    // (with a single group the table is the one that the norm used)
+    if (groups > 1 || out == nullptr)
+      if (fill(t, g * NT, t1, grads, sizes, dtypes, out, chunk, most) == 0 && g > 0) continue;
+    const int rc = launch_pdl(scale_kernel<NT>, dim3(t.blocks), dim3(kThreads), 0, stream, t,
                               static_cast<const double*>(partial), n_partial, max_norm, eps,
                               g == 0 ? norm : static_cast<float*>(nullptr));
     if (rc != IGC_OK) return rc;
-    if (out == nullptr) break;
   }
   return IGC_OK;
 }

@@ -32,21 +32,11 @@ extern "C" int linear_act(int64_t M, int64_t N, int64_t K, int dtype, const void
     a.out[0] = outs[0], a.out[1] = outs[1];
     return ffn_bias_only(a, false, stream);
   }
-  const Mat x{X, ldx, dtype}, w{W, ldw, dtype};
-  if (M <= kSkinnyMaxM) {
-    SkinnyParams p = {};
-    p.M = static_cast<int>(M), p.N = static_cast<int>(N);
-    p.act = act;
-    p.bias0 = bias, p.bias_f32 = bias_dtype == IGC_F32;
-    p.R = R, p.ldr = ldr, p.r_vec = rows_aligned(R, ldr, 2, 8);
-    return ffn_launch_skinny<false>(dev, dtype, K, x, &w, p, outs, 2, stream);
-  }
-  FfnParams p = {};
-  p.M = static_cast<int>(M), p.N = static_cast<int>(N);
-  p.kb_seg = static_cast<int>((K + kFfnKS - 1) / kFfnKS);
-  p.segs = 1, p.srcs = 1;
-  p.act = act;
-  p.bias0 = bias, p.bias_f32 = bias_dtype == IGC_F32;
-  p.R = R, p.ldr = ldr, p.r_vec = rows_aligned(R, ldr, 2, 16);
-  return ffn_launch<FfnOp::Linear>(dev, dtype, 1, &x, M, K, 1, &w, N, K, outs, 2, p, stream);
+  FfnProblem q;
+  q.M = M, q.N = N, q.K = K, q.dtype = dtype;
+  q.A[0] = {X, ldx, dtype}, q.B[0] = {W, ldw, dtype};
+  q.out[0] = outs[0], q.out[1] = outs[1];
+  q.act = act, q.bias[0] = bias, q.bias_dtype = bias_dtype;
+  q.R = {R, ldr, dtype};
+  return ffn_launch<FfnOp::Linear>(dev, q, stream);
 }

@@ -161,6 +161,24 @@ int grad_norm_clip(int64_t count, const void *const *grads, const int64_t *sizes
                    const int32_t *dtypes, void *const *out, float max_norm, float eps,
                    float *norm, void *workspace, size_t workspace_bytes, igc_stream_t stream);
 
+/*
+ * igc_plan_ffn -- the schedule that one of the products above runs with, on a GPU of
+ * `sms` SMs, computed on the host by the launches' own decision functions.
+ *
+ *  op     IGC_PLAN_FFN_LINEAR, _GATED (the forward products), _GRAD_X, _GRAD_W (the
+ *         products of the backward passes); M, N (or F), K are the operator's sizes,
+ *         rows taken to start on 128-byte lines.
+ *  count  1 for linear_act_backward's products, 2 for gated_ffn_backward's.
+ *  out    int32[6]: 0 = 256-row tiles, 1 = the kernel for small outputs; output rows of a
+ *         tile or block; their number; CTAs that share the contraction of a block; the
+ *         estimated times of the small and of the tile kernel in nanoseconds.
+ */
+#define IGC_PLAN_FFN_LINEAR 0
+#define IGC_PLAN_FFN_GATED 1
+#define IGC_PLAN_FFN_GRAD_X 2
+#define IGC_PLAN_FFN_GRAD_W 3
+int igc_plan_ffn(int op, int64_t M, int64_t N, int64_t K, int count, int sms, int32_t *out);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,7 +18,7 @@ ODD = ctypes.c_void_p(4098)
 def test_header_declares_the_operators_and_the_library_exports_them():
     names = {"linear_act", "linear_act_backward", "linear_act_backward_workspace_size", "gated_ffn",
              "gated_ffn_backward", "gated_ffn_backward_workspace_size", "grad_norm_clip",
-             "grad_norm_clip_workspace_size"}
+             "grad_norm_clip_workspace_size", "igc_plan_ffn"}
     assert set(igc.declared_functions(igc.FFN_HEADER)) == names
     for n in names:
         assert ctypes.cast(getattr(igc.lib(), n), ctypes.c_void_p).value

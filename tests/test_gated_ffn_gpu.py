@@ -6,7 +6,7 @@ import torch
 import ffn_reference as ref
 import implicit_gemm_conv_tcgen05_gb300 as igc
 from gpu_helpers import check_device_ok
-from test_linear_act_gpu import BF16, F16, F32, d, generator, matrix
+from test_linear_act_gpu import BF16, F16, F32, d, generator, matrix, width  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -25,7 +25,7 @@ def make(M, F, K, dtype, bias, seed, pad=0):
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("M,F,K", SHAPES)
-def test_forward_shapes(M, F, K, dtype):
+def test_forward_shapes(M, F, K, dtype, width):
     i = SHAPES.index((M, F, K))
     name = ref.ACTS[i % 5]
     x, wg, wu, bg, bu = make(M, F, K, dtype, i % 2 == 0, i, pad=8 * (i % 2))
@@ -41,7 +41,7 @@ def test_forward_shapes(M, F, K, dtype):
 
 
 @pytest.mark.parametrize("M", [5, 200])
-def test_forward_one_bias_joined_weights_and_unaligned_outputs(M):
+def test_forward_one_bias_joined_weights_and_unaligned_outputs(M, width):
     F, K = 203, 264
     gen = generator(M, 31)
     x = matrix(gen, M, K, BF16)
@@ -102,7 +102,7 @@ BWD_SHAPES = [(1, 1, 1), (1, 64, 64), (3, 5, 8), (50, 129, 200), (129, 130, 72),
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("M,F,K", BWD_SHAPES)
-def test_backward_shapes(M, F, K, dtype):
+def test_backward_shapes(M, F, K, dtype, width):
     i = BWD_SHAPES.index((M, F, K))
     name = ref.ACTS[(i + 1) % 5]
     x, wg, wu, _, _ = make(M, F, K, dtype, False, 40 + i, pad=8 * (i % 2))
