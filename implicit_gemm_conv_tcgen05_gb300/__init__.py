@@ -563,10 +563,12 @@ def _act_code(act):
         raise ValueError(f"act is {act!r}: one of {', '.join(_ACTS)}") from None
 
 
-def _mat(t, name, dtypes, rows, cols):
-    """Row stride (in elements) of a rows x cols matrix: unit inner stride, rows that
-    do not overlap (so no broadcast view), one of `dtypes`.  A single row has no
-    stride of its own: it gets one that suits TMA."""
+def _mat(t, name, dtypes, rows, cols, dev):
+    """(pointer, row stride in elements) of a rows x cols matrix: unit inner stride, rows
+    that do not overlap (so no broadcast view), one of `dtypes`, on device `dev`.  A single
+    row has no stride of its own: it gets one that suits TMA.  (None, 0) for None."""
+    if t is None:
+        return None, 0
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}")
     if t.shape != (rows, cols):
@@ -574,17 +576,21 @@ def _mat(t, name, dtypes, rows, cols):
     s0, s1 = t.stride()
     if (s1 != 1 and cols > 1) or (s0 < cols and rows > 1):
         raise ValueError(f"{name} must be row-major with unit inner stride and rows apart")
-    return s0 if rows > 1 else (cols + 7) // 8 * 8
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    return t.data_ptr(), s0 if rows > 1 else (cols + 7) // 8 * 8
 
 
-def _vec_code(v, name, dtypes, n):
-    """dtype code of an optional vector of n elements (IGC_F32 for none)."""
+def _vector(v, name, dtypes, n, dev):
+    """(pointer, dtype code) of an optional vector of n elements ((None, IGC_F32) for None)."""
     if v is None:
-        return IGC_F32
-    if v.dtype not in dtypes or v.dim() != 1 or v.shape[0] != n or not v.is_contiguous():
+        return None, IGC_F32
+    if v.dtype not in dtypes or v.shape != (n,) or not v.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of length {n} and type "
                          f"{' or '.join(str(d) for d in dtypes)}")
-    return _dtype_code(v.dtype)
+    if v.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    return v.data_ptr(), _dtype_code(v.dtype)
 
 
 def _two_dims(t, name):
@@ -593,28 +599,23 @@ def _two_dims(t, name):
     return t.shape
 
 
-def _one_device(*pairs):
-    """Checks that all tensors given are on one CUDA device, and makes it current."""
-    dev = None
-    for name, t in pairs:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{name} is on another device")
-    import torch
-    if dev is not None and torch.cuda.current_device() != dev:
+def _check_device(dev, name):
+    """The device that all tensors of a call are on must be the current CUDA device."""
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _torch().cuda.current_device():
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+
+
+def _torch():
+    import torch
+    return torch
 
 
 def _new(shape, dtype, device, stream):
     """An uninitialised tensor that is safe to use on `stream` (None: the current one):
     memory that the caching allocator hands out belongs to the stream it was asked on."""
-    import torch
+    torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -623,13 +624,34 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _workspace(workspace, need, device, stream):
-    import torch
-    if workspace is None:
-        return _new(max(need, 1), torch.uint8, device, stream)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    return workspace
+# Workspaces up to this size are kept for the next call of the same thread on the same
+# stream (asking the allocator for one costs as much host time as the launches of a small
+# call); larger ones go back to the allocator when the call returns.
+_KEPT_WORKSPACE_BYTES = 32 * 1024 * 1024
+_kept = threading.local()
+
+
+def _workspace(workspace, need, like, stream):
+    """The workspace of a call: the one given, one kept by this thread for this stream, or
+    a new one.  Calls on one stream use it in stream order; another thread's calls, which
+    could come between a call's launches, have their own.  A CUDA graph under capture gets
+    its own too, since it goes on using it."""
+    torch = _torch()
+    if workspace is not None:
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor")
+        if workspace.get_device() != like.get_device():
+            raise ValueError("workspace is on another device")
+        return workspace
+    need = max(need, 1)
+    if need > _KEPT_WORKSPACE_BYTES or torch.cuda.is_current_stream_capturing():
+        return _new((need,), torch.uint8, like.device, stream)
+    key = (like.get_device(), _stream(stream))
+    kept = _kept.__dict__.get(key)
+    if kept is None or kept.numel() < need:
+        kept = _new((need,), torch.uint8, like.device, stream)
+        _kept.__dict__[key] = kept
+    return kept
 
 
 def linear_act(X, W, bias=None, act="none", residual=None, Y=None, Z=None, stream=None):
@@ -637,26 +659,25 @@ def linear_act(X, W, bias=None, act="none", residual=None, Y=None, Z=None, strea
     type (fp16 or bf16), Y (M,N) of that type or fp32, bias (N) of that type or fp32.
     Z, if given, receives the pre-activation for linear_act_backward.  residual may be
     Y itself.  Returns Y (allocated if None)."""
-    import torch
+    dtype = X.dtype
     dt = _operand_code(X, "X")
     code = _act_code(act)
     M, K = _two_dims(X, "X")
     N = _two_dims(W, "W")[0]
-    own = (X.dtype,)
-    either = (X.dtype, torch.float32)
-    ldx, ldw = _mat(X, "X", own, M, K), _mat(W, "W", own, N, K)
-    ldr = _mat(residual, "residual", own, M, N) if residual is not None else 0
-    ldz = _mat(Z, "Z", own, M, N) if Z is not None else 0
-    ldy = _mat(Y, "Y", either, M, N) if Y is not None else 0
-    bt = _vec_code(bias, "bias", either, N)
-    _one_device(("X", X), ("W", W), ("bias", bias), ("residual", residual), ("Y", Y), ("Z", Z))
+    dev = X.get_device()
+    own, either = (dtype,), (dtype, _torch().float32)
+    x, ldx = _mat(X, "X", own, M, K, dev)
+    w, ldw = _mat(W, "W", own, N, K, dev)
+    r, ldr = _mat(residual, "residual", own, M, N, dev)
+    z, ldz = _mat(Z, "Z", own, M, N, dev)
+    b, bt = _vector(bias, "bias", either, N, dev)
+    y, ldy = _mat(Y, "Y", either, M, N, dev)
+    _check_device(dev, "X")
     if Y is None:
-        Y = _new((M, N), X.dtype, X.device, stream)
-        ldy = N
-    rc = lib().linear_act(M, N, K, dt, X.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(bias), bt, code,
-                          _ptr(residual), ldr, _ptr(Z), ldz, Y.data_ptr(), ldy,
-                          _dtype_code(Y.dtype), _stream(stream))
-    _check(rc, "linear_act")
+        Y = _new((M, N), dtype, X.device, stream)
+        y, ldy = Y.data_ptr(), N
+    _check(lib().linear_act(M, N, K, dt, x, ldx, w, ldw, b, bt, code, r, ldr, z, ldz, y, ldy,
+                            dt if Y.dtype is dtype else IGC_F32, _stream(stream)), "linear_act")
     return Y
 
 
@@ -670,39 +691,43 @@ def linear_act_backward(dY, X, W, act="none", Z=None, dX=None, dW=None, dbias=No
     (not needed without an activation): dX (M,K), dW (N,K), dbias (N).  The ones given
     are computed (X is needed for dW, W for dX; the other may be None); with none
     given, dX and dW are allocated.  dW and dbias may be fp32.  Returns (dX, dW, dbias)."""
-    import torch
+    dtype = dY.dtype
     dt = _operand_code(dY, "dY")
     code = _act_code(act)
     M, N = _two_dims(dY, "dY")
+    dev = dY.get_device()
     if dX is None and dW is None and dbias is None:
         if X is None or W is None:
             raise ValueError("X and W are needed for dX and dW")
-        dX = _new(X.shape, dY.dtype, dY.device, stream)
-        dW = _new(W.shape, dY.dtype, dY.device, stream)
+        dX = _new(X.shape, dtype, dY.device, stream)
+        dW = _new(W.shape, dtype, dY.device, stream)
     if (dX is not None and W is None) or (dW is not None and X is None):
         raise ValueError("dX needs W and dW needs X")
     if code != IGC_ACT_NONE and Z is None:
         raise ValueError("Z, the pre-activation, is needed with an activation")
     k_of = W if W is not None else X
     K = _two_dims(k_of, "W" if W is not None else "X")[1] if k_of is not None else 0
-    own = (dY.dtype,)
-    either = (dY.dtype, torch.float32)
-    lddy = _mat(dY, "dY", own, M, N)
-    ldz = _mat(Z, "Z", own, M, N) if Z is not None else 0
-    ldx = _mat(X, "X", own, M, K) if X is not None else 0
-    ldw = _mat(W, "W", own, N, K) if W is not None else 0
-    lddx = _mat(dX, "dX", own, M, K) if dX is not None else 0
-    lddw = _mat(dW, "dW", either, N, K) if dW is not None else 0
-    bt = _vec_code(dbias, "dbias", either, N)
-    _one_device(("dY", dY), ("X", X), ("W", W), ("Z", Z), ("dX", dX), ("dW", dW),
-                ("dbias", dbias), ("workspace", workspace))
-    ws = _workspace(workspace, linear_act_backward_workspace_size(M, N, K), dY.device, stream)
-    rc = lib().linear_act_backward(M, N, K, dt, dY.data_ptr(), lddy, _ptr(Z), ldz, code, _ptr(X),
-                                   ldx, _ptr(W), ldw, _ptr(dX), lddx, _ptr(dW), lddw,
-                                   _dtype_code(dW.dtype) if dW is not None else IGC_F32,
-                                   _ptr(dbias), bt, ws.data_ptr(), ws.numel(), _stream(stream))
-    _check(rc, "linear_act_backward")
+    own, either = (dtype,), (dtype, _torch().float32)
+    dy, lddy = _mat(dY, "dY", own, M, N, dev)
+    z, ldz = _mat(Z, "Z", own, M, N, dev)
+    x, ldx = _mat(X, "X", own, M, K, dev)
+    w, ldw = _mat(W, "W", own, N, K, dev)
+    dx, lddx = _mat(dX, "dX", own, M, K, dev)
+    dw, lddw = _mat(dW, "dW", either, N, K, dev)
+    db, bt = _vector(dbias, "dbias", either, N, dev)
+    _check_device(dev, "dY")
+    L = lib()
+    ws = _workspace(workspace, L.linear_act_backward_workspace_size(M, N, K), dY, stream)
+    _check(L.linear_act_backward(M, N, K, dt, dy, lddy, z, ldz, code, x, ldx, w, ldw, dx, lddx,
+                                 dw, lddw, IGC_F32 if dW is None else _dtype_code(dW.dtype), db,
+                                 bt, ws.data_ptr(), ws.numel(), _stream(stream)),
+           "linear_act_backward")
     return dX, dW, dbias
+
+
+def _one_stride(a, b, names):
+    if a != b:
+        raise ValueError(f"{names} must have one row stride")
 
 
 def gated_ffn(X, Wg, Wu, bg=None, bu=None, act="silu", H=None, G=None, U=None, stream=None):
@@ -710,38 +735,33 @@ def gated_ffn(X, Wg, Wu, bg=None, bu=None, act="silu", H=None, G=None, U=None, s
     (two matrices, or the halves of a (2F,K) one), H (M,F), all of one type (fp16 or
     bf16); bg and bu (F) of that type or fp32.  G and U, if given, receive the two
     pre-activations for gated_ffn_backward.  Returns H (allocated if None)."""
-    import torch
+    dtype = X.dtype
     dt = _operand_code(X, "X")
     code = _act_code(act)
     M, K = _two_dims(X, "X")
     F = _two_dims(Wg, "Wg")[0]
-    own = (X.dtype,)
-    ldx = _mat(X, "X", own, M, K)
-    ldw = _mat(Wg, "Wg", own, F, K)
-    if _mat(Wu, "Wu", own, F, K) != ldw:
-        raise ValueError("Wg and Wu must have one row stride")
+    dev = X.get_device()
+    own, either = (dtype,), (dtype, _torch().float32)
     if (G is None) != (U is None):
         raise ValueError("G and U go together")
-    ldh = _mat(H, "H", own, M, F) if H is not None else 0
-    ldgu = 0
-    if G is not None:
-        ldgu = _mat(G, "G", own, M, F)
-        if _mat(U, "U", own, M, F) != ldgu:
-            raise ValueError("G and U must have one row stride")
-    either = (X.dtype, torch.float32)
-    bt = _vec_code(bg, "bg", either, F)
-    but = _vec_code(bu, "bu", either, F)
-    if bg is not None and bu is not None and bt != but:
+    x, ldx = _mat(X, "X", own, M, K, dev)
+    wg, ldw = _mat(Wg, "Wg", own, F, K, dev)
+    wu, ldwu = _mat(Wu, "Wu", own, F, K, dev)
+    _one_stride(ldw, ldwu, "Wg and Wu")
+    h, ldh = _mat(H, "H", own, M, F, dev)
+    g, ldg = _mat(G, "G", own, M, F, dev)
+    u, ldu = _mat(U, "U", own, M, F, dev)
+    _one_stride(ldg, ldu, "G and U")
+    b0, bt0 = _vector(bg, "bg", either, F, dev)
+    b1, bt1 = _vector(bu, "bu", either, F, dev)
+    if bg is not None and bu is not None and bt0 != bt1:
         raise ValueError("bg and bu must have one type")
-    _one_device(("X", X), ("Wg", Wg), ("Wu", Wu), ("bg", bg), ("bu", bu), ("H", H), ("G", G),
-                ("U", U))
+    _check_device(dev, "X")
     if H is None:
-        H = _new((M, F), X.dtype, X.device, stream)
-        ldh = F
-    rc = lib().gated_ffn(M, F, K, dt, X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw,
-                         _ptr(bg), _ptr(bu), bt if bg is not None else but, code, _ptr(G),
-                         _ptr(U), ldgu, H.data_ptr(), ldh, _stream(stream))
-    _check(rc, "gated_ffn")
+        H = _new((M, F), dtype, X.device, stream)
+        h, ldh = H.data_ptr(), F
+    _check(lib().gated_ffn(M, F, K, dt, x, ldx, wg, wu, ldw, b0, b1, bt0 if bg is not None else bt1,
+                           code, g, u, ldg, h, ldh, _stream(stream)), "gated_ffn")
     return H
 
 
@@ -756,54 +776,49 @@ def gated_ffn_backward(dH, G, U, X, Wg, Wu, act="silu", dX=None, dWg=None, dWu=N
     (the pairs go together; X is needed for the weights', Wg and Wu for dX); with none
     given, dX, dWg and dWu are allocated.  The weights' and biases' may be fp32.
     Returns (dX, dWg, dWu, dbg, dbu)."""
-    import torch
+    dtype = dH.dtype
     dt = _operand_code(dH, "dH")
     code = _act_code(act)
     M, F = _two_dims(dH, "dH")
+    dev = dH.get_device()
     if (Wg is None) != (Wu is None) or (dWg is None) != (dWu is None) or \
             (dbg is None) != (dbu is None):
         raise ValueError("Wg and Wu, dWg and dWu, and dbg and dbu go together")
     if dX is None and dWg is None and dbg is None:
         if X is None or Wg is None:
             raise ValueError("X, Wg and Wu are needed for dX, dWg and dWu")
-        dX = _new(X.shape, dH.dtype, dH.device, stream)
-        dWg = _new(Wg.shape, dH.dtype, dH.device, stream)
-        dWu = _new(Wg.shape, dH.dtype, dH.device, stream)
+        dX = _new(X.shape, dtype, dH.device, stream)
+        dWg = _new(Wg.shape, dtype, dH.device, stream)
+        dWu = _new(Wg.shape, dtype, dH.device, stream)
     if (dX is not None and Wg is None) or (dWg is not None and X is None):
         raise ValueError("dX needs Wg and Wu, dWg and dWu need X")
     k_of = Wg if Wg is not None else X
     K = _two_dims(k_of, "Wg" if Wg is not None else "X")[1] if k_of is not None else 0
-    own = (dH.dtype,)
-    either = (dH.dtype, torch.float32)
-    lddh = _mat(dH, "dH", own, M, F)
-    ldgu = _mat(G, "G", own, M, F)
-    if _mat(U, "U", own, M, F) != ldgu:
-        raise ValueError("G and U must have one row stride")
-    ldx = _mat(X, "X", own, M, K) if X is not None else 0
-    ldw = 0
-    if Wg is not None:
-        ldw = _mat(Wg, "Wg", own, F, K)
-        if _mat(Wu, "Wu", own, F, K) != ldw:
-            raise ValueError("Wg and Wu must have one row stride")
-    lddx = _mat(dX, "dX", own, M, K) if dX is not None else 0
-    lddw = 0
-    if dWg is not None:
-        lddw = _mat(dWg, "dWg", either, F, K)
-        if _mat(dWu, "dWu", (dWg.dtype,), F, K) != lddw:
-            raise ValueError("dWg and dWu must have one row stride")
-    bt = _vec_code(dbg, "dbg", either, F)
-    if _vec_code(dbu, "dbu", either, F) != bt:
+    own, either = (dtype,), (dtype, _torch().float32)
+    dh, lddh = _mat(dH, "dH", own, M, F, dev)
+    g, ldg = _mat(G, "G", own, M, F, dev)
+    u, ldu = _mat(U, "U", own, M, F, dev)
+    _one_stride(ldg, ldu, "G and U")
+    x, ldx = _mat(X, "X", own, M, K, dev)
+    wg, ldw = _mat(Wg, "Wg", own, F, K, dev)
+    wu, ldwu = _mat(Wu, "Wu", own, F, K, dev)
+    _one_stride(ldw, ldwu, "Wg and Wu")
+    dx, lddx = _mat(dX, "dX", own, M, K, dev)
+    dwg, lddw = _mat(dWg, "dWg", either, F, K, dev)
+    dwu, lddwu = _mat(dWu, "dWu", either if dWg is None else (dWg.dtype,), F, K, dev)
+    _one_stride(lddw, lddwu, "dWg and dWu")
+    b0, bt = _vector(dbg, "dbg", either, F, dev)
+    b1, bt1 = _vector(dbu, "dbu", either, F, dev)
+    if bt != bt1:
         raise ValueError("dbg and dbu must have one type")
-    _one_device(("dH", dH), ("G", G), ("U", U), ("X", X), ("Wg", Wg), ("Wu", Wu), ("dX", dX),
-                ("dWg", dWg), ("dWu", dWu), ("dbg", dbg), ("dbu", dbu), ("workspace", workspace))
-    ws = _workspace(workspace, gated_ffn_backward_workspace_size(M, F, K), dH.device, stream)
-    rc = lib().gated_ffn_backward(M, F, K, dt, dH.data_ptr(), lddh, G.data_ptr(), U.data_ptr(),
-                                  ldgu, code, _ptr(X), ldx, _ptr(Wg), _ptr(Wu), ldw, _ptr(dX),
-                                  lddx, _ptr(dWg), _ptr(dWu), lddw,
-                                  _dtype_code(dWg.dtype) if dWg is not None else IGC_F32,
-                                  _ptr(dbg), _ptr(dbu), bt, ws.data_ptr(), ws.numel(),
-                                  _stream(stream))
-    _check(rc, "gated_ffn_backward")
+    _check_device(dev, "dH")
+    L = lib()
+    ws = _workspace(workspace, L.gated_ffn_backward_workspace_size(M, F, K), dH, stream)
+    _check(L.gated_ffn_backward(M, F, K, dt, dh, lddh, g, u, ldg, code, x, ldx, wg, wu, ldw, dx,
+                                lddx, dwg, dwu, lddw,
+                                IGC_F32 if dWg is None else _dtype_code(dWg.dtype), b0, b1, bt,
+                                ws.data_ptr(), ws.numel(), _stream(stream)),
+           "gated_ffn_backward")
     return dX, dWg, dWu, dbg, dbu
 
 
@@ -863,8 +878,10 @@ def grad_norm_clip(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=Non
     device = grads[0].device if n else (norm.device if norm is not None else "cuda")
     if norm is None:
         norm = _new((), torch.float32, device, stream)
-    _one_device(("grads", grads[0] if n else None), ("norm", norm), ("workspace", workspace))
-    ws = _workspace(workspace, grad_norm_clip_workspace_size(n), device, stream)
+    if n and norm.get_device() != grads[0].get_device():
+        raise ValueError("norm is on another device")
+    _check_device(norm.get_device(), "norm")
+    ws = _workspace(workspace, grad_norm_clip_workspace_size(n), norm, stream)
     rc = lib().grad_norm_clip(n, g_ptr, sizes.buffer_info()[0], codes.buffer_info()[0], o_ptr,
                               float(max_norm), float(eps), norm.data_ptr(), ws.data_ptr(),
                               ws.numel(), _stream(stream))

@@ -71,12 +71,15 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
   const bool identity = !gated && act == IGC_ACT_NONE;
   const bool copy = (want_x || want_w) && (!identity || !operand_ok(dO.ptr, dO.ld));
   Mat D[2] = {{dO.ptr, dO.ld, dtype}, {}};
+  // The three results after it read what the activation's pass wrote and nothing of one
+  // another: each but the first may run beside the one before it (late_wait).
+  bool after_first = false;
+  DactArgs a;
   if (copy || want_b) {
     if (workspace == nullptr || workspace_bytes < need ||
         reinterpret_cast<uintptr_t>(workspace) % kAlign != 0)
       return IGC_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    DactArgs a;
     a.M = M, a.N = N, a.dtype = dtype, a.act = act;
     a.dO = dO, a.Z = Z, a.U = U;
     a.ldd = padded(N);
@@ -93,10 +96,16 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
     if (rc != IGC_OK) return rc;
   }
   if (want_x) {
-    rc = ffn_grad_x(dev, M, N, K, dtype, n, D, W, dX, stream);
+    rc = ffn_grad_x(dev, M, N, K, dtype, n, D, W, dX, after_first, stream);
     if (rc != IGC_OK) return rc;
+    after_first = true;
   }
-  if (want_w) rc = ffn_grad_w(dev, M, N, K, dtype, n, D, X, dW, stream);
+  if (want_w) {
+    rc = ffn_grad_w(dev, M, N, K, dtype, n, D, X, dW, after_first, stream);
+    if (rc != IGC_OK) return rc;
+    after_first = true;
+  }
+  if (want_b) rc = ffn_dact_sums(a, gated, after_first, stream);
   return rc;
 }
 

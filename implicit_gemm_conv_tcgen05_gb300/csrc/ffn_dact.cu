@@ -11,7 +11,7 @@
 // workspace, and a second kernel adds the chunks in order (no atomics).
 #include "ffn_act.cuh"
 #include "ffn_host.h"
-#include "sm100_ptx.cuh"
+#include "ffn_tc.cuh"
 
 namespace igc {
 
@@ -109,7 +109,7 @@ __device__ __forceinline__ void unpack8(uint4 q, bool bf16, float (&v)[8]) {
 template <bool kGated, int kAct, bool kSum>
 __device__ __forceinline__ void dact_rows(const DactParams& p, int n, long long r0, long long r1,
                                           float (&s0)[8], float (&s1)[8]) {
-  constexpr int kUnroll = 2;
+  constexpr int kUnroll = kGated ? 2 : 4;
   constexpr bool kNeedZ = kGated || kAct != IGC_ACT_NONE;
   const int warp = threadIdx.x / 32;
   const bool bf16 = p.bf16 != 0;
@@ -199,10 +199,9 @@ int launch_dact(const DactParams& p, dim3 grid, cudaStream_t stream) {
 __global__ void __launch_bounds__(256) sum_chunks_kernel(const float* partial0,
                                                          const float* partial1, int chunks, int N,
                                                          void* out0, void* out1, int f32,
-                                                         int bf16) {
+                                                         int bf16, int late_wait) {
   __shared__ float red[8][32];
-  grid_dependency_wait();
-  grid_dependents_launch();
+  ffn_dependency_wait(late_wait);
   const float* partial = blockIdx.y ? partial1 : partial0;
   void* out = blockIdx.y ? out1 : out0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -212,13 +211,15 @@ __global__ void __launch_bounds__(256) sum_chunks_kernel(const float* partial0,
     for (int c = warp; c < chunks; c += 8) t += partial[static_cast<long long>(c) * N + n];
   red[warp][lane] = t;
   __syncthreads();
-  if (warp != 0 || n >= N) return;
+  if (warp == 0 && n < N) {
 #pragma unroll
-  for (int w = 1; w < 8; ++w) t += red[w][lane];
-  if (f32)
-    static_cast<float*>(out)[n] = t;
-  else
-    store16(out, n, t, bf16);
+    for (int w = 1; w < 8; ++w) t += red[w][lane];
+    if (f32)
+      static_cast<float*>(out)[n] = t;
+    else
+      store16(out, n, t, bf16);
+  }
+  ffn_dependency_end(late_wait);
 }
 
 // ---------------------------------------------------------------------------
@@ -298,15 +299,21 @@ int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream) {
   }
   const dim3 grid(static_cast<unsigned>((a.N + kCols - 1) / kCols), static_cast<unsigned>(chunks));
   const bool sum = a.db0 != nullptr;
-  const int rc = gated ? (sum ? launch_dact<true, true>(p, grid, stream)
-                              : launch_dact<true, false>(p, grid, stream))
-                       : (sum ? launch_dact<false, true>(p, grid, stream)
-                              : launch_dact<false, false>(p, grid, stream));
-  if (rc != IGC_OK || a.db0 == nullptr) return rc;
+  return gated ? (sum ? launch_dact<true, true>(p, grid, stream)
+                      : launch_dact<true, false>(p, grid, stream))
+               : (sum ? launch_dact<false, true>(p, grid, stream)
+                      : launch_dact<false, false>(p, grid, stream));
+}
+
+int ffn_dact_sums(const DactArgs& a, bool gated, bool late_wait, cudaStream_t stream) {
+  const int64_t chunks = dact_chunks(a.M, a.N);
   return launch_pdl(sum_chunks_kernel,
                     dim3(static_cast<unsigned>((a.N + 31) / 32), gated ? 2 : 1), dim3(256), 0,
-                    stream, p.partial0, p.partial1, static_cast<int>(chunks), p.N, a.db0, a.db1,
-                    a.db_dtype == IGC_F32 ? 1 : 0, p.bf16);
+                    stream, static_cast<const float*>(a.partial),
+                    static_cast<const float*>(a.partial + (gated ? chunks * a.N : 0)),
+                    static_cast<int>(chunks), static_cast<int>(a.N), a.db0, a.db1,
+                    a.db_dtype == IGC_F32 ? 1 : 0, a.dtype == IGC_BF16 ? 1 : 0,
+                    late_wait ? 1 : 0);
 }
 
 int ffn_bias_only(const PointwiseArgs& a, bool gated, cudaStream_t stream) {

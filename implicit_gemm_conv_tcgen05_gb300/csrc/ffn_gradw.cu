@@ -5,8 +5,10 @@
 namespace igc {
 
 int ffn_grad_w(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
-               const Mat* D, const Mat& X, const Mat* dW, cudaStream_t stream) {
+               const Mat* D, const Mat& X, const Mat* dW, bool late_wait,
+               cudaStream_t stream) {
   FfnProblem q;
+  q.late_wait = late_wait;
   q.M = N, q.N = K, q.K = M, q.dtype = dtype;
   q.srcs = q.count_a = count;
   for (int i = 0; i < count; ++i) q.A[i] = D[i], q.out[i] = dW[i];

@@ -5,8 +5,10 @@
 namespace igc {
 
 int ffn_grad_x(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
-               const Mat* D, const Mat* W, const Mat& dX, cudaStream_t stream) {
+               const Mat* D, const Mat* W, const Mat& dX, bool late_wait,
+               cudaStream_t stream) {
   FfnProblem q;
+  q.late_wait = late_wait;
   q.M = M, q.N = K, q.K = N, q.dtype = dtype;
   q.segs = q.count_a = q.count_b = count;
   for (int i = 0; i < count; ++i) q.A[i] = D[i], q.B[i] = W[i];

@@ -28,12 +28,13 @@ struct Mat {
   int dtype = IGC_F32;
 };
 
-// dX = sum_s D[s] W[s]: D[s] M x N, W[s] N x K, dX M x K (ffn_gradx.cu)
+// dX = sum_s D[s] W[s]: D[s] M x N, W[s] N x K, dX M x K (ffn_gradx.cu).  late_wait: the
+// kernel may run beside the one before it in the stream (ffn_dependency_wait, ffn_tc.cuh).
 int ffn_grad_x(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
-               const Mat* D, const Mat* W, const Mat& dX, cudaStream_t stream);
+               const Mat* D, const Mat* W, const Mat& dX, bool late_wait, cudaStream_t stream);
 // dW[s] = D[s]^T X: X M x K, dW[s] N x K (ffn_gradw.cu)
 int ffn_grad_w(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
-               const Mat* D, const Mat& X, const Mat* dW, cudaStream_t stream);
+               const Mat* D, const Mat& X, const Mat* dW, bool late_wait, cudaStream_t stream);
 
 // Forward passes over the fp32 pre-activations of a contraction of length zero
 // (the biases alone), and the backward passes over stored pre-activations (ffn_dact.cu).
@@ -62,5 +63,7 @@ struct DactArgs {
 };
 int64_t dact_chunks(int64_t M, int64_t N);
 int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream);
+// The bias gradients from the partial sums that ffn_dact left.
+int ffn_dact_sums(const DactArgs& a, bool gated, bool late_wait, cudaStream_t stream);
 
 }  // namespace igc

@@ -149,6 +149,7 @@ struct FfnProblem {
   const void* bias[2] = {};
   int bias_dtype = IGC_F32;
   Mat R;
+  bool late_wait = false;       // see ffn_dependency_wait
 };
 
 // Stored extents of operand i: MN-major operands have k as their rows.
@@ -169,6 +170,7 @@ int ffn_launch_tiles(const DeviceInfo& dev, const FfnProblem& q, int clusters,
   p.M = static_cast<int>(q.M), p.N = static_cast<int>(q.N);
   p.kb_seg = static_cast<int>((q.K + kFfnKS - 1) / kFfnKS);
   p.segs = q.segs, p.srcs = q.srcs;
+  p.late_wait = q.late_wait;
   p.bf16 = q.dtype == IGC_BF16;
   p.act = q.act;
   p.bias0 = q.bias[0], p.bias1 = q.bias[1], p.bias_f32 = q.bias_dtype == IGC_F32;
@@ -198,6 +200,7 @@ int ffn_launch_tiles(const DeviceInfo& dev, const FfnProblem& q, int clusters,
 // ---------------------------------------------------------------------------
 constexpr size_t kSmallSmemTwo = 110 * 1024;  // two CTAs on an SM
 constexpr size_t kSmallSmemOne = 224 * 1024;
+constexpr size_t kSmemPerSm = 228 * 1024;
 
 // Estimated times in microseconds, for choosing between schedules (measured on GB300: a
 // CTA takes in about 65 bytes a nanosecond through TMA, two on an SM 95 together, one with
@@ -337,6 +340,16 @@ int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const SmallPlan
   if (stages > static_cast<size_t>(p.per_cta)) stages = static_cast<size_t>(p.per_cta);
   p.stages = static_cast<int>(stages);
   const size_t ring = stages * stage;
+  // No more CTAs on an SM than its 512 tensor-memory columns serve: a CTA waiting for
+  // columns that CTAs of other clusters hold, while those wait for its own cluster, would
+  // never get them.
+  const size_t spread = kSmemPerSm / (512 / p.tmem_cols + 1);
+  p.late_wait = q.late_wait;
+  // Weights past half of the L2 are gone before they are read again: marked to be evicted
+  // first, they leave the lines that the next kernel prefetches alone (134 MB, one token:
+  // 22.7 -> 21.1 us; smaller weights, which may still be there next time, are not marked).
+  p.once = p.m_blocks == 1 &&
+           2.0 * static_cast<double>(q.N) * static_cast<double>(q.K) * q.count_b >= 64e6;
   p.bf16 = q.dtype == IGC_BF16;
   p.act = q.act;
   p.bias0 = q.bias[0], p.bias1 = q.bias[1], p.bias_f32 = q.bias_dtype == IGC_F32;
@@ -361,7 +374,7 @@ int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const SmallPlan
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks * p.split), 1, 1);
   cfg.blockDim = dim3(kSkThreads, 1, 1);
-  cfg.dynamicSmemBytes = 1024 + (ring > part ? ring : part);
+  cfg.dynamicSmemBytes = std::max(1024 + std::max(ring, part), spread);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -81,6 +81,7 @@ struct FfnParams {
   int tiles_m;   // m-tiles of one output matrix
   int tiles_n, num_tiles, group_m, tail_start, num_units;
   int bf16;      // operand type (else fp16)
+  int late_wait; // see ffn_dependency_wait
   int act;
   const void* bias0;
   const void* bias1;
@@ -105,6 +106,19 @@ __device__ __forceinline__ uint64_t make_sw128_mnmajor_desc(uint32_t smem_addr, 
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
+}
+
+// Programmatic dependent launch.  A kernel normally waits for the one before it in the
+// stream (kernel B) before it touches memory.  With `late` it shares no memory with B
+// that either of them writes, and B waited early itself: then everything before B is
+// complete once B's blocks have let this kernel start, and it may run beside B.  It still
+// waits for B before it ends, so that its own completion means B's to what comes next.
+__device__ __forceinline__ void ffn_dependency_wait(bool late) {
+  if (!late) grid_dependency_wait();
+  grid_dependents_launch();
+}
+__device__ __forceinline__ void ffn_dependency_end(bool late) {
+  if (late) grid_dependency_wait();
 }
 
 // A unit of the schedule: the columns [n0, n0 + cols) of m-tile mb.
@@ -436,8 +450,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
   tc_fence_after();
   // nothing above touches global memory; from here on the previous kernel in the
   // stream must have finished (programmatic dependent launch)
-  grid_dependency_wait();
-  grid_dependents_launch();
+  ffn_dependency_wait(p.late_wait);
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t lim = p.wait_limit_ns;
   // the pair's MMAs write both CTAs' tensor memory at the leader's address
@@ -602,6 +615,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     tc_fence_after();
     tmem_dealloc_2cta(tmem_base, Cfg::kTmemCols);
   }
+  ffn_dependency_end(p.late_wait);
 }
 
 }  // namespace igc
