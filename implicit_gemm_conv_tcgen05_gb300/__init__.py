@@ -625,17 +625,18 @@ def _new(shape, dtype, device, stream):
 
 
 # Workspaces up to this size are kept for the next call of the same thread on the same
-# stream (asking the allocator for one costs as much host time as the launches of a small
-# call); larger ones go back to the allocator when the call returns.
+# current stream (asking the allocator for one costs as much host time as the launches of
+# a small call); larger ones go back to the allocator when the call returns.
 _KEPT_WORKSPACE_BYTES = 32 * 1024 * 1024
 _kept = threading.local()
 
 
 def _workspace(workspace, need, like, stream):
-    """The workspace of a call: the one given, one kept by this thread for this stream, or
-    a new one.  Calls on one stream use it in stream order; another thread's calls, which
-    could come between a call's launches, have their own.  A CUDA graph under capture gets
-    its own too, since it goes on using it."""
+    """The workspace of a call: the one given, one kept by this thread for the current
+    stream, or a new one.  Calls on one stream use it in stream order; another thread's
+    calls, which could come between a call's launches, have their own.  A call on a stream
+    named by the caller and one under graph capture (the graph goes on using it) get a new
+    one."""
     torch = _torch()
     if workspace is not None:
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -644,13 +645,13 @@ def _workspace(workspace, need, like, stream):
             raise ValueError("workspace is on another device")
         return workspace
     need = max(need, 1)
-    if need > _KEPT_WORKSPACE_BYTES or torch.cuda.is_current_stream_capturing():
+    if stream is not None or need > _KEPT_WORKSPACE_BYTES or \
+            torch.cuda.is_current_stream_capturing():
         return _new((need,), torch.uint8, like.device, stream)
-    key = (like.get_device(), _stream(stream))
+    key = (like.get_device(), _stream(None))
     kept = _kept.__dict__.get(key)
     if kept is None or kept.numel() < need:
-        kept = _new((need,), torch.uint8, like.device, stream)
-        _kept.__dict__[key] = kept
+        kept = _kept.__dict__[key] = _new((need,), torch.uint8, like.device, None)
     return kept
 
 

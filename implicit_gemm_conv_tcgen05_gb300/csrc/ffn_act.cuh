@@ -13,26 +13,43 @@
 
 namespace igc {
 
-// 1 / (1 + exp(-x)): exp(-x) overflows to infinity for x < -88, and the quotient
-// is then 0, as it should be to fp32's precision.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(-x));
+// 2^x and 1/x to within 2^-22 and 2^-23 of their value (one instruction each: the forms
+// that flush subnormals need no range handling, and a subnormal 2^x is 0 beside the 1 that
+// it is added to here).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 constexpr float kInvSqrt2 = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-// act(z).  z (1 + tanh(u)) / 2 equals z sigmoid(2u), which needs one exponential and
-// one division, and keeps its relative accuracy where tanh(u) is near -1.
+// 1 / (1 + 2^-t): the sigmoid of t / log2(e).  2^-t overflows to infinity for t < -128,
+// and its reciprocal is then 0, as the sigmoid is to fp32's precision.
+__device__ __forceinline__ float sigmoid2(float t) { return rcp_approx(1.0f + exp2_approx(-t)); }
+
+// 2 log2(e) c (z + a z^3), c = sqrt(2 / pi): z (1 + tanh(u)) / 2 equals z sigmoid(2 u), which
+// needs no tanh and keeps its relative accuracy where tanh(u) is near -1.
+__device__ __forceinline__ float gelu_tanh_arg(float z, float z2) {
+  return z * fmaf(2.0f * kLog2E * kGeluC * kGeluA, z2, 2.0f * kLog2E * kGeluC);
+}
+
+// act(z)
 template <int kAct>
 __device__ __forceinline__ float act_f32(float z) {
   if constexpr (kAct == IGC_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
   if constexpr (kAct == IGC_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kInvSqrt2));
-  if constexpr (kAct == IGC_ACT_GELU_TANH)
-    return z * sigmoid_f32(2.0f * kGeluC * (z + kGeluA * z * z * z));
-  if constexpr (kAct == IGC_ACT_SILU) return z * sigmoid_f32(z);
+  if constexpr (kAct == IGC_ACT_GELU_TANH) return z * sigmoid2(gelu_tanh_arg(z, z * z));
+  if constexpr (kAct == IGC_ACT_SILU) return z * sigmoid2(kLog2E * z);
   return z;
 }
 
@@ -43,19 +60,19 @@ __device__ __forceinline__ void act_grad_f32(float z, float& f, float& d) {
     f = z > 0.0f ? z : (z != z ? z : 0.0f);
     d = z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (kAct == IGC_ACT_GELU) {
-    const float cdf = 0.5f * (1.0f + erff(z * kInvSqrt2));
+    const float cdf = fmaf(0.5f, erff(z * kInvSqrt2), 0.5f);
     f = z * cdf;
-    d = cdf + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+    d = fmaf(z * kInvSqrt2Pi, exp2_approx((-0.5f * kLog2E) * z * z), cdf);
   } else if constexpr (kAct == IGC_ACT_GELU_TANH) {
-    const float s = sigmoid_f32(2.0f * kGeluC * (z + kGeluA * z * z * z));
+    // s (1 - s) is 0 long before z^2 reaches the bound, which keeps its factor finite
+    const float z2 = fminf(z * z, 1e12f);
+    const float s = sigmoid2(gelu_tanh_arg(z, z2));
     f = z * s;
-    // s (1 - s) is 0 once |z| is large, where z (1 + 3 a z^2) may be infinite
-    const float q = s * (1.0f - s);
-    d = s + (q == 0.0f ? 0.0f : z * q * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * z * z));
+    d = fmaf(z * fmaf(6.0f * kGeluC * kGeluA, z2, 2.0f * kGeluC), fmaf(-s, s, s), s);
   } else if constexpr (kAct == IGC_ACT_SILU) {
-    const float s = sigmoid_f32(z);
+    const float s = sigmoid2(kLog2E * z);
     f = z * s;
-    d = s + f * (1.0f - s);
+    d = fmaf(f, 1.0f - s, s);
   } else {
     f = z;
     d = 1.0f;

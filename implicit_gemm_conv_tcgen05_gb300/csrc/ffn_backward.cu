@@ -40,6 +40,14 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
   const bool want_w = dW[0].ptr != nullptr && N > 0 && K > 0;
   const bool want_b = db[0] != nullptr && N > 0;
   if (!want_x && !want_w && !want_b) return IGC_OK;
+  // outputs are no inputs and all different
+  const void* outs[5] = {dX.ptr, dW[0].ptr, n > 1 ? dW[1].ptr : nullptr, db[0], db[1]};
+  for (int i = 0; i < 5; ++i) {
+    if (is_any(outs[i], dO.ptr, Z.ptr, U.ptr, X.ptr, W[0].ptr, n > 1 ? W[1].ptr : nullptr))
+      return IGC_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (is_any(outs[i], outs[j])) return IGC_ERR_INVALID_ARG;
+  }
   if (!fits32(M) || !fits32(N) || !fits32(K)) return IGC_ERR_UNSUPPORTED;
   if (M > 0 && N > 0) {
     if (dO.ptr == nullptr || dO.ld < N) return IGC_ERR_INVALID_ARG;

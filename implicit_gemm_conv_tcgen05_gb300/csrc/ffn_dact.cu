@@ -106,13 +106,13 @@ __device__ __forceinline__ void unpack8(uint4 q, bool bf16, float (&v)[8]) {
 
 // Bound by memory where it reads 16-byte vectors: kUnroll rows' loads are issued before
 // the first is used, so that an SM keeps some 70 KB in flight.
-template <bool kGated, int kAct, bool kSum>
+template <bool kGated, int kAct, bool kSum, bool kBf16>
 __device__ __forceinline__ void dact_rows(const DactParams& p, int n, long long r0, long long r1,
                                           float (&s0)[8], float (&s1)[8]) {
   constexpr int kUnroll = kGated ? 2 : 4;
   constexpr bool kNeedZ = kGated || kAct != IGC_ACT_NONE;
+  constexpr bool bf16 = kBf16;  // (as a run-time flag: 28 instructions an element)
   const int warp = threadIdx.x / 32;
-  const bool bf16 = p.bf16 != 0;
   auto finish = [&](long long r, float(&o)[8], float(&z)[8], float(&u)[8]) {
     if constexpr (kNeedZ) dact8<kGated, kAct>(o, z, u);
     float(&d0)[8] = kGated ? z : o;
@@ -162,7 +162,7 @@ __device__ __forceinline__ void dact_rows(const DactParams& p, int n, long long 
   }
 }
 
-template <bool kGated, int kAct, bool kSum>
+template <bool kGated, int kAct, bool kSum, bool kBf16>
 __global__ void __launch_bounds__(kRowLanes * 32, 3) dact_kernel(const DactParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kRowLanes * 32, 3) dact_kernel(const DactParam
   const long long r0 = static_cast<long long>(blockIdx.y) * p.rows_per_chunk;
   const long long r1 = min(static_cast<long long>(p.M), r0 + p.rows_per_chunk);
   float s0[8] = {}, s1[8] = {};
-  if (n < p.N) dact_rows<kGated, kAct, kSum>(p, n, r0, r1, s0, s1);
+  if (n < p.N) dact_rows<kGated, kAct, kSum, kBf16>(p, n, r0, r1, s0, s1);
   if constexpr (kSum) {
     __shared__ float red[kRowLanes][kCols];
     block_sums(red, s0, p.partial0, p.N);
@@ -178,21 +178,23 @@ __global__ void __launch_bounds__(kRowLanes * 32, 3) dact_kernel(const DactParam
   }
 }
 
-template <bool kGated, bool kSum>
+template <bool kGated, bool kSum, bool kBf16>
 int launch_dact(const DactParams& p, dim3 grid, cudaStream_t stream) {
-  const dim3 block(kRowLanes * 32);
+  void (*kern)(DactParams) = dact_kernel<kGated, IGC_ACT_NONE, kSum, kBf16>;
   switch (p.act) {
-    case IGC_ACT_RELU:
-      return launch_pdl(dact_kernel<kGated, IGC_ACT_RELU, kSum>, grid, block, 0, stream, p);
-    case IGC_ACT_GELU:
-      return launch_pdl(dact_kernel<kGated, IGC_ACT_GELU, kSum>, grid, block, 0, stream, p);
-    case IGC_ACT_GELU_TANH:
-      return launch_pdl(dact_kernel<kGated, IGC_ACT_GELU_TANH, kSum>, grid, block, 0, stream, p);
-    case IGC_ACT_SILU:
-      return launch_pdl(dact_kernel<kGated, IGC_ACT_SILU, kSum>, grid, block, 0, stream, p);
-    default:
-      return launch_pdl(dact_kernel<kGated, IGC_ACT_NONE, kSum>, grid, block, 0, stream, p);
+    case IGC_ACT_RELU: kern = dact_kernel<kGated, IGC_ACT_RELU, kSum, kBf16>; break;
+    case IGC_ACT_GELU: kern = dact_kernel<kGated, IGC_ACT_GELU, kSum, kBf16>; break;
+    case IGC_ACT_GELU_TANH: kern = dact_kernel<kGated, IGC_ACT_GELU_TANH, kSum, kBf16>; break;
+    case IGC_ACT_SILU: kern = dact_kernel<kGated, IGC_ACT_SILU, kSum, kBf16>; break;
+    default: break;
   }
+  return launch_pdl(kern, grid, dim3(kRowLanes * 32), 0, stream, p);
+}
+
+template <bool kGated, bool kSum>
+int launch_dact_type(const DactParams& p, dim3 grid, cudaStream_t stream) {
+  return p.bf16 ? launch_dact<kGated, kSum, true>(p, grid, stream)
+                : launch_dact<kGated, kSum, false>(p, grid, stream);
 }
 
 // out[n] = sum over chunks of partial[chunk][n]; blockIdx.y: which vector.
@@ -268,22 +270,26 @@ __global__ void __launch_bounds__(256) bias_only_kernel(const BiasOnlyParams p) 
 
 }  // namespace
 
-// Chunks of rows: enough blocks to fill the GPU several times over, at least a row for
-// each of a block's warps.
-int64_t dact_chunks(int64_t M, int64_t N) {
+// Rows of a chunk: a whole number of unrolled steps of a block's warps (8, 16 or a multiple
+// of 32 rows), few enough that some 4096 blocks even out over the SMs.
+static int64_t dact_rows(int64_t M, int64_t N) {
   const int64_t col_blocks = (N + kCols - 1) / kCols;
-  const int64_t most = (M + kRowLanes - 1) / kRowLanes;
-  int64_t want = col_blocks > 0 ? (2432 + col_blocks - 1) / col_blocks : 1;
-  if (want > kMaxChunks) want = kMaxChunks;
-  if (want > most) want = most;
-  return want < 1 ? 1 : want;
+  int64_t chunks = col_blocks > 0 ? (4096 + col_blocks - 1) / col_blocks : 1;
+  if (chunks > kMaxChunks) chunks = kMaxChunks;
+  const int64_t rows = (M + chunks - 1) / chunks;
+  return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows + 31) / 32 * 32);
+}
+
+int64_t dact_chunks(int64_t M, int64_t N) {
+  const int64_t rows = dact_rows(M, N);
+  return M > 0 ? (M + rows - 1) / rows : 1;
 }
 
 int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream) {
   DactParams p = {};
   p.M = static_cast<int>(a.M), p.N = static_cast<int>(a.N);
   const int64_t chunks = dact_chunks(a.M, a.N);
-  p.rows_per_chunk = static_cast<int>((a.M + chunks - 1) / chunks);
+  p.rows_per_chunk = static_cast<int>(dact_rows(a.M, a.N));
   p.bf16 = a.dtype == IGC_BF16, p.act = a.act;
   p.dO = static_cast<const uint16_t*>(a.dO.ptr), p.ldo = a.dO.ld;
   p.Z = static_cast<const uint16_t*>(a.Z.ptr), p.ldz = a.Z.ld;
@@ -299,10 +305,10 @@ int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream) {
   }
   const dim3 grid(static_cast<unsigned>((a.N + kCols - 1) / kCols), static_cast<unsigned>(chunks));
   const bool sum = a.db0 != nullptr;
-  return gated ? (sum ? launch_dact<true, true>(p, grid, stream)
-                      : launch_dact<true, false>(p, grid, stream))
-               : (sum ? launch_dact<false, true>(p, grid, stream)
-                      : launch_dact<false, false>(p, grid, stream));
+  return gated ? (sum ? launch_dact_type<true, true>(p, grid, stream)
+                      : launch_dact_type<true, false>(p, grid, stream))
+               : (sum ? launch_dact_type<false, true>(p, grid, stream)
+                      : launch_dact_type<false, false>(p, grid, stream));
 }
 
 int ffn_dact_sums(const DactArgs& a, bool gated, bool late_wait, cudaStream_t stream) {

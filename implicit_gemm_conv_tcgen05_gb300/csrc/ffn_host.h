@@ -8,7 +8,13 @@ namespace igc {
 
 inline size_t elem_size(int dtype) { return dtype == IGC_F32 ? 4 : 2; }
 inline bool is_operand_type(int dtype) { return dtype == IGC_F16 || dtype == IGC_BF16; }
-inline bool fits32(int64_t v) { return v <= 0x7fffffff; }
+// Sizes that tile coordinates (up to a tile past the end) hold in 32 bits.
+inline bool fits32(int64_t v) { return v <= 0x7ffffe00; }
+// Whether an output pointer is one of the others (a null output is none).
+template <typename... P>
+bool is_any(const void* out, P... others) {
+  return out != nullptr && ((out == static_cast<const void*>(others)) || ...);
+}
 inline CUtensorMapDataType map_type(int dtype) {
   return dtype == IGC_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                           : (dtype == IGC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16

@@ -18,6 +18,9 @@ extern "C" int gated_ffn(int64_t M, int64_t F, int64_t K, int dtype, const void*
   if ((G == nullptr) != (U == nullptr) || (G != nullptr && ldgu < F)) return IGC_ERR_INVALID_ARG;
   if (K > 0 && (X == nullptr || Wg == nullptr || Wu == nullptr || ldx < K || ldw < K))
     return IGC_ERR_INVALID_ARG;
+  if (is_any(H, X, Wg, Wu, bg, bu, G, U) || is_any(G, X, Wg, Wu, bg, bu, U) ||
+      is_any(U, X, Wg, Wu, bg, bu))
+    return IGC_ERR_INVALID_ARG;  // outputs are no inputs
   if (!fits32(M) || !fits32(F) || !fits32(K)) return IGC_ERR_UNSUPPORTED;
   if (K > 0 && (!operand_ok(X, ldx) || !operand_ok(Wg, ldw) || !operand_ok(Wu, ldw)))
     return IGC_ERR_MISALIGNED;

@@ -16,6 +16,9 @@ extern "C" int linear_act(int64_t M, int64_t N, int64_t K, int dtype, const void
   if (Y == nullptr || ldy < N || (R != nullptr && ldr < N) || (Z != nullptr && ldz < N))
     return IGC_ERR_INVALID_ARG;
   if (K > 0 && (X == nullptr || W == nullptr || ldx < K || ldw < K)) return IGC_ERR_INVALID_ARG;
+  // outputs are no inputs; the residual may be Y itself, element for element
+  if (is_any(Y, X, W, bias, Z) || is_any(Z, X, W, bias, R)) return IGC_ERR_INVALID_ARG;
+  if (R == Y && (ldr != ldy || y_dtype != dtype)) return IGC_ERR_INVALID_ARG;
   if (!fits32(M) || !fits32(N) || !fits32(K)) return IGC_ERR_UNSUPPORTED;
   if (K > 0 && (!operand_ok(X, ldx) || !operand_ok(W, ldw))) return IGC_ERR_MISALIGNED;
 

@@ -14,8 +14,10 @@
  *    every other matrix and every vector may have any alignment and stride.
  *  - Sizes: any M, N, F, K >= 0 that fit 32 bits.  An empty output is a no-op.
  *    A contraction of length zero is an empty sum: zeros.
- *  - Aliasing: outputs must not overlap inputs or each other, with one exception:
- *    a residual may be the output itself (same pointer, type and row stride).
+ *  - Aliasing: outputs must not overlap inputs or each other (the kernels of a call
+ *    may run side by side), with one exception: a residual may be the output itself
+ *    (same pointer, type and row stride).  An output pointer that equals another
+ *    pointer of the call is refused; other overlaps are not detected.
  *  - Activations (z is fp32, c = sqrt(2 / pi)):
  *      IGC_ACT_NONE       z
  *      IGC_ACT_RELU       max(z, 0)                     derivative 0 at z = 0
@@ -151,10 +153,11 @@ int gated_ffn_backward(int64_t M, int64_t F, int64_t K, int dtype,
  *           the type and size of grads[t] and may be grads[t] itself (in place).
  *  norm     device fp32 scalar.
  *
- *  The three host arrays may be freed once the call has returned.  Squares and sums
- *  are fp32 (partial sums are joined in fp64).  A tensor with a NaN makes the norm
- *  and every output NaN; one with an infinity makes the norm infinite, every finite
- *  output 0 and the infinite ones NaN, as the formula has it.
+ *  The tensors must be distinct.  The host arrays may be freed once the call has
+ *  returned.  Squares and each thread's sums of them are fp32, what is joined after that
+ *  fp64: a value over 2^64 in magnitude makes the norm infinite, one under 2^-75 adds
+ *  nothing to it.  A NaN makes the norm and every output NaN; an infinite norm makes
+ *  every finite output 0 and the infinite ones NaN, as the formula has it.
  */
 size_t grad_norm_clip_workspace_size(int64_t count);
 int grad_norm_clip(int64_t count, const void *const *grads, const int64_t *sizes,

@@ -4,9 +4,10 @@ by their tests.
 Bounds.  u is the unit roundoff of the 16-bit type (2^-8 bf16, 2^-11 fp16; fp16 values
 below 2^-14 have spacing 2^-24).  A product sum of K terms in fp32 with truncating
 additions is off by at most gamma = (K + 8) 2^-23 of sum |x w|.  The activations use
-CUDA's fast exponential (2 + 1.173 |x| ulp), a fast division (2 ulp) and erff (2 ulp):
-their value is off by at most 1e-5 |z|, their derivative by at most 1e-5 (1 + |z|), where
-the sigmoid exceeds 1e-17; below that both are far under the other terms.  The slopes of
+approximate exponentials (2^-22, and |x| 2^-23 from the rounded argument), reciprocals
+(2^-23) and erff (2 ulp): their value is off by at most 1e-5 |z|, their derivative by at
+most 1e-5 (1 + |z|), where the sigmoid exceeds 1e-17; below that both are far under the
+other terms.  The slopes of
 the activations are at most 1.13.
 """
 
