@@ -114,12 +114,10 @@ inline void ffn_set_out(FfnParams& p, CUtensorMap* maps, int i, const Mat& m) {
   o.ptr = const_cast<void*>(m.ptr);
   o.ld = m.ld;
   o.f32 = m.dtype == IGC_F32;
-  o.vec = 0;
   o.tma = 0;
   if (m.ptr == nullptr) return;
   const size_t es = elem_size(m.dtype);
-  o.vec = rows_aligned(m.ptr, m.ld, es, 16);
-  if (o.vec)
+  if (rows_aligned(m.ptr, m.ld, es, 16))
     o.tma = encode_tiled_2d_fresh(&maps[i], map_type(m.dtype), m.ptr,
                                   static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M),
                                   static_cast<uint64_t>(m.ld) * es,

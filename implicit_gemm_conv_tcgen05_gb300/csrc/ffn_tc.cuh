@@ -70,7 +70,6 @@ struct FfnOut {
   long long ld;
   int f32;  // fp32 elements, else 16-bit
   int tma;  // written by bulk tensor stores
-  int vec;  // 16-byte aligned rows
 };
 
 struct FfnParams {
@@ -200,89 +199,112 @@ __device__ __forceinline__ void ffn_mma_stage(uint32_t d_tmem, uint64_t a_st, ui
 // epilogue: a warp owns 32 rows (a row per lane) and one box of 64 columns at a time
 // ---------------------------------------------------------------------------
 
-// Stores 64 columns of 16-bit results (packed pairs) of this lane's row.
-__device__ __forceinline__ void ffn_store_box16(const FfnOut& o, const CUtensorMap* map,
-                                                const Stager& st, int m, int n0,
-                                                const uint32_t (&v)[32]) {
-  if (o.tma) {
-    st.begin();
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      st.put(k, make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
-    st.issue(map, n0);
-    return;
-  }
-  if (m >= st.M) return;
-  uint16_t* row = static_cast<uint16_t*>(o.ptr) + static_cast<long long>(m) * o.ld + n0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (o.vec && n0 + 8 * k + 8 <= st.N) {
-      reinterpret_cast<uint4*>(row)[k] =
-          make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    } else {
-#pragma unroll
-      for (int i = 8 * k; i < 8 * k + 8; ++i)
-        if (n0 + i < st.N) row[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
-    }
-  }
+// Byte offset, in a warp's staging buffer, of 16-bit element c of row r (Stager::put's layout).
+__device__ __forceinline__ int ffn_staged(int r, int c) {
+  return r * 128 + ((((c >> 3) ^ (r & 7)) << 4) | ((c & 7) << 1));
 }
 
-// Stores 32 columns of fp32 results of this lane's row.
-__device__ __forceinline__ void ffn_store_box32(const FfnOut& o, const CUtensorMap* map,
-                                                const Stager& st, int m, int n0,
-                                                const float (&v)[32]) {
-  if (o.tma) {
-    st.begin();
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      st.put(k, make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
-                           __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3])));
-    st.issue(map, n0);
-    return;
-  }
-  if (m >= st.M) return;
-  float* row = static_cast<float*>(o.ptr) + static_cast<long long>(m) * o.ld + n0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (o.vec && n0 + 4 * k + 4 <= st.N) {
-      reinterpret_cast<float4*>(row)[k] =
-          make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+// Stores a box whose rows TMA cannot address, from the staging buffer: a row at a time, a
+// column per lane, so that a warp's stores fall into the few sectors of one row.  kWords:
+// fp32 (32 columns), else 16-bit (64 columns).
+template <bool kWords>
+__device__ __forceinline__ void ffn_store_rows(const FfnOut& o, const Stager& st, int n0) {
+  __syncwarp();
+  const int rows = min(32, st.M - st.row0);
+  for (int r = 0; r < rows; ++r) {
+    const long long at = static_cast<long long>(st.row0 + r) * o.ld + n0;
+    if constexpr (kWords) {
+      if (n0 + st.lane < st.N)
+        static_cast<float*>(o.ptr)[at + st.lane] =
+            *reinterpret_cast<const float*>(st.buf + ffn_staged(r, 2 * st.lane));
     } else {
 #pragma unroll
-      for (int i = 4 * k; i < 4 * k + 4; ++i)
-        if (n0 + i < st.N) row[i] = v[i];
+      for (int c = st.lane; c < kFfnBox; c += 32)
+        if (n0 + c < st.N)
+          static_cast<uint16_t*>(o.ptr)[at + c] =
+              *reinterpret_cast<const uint16_t*>(st.buf + ffn_staged(r, c));
     }
   }
+  __syncwarp();
+}
+
+// Stores one box: the 128 bytes of this lane's row (64 16-bit or 32 fp32 columns from n0).
+template <bool kWords>
+__device__ __forceinline__ void ffn_store_box(const FfnOut& o, const CUtensorMap* map,
+                                              const Stager& st, int n0, const uint32_t (&v)[32]) {
+  st.begin();
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    st.put(k, make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+  if (o.tma)
+    st.issue(map, n0);
+  else
+    ffn_store_rows<kWords>(o, st, n0);
 }
 
 // What a box's epilogue reads besides the accumulator, fetched before the accumulator is
 // waited for: the biases of columns n0 + lane and n0 + 32 + lane (broadcast by shuffles
-// later) and, where 16-byte loads can take it whole, this lane's row of the residual.
+// later) and this lane's row of the residual.
 struct FfnFetched {
   float bias0[2], bias1[2];
   uint4 res[8];
-  bool res_ok;
 };
 
+// The residual's box where 16-byte loads cannot take it (rows not 16-byte aligned, or
+// columns past N): a row at a time through the staging buffer, a column per lane.
+// (Loads of one element of every lane's own row, 64 of them, took 12 us more on
+// 3630 x 702 x 2944 fp16.)
+__device__ __forceinline__ void ffn_gather_residual(const FfnParams& p, const Stager& st, int n0,
+                                                    FfnFetched& f) {
+  st.begin();
+  const uint16_t* src = static_cast<const uint16_t*>(p.R);
+  const int rows = min(32, st.M - st.row0);
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    uint16_t e[8][2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = n0 + st.lane + 32 * h;
+        e[j][h] = r0 + j < rows && n < p.N
+                      ? src[static_cast<long long>(st.row0 + r0 + j) * p.ldr + n]
+                      : static_cast<uint16_t>(0);
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<uint16_t*>(st.buf + ffn_staged(r0 + j, st.lane + 32 * h)) = e[j][h];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    f.res[k] = *reinterpret_cast<const uint4*>(st.buf + ffn_staged(st.lane, 8 * k));
+  __syncwarp();
+}
+
 template <FfnOp kOp>
-__device__ __forceinline__ void ffn_fetch(const FfnParams& p, int m, int n0, int lane,
+__device__ __forceinline__ void ffn_fetch(const FfnParams& p, const Stager& st, int n0,
                                           FfnFetched& f) {
   if constexpr (kOp == FfnOp::Linear || kOp == FfnOp::Gated) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int n = n0 + 32 * c + lane;
+      const int n = n0 + 32 * c + st.lane;
       f.bias0[c] = n < p.N ? load_vec(p.bias0, n, p.bias_f32, p.bf16) : 0.0f;
       if constexpr (kOp == FfnOp::Gated)
         f.bias1[c] = n < p.N ? load_vec(p.bias1, n, p.bias_f32, p.bf16) : 0.0f;
     }
   }
   if constexpr (kOp == FfnOp::Linear) {
-    f.res_ok = p.R != nullptr && p.r_vec && m < p.M && n0 + kFfnBox <= p.N;
-    if (f.res_ok) {
+    if (p.R == nullptr) return;
+    if (p.r_vec && n0 + kFfnBox <= p.N) {
+      const int m = st.row0 + st.lane;
       const uint4* r = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(p.R) + static_cast<long long>(m) * p.ldr + n0);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f.res[k] = r[k];
+      for (int k = 0; k < 8; ++k) f.res[k] = m < p.M ? r[k] : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      ffn_gather_residual(p, st, n0, f);
     }
   }
 }
@@ -292,28 +314,19 @@ __device__ __forceinline__ void ffn_add_bias(float b, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
 }
 
-// v += R[m, n0 + 32 c .. + 31].
-__device__ __forceinline__ void ffn_add_residual(const FfnParams& p, const FfnFetched& f, int m,
-                                                 int n0, int c, float (&v)[32]) {
-  if (f.res_ok) {
+// v += the residual's columns n0 + 32 c .. + 31.
+__device__ __forceinline__ void ffn_add_residual(const FfnParams& p, const FfnFetched& f, int c,
+                                                 float (&v)[32]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint4 q = f.res[4 * c + k];
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  for (int k = 0; k < 4; ++k) {
+    const uint4 q = f.res[4 * c + k];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 e = unpack16(w[i], p.bf16);
-        v[8 * k + 2 * i] += e.x;
-        v[8 * k + 2 * i + 1] += e.y;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 e = unpack16(w[i], p.bf16);
+      v[8 * k + 2 * i] += e.x;
+      v[8 * k + 2 * i + 1] += e.y;
     }
-  } else if (p.R != nullptr && m < p.M) {
-    const int n = n0 + 32 * c;
-    const uint16_t* row =
-        static_cast<const uint16_t*>(p.R) + static_cast<long long>(m) * p.ldr + n;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (n + i < p.N) v[i] += load16(row, i, p.bf16);
   }
 }
 
@@ -336,7 +349,7 @@ template <FfnOp kOp>
 __device__ __forceinline__ void ffn_epilogue_box(const FfnParams& p, const CUtensorMap* tmO0,
                                                  const CUtensorMap* tmO1, const CUtensorMap* tmO2,
                                                  const Stager& st, uint32_t acc, int u_off,
-                                                 const FfnFetched& f, int m, int n0, int src) {
+                                                 const FfnFetched& f, int n0, int src) {
   const bool bf16 = p.bf16 != 0;
   if constexpr (kOp == FfnOp::Gated) {
     uint32_t h[32], gk[32], uk[32];
@@ -357,10 +370,10 @@ __device__ __forceinline__ void ffn_epilogue_box(const FfnParams& p, const CUten
       });
       ffn_pack(g, h + 16 * c, bf16);
     }
-    ffn_store_box16(p.out[0], tmO0, st, m, n0, h);
+    ffn_store_box<false>(p.out[0], tmO0, st, n0, h);
     if (p.out[1].ptr != nullptr) {
-      ffn_store_box16(p.out[1], tmO1, st, m, n0, gk);
-      ffn_store_box16(p.out[2], tmO2, st, m, n0, uk);
+      ffn_store_box<false>(p.out[1], tmO1, st, n0, gk);
+      ffn_store_box<false>(p.out[2], tmO2, st, n0, uk);
     }
   } else {
     // GradW's second matrix is written through slot 1
@@ -379,16 +392,20 @@ __device__ __forceinline__ void ffn_epilogue_box(const FfnParams& p, const CUten
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = act_f32<decltype(a)::value>(v[i]);
         });
-        ffn_add_residual(p, f, m, n0, c, v);
+        if (p.R != nullptr) ffn_add_residual(p, f, c, v);
       }
-      if (o.f32)
-        ffn_store_box32(o, map, st, m, n, v);
-      else
+      if (o.f32) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+        if (n < p.N) ffn_store_box<true>(o, map, st, n, w);
+      } else {
         ffn_pack(v, y + 16 * c, bf16);
+      }
     }
-    if (!o.f32) ffn_store_box16(o, map, st, m, n0, y);
+    if (!o.f32) ffn_store_box<false>(o, map, st, n0, y);
     if constexpr (kOp == FfnOp::Linear)
-      if (p.out[1].ptr != nullptr) ffn_store_box16(p.out[1], tmO1, st, m, n0, z);
+      if (p.out[1].ptr != nullptr) ffn_store_box<false>(p.out[1], tmO1, st, n0, z);
   }
 }
 
@@ -579,7 +596,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       const int src = kOp == FfnOp::GradW ? w.mb / p.tiles_m : 0;
       st.row0 = (w.mb - src * p.tiles_m) * BM + static_cast<int>(rank) * BM_CTA + quad * 32;
       FfnFetched f;
-      ffn_fetch<kOp>(p, st.row0 + lane, w.n0 + first_box * kFfnBox, lane, f);
+      ffn_fetch<kOp>(p, st, w.n0 + first_box * kFfnBox, f);
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, lim, abort_flag, p.status,
                                               kSiteEpiFull)))
         goto epi_done;
@@ -587,11 +604,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                              static_cast<uint32_t>(acc) * BN;
       for (int b = first_box; b < w.cols / kFfnBox && w.n0 + b * kFfnBox < p.N; b += 2) {
-        if (b != first_box)
-          ffn_fetch<kOp>(p, st.row0 + lane, w.n0 + b * kFfnBox, lane, f);
+        if (b != first_box) ffn_fetch<kOp>(p, st, w.n0 + b * kFfnBox, f);
         ffn_epilogue_box<kOp>(p, &tmO0, &tmO1, &tmO2, st,
                               taddr + static_cast<uint32_t>(b * kFfnBox), w.cols, f,
-                              st.row0 + lane, w.n0 + b * kFfnBox, src);
+                              w.n0 + b * kFfnBox, src);
       }
       tc_fence_before();
       __syncwarp();
