@@ -603,13 +603,18 @@ def _check_device(dev, name):
     """The device that all tensors of a call are on must be the current CUDA device."""
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != _torch().cuda.current_device():
+    if dev != _torch()._C._cuda_getDevice():
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
 
 
 def _torch():
     import torch
     return torch
+
+
+def _handle(stream, dev):
+    """The cudaStream_t handle of `stream`, or of device dev's current stream."""
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _new(shape, dtype, device, stream):
@@ -648,7 +653,8 @@ def _workspace(workspace, need, like, stream):
     if stream is not None or need > _KEPT_WORKSPACE_BYTES or \
             torch.cuda.is_current_stream_capturing():
         return _new((need,), torch.uint8, like.device, stream)
-    key = (like.get_device(), _stream(None))
+    dev = like.get_device()
+    key = (dev, _handle(None, dev))
     kept = _kept.__dict__.get(key)
     if kept is None or kept.numel() < need:
         kept = _kept.__dict__[key] = _new((need,), torch.uint8, like.device, None)
@@ -678,7 +684,8 @@ def linear_act(X, W, bias=None, act="none", residual=None, Y=None, Z=None, strea
         Y = _new((M, N), dtype, X.device, stream)
         y, ldy = Y.data_ptr(), N
     _check(lib().linear_act(M, N, K, dt, x, ldx, w, ldw, b, bt, code, r, ldr, z, ldz, y, ldy,
-                            dt if Y.dtype is dtype else IGC_F32, _stream(stream)), "linear_act")
+                            dt if Y.dtype is dtype else IGC_F32, _handle(stream, dev)),
+           "linear_act")
     return Y
 
 
@@ -721,7 +728,7 @@ def linear_act_backward(dY, X, W, act="none", Z=None, dX=None, dW=None, dbias=No
     ws = _workspace(workspace, L.linear_act_backward_workspace_size(M, N, K), dY, stream)
     _check(L.linear_act_backward(M, N, K, dt, dy, lddy, z, ldz, code, x, ldx, w, ldw, dx, lddx,
                                  dw, lddw, IGC_F32 if dW is None else _dtype_code(dW.dtype), db,
-                                 bt, ws.data_ptr(), ws.numel(), _stream(stream)),
+                                 bt, ws.data_ptr(), ws.numel(), _handle(stream, dev)),
            "linear_act_backward")
     return dX, dW, dbias
 
@@ -762,7 +769,7 @@ def gated_ffn(X, Wg, Wu, bg=None, bu=None, act="silu", H=None, G=None, U=None, s
         H = _new((M, F), dtype, X.device, stream)
         h, ldh = H.data_ptr(), F
     _check(lib().gated_ffn(M, F, K, dt, x, ldx, wg, wu, ldw, b0, b1, bt0 if bg is not None else bt1,
-                           code, g, u, ldg, h, ldh, _stream(stream)), "gated_ffn")
+                           code, g, u, ldg, h, ldh, _handle(stream, dev)), "gated_ffn")
     return H
 
 
@@ -818,7 +825,7 @@ def gated_ffn_backward(dH, G, U, X, Wg, Wu, act="silu", dX=None, dWg=None, dWu=N
     _check(L.gated_ffn_backward(M, F, K, dt, dh, lddh, g, u, ldg, code, x, ldx, wg, wu, ldw, dx,
                                 lddx, dwg, dwu, lddw,
                                 IGC_F32 if dWg is None else _dtype_code(dWg.dtype), b0, b1, bt,
-                                ws.data_ptr(), ws.numel(), _stream(stream)),
+                                ws.data_ptr(), ws.numel(), _handle(stream, dev)),
            "gated_ffn_backward")
     return dX, dWg, dWu, dbg, dbu
 
@@ -879,12 +886,13 @@ def grad_norm_clip(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=Non
     device = grads[0].device if n else (norm.device if norm is not None else "cuda")
     if norm is None:
         norm = _new((), torch.float32, device, stream)
-    if n and norm.get_device() != grads[0].get_device():
+    dev = norm.get_device()
+    if n and dev not in devices:
         raise ValueError("norm is on another device")
-    _check_device(norm.get_device(), "norm")
+    _check_device(dev, "norm")
     ws = _workspace(workspace, grad_norm_clip_workspace_size(n), norm, stream)
     rc = lib().grad_norm_clip(n, g_ptr, sizes.buffer_info()[0], codes.buffer_info()[0], o_ptr,
                               float(max_norm), float(eps), norm.data_ptr(), ws.data_ptr(),
-                              ws.numel(), _stream(stream))
+                              ws.numel(), _handle(stream, dev))
     _check(rc, "grad_norm_clip")
     return norm

@@ -69,7 +69,8 @@ struct DactArgs {
 };
 int64_t dact_chunks(int64_t M, int64_t N);
 int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream);
-// The bias gradients from the partial sums that ffn_dact left.
+// The bias gradients from the partial sums that ffn_dact left (up to 512 rows it has
+// written them already, and nothing is launched).
 int ffn_dact_sums(const DactArgs& a, bool gated, bool late_wait, cudaStream_t stream);
 
 }  // namespace igc
