@@ -831,12 +831,12 @@ def gated_ffn_backward(dH, G, U, X, Wg, Wu, act="silu", dX=None, dWg=None, dWu=N
 
 
 PLAN_FFN_LINEAR, PLAN_FFN_GATED, PLAN_FFN_GRAD_X, PLAN_FFN_GRAD_W = 0, 1, 2, 3
-_PLAN_FFN_FIELDS = ("small", "rows", "row_blocks", "split", "small_ns", "tiles_ns")
+_PLAN_FFN_FIELDS = ("small", "rows", "row_blocks", "columns", "split", "small_ns", "tiles_ns")
 
 
 def igc_plan_ffn(op: int, M: int, N: int, K: int, count: int = 1, sms: int = 152) -> dict:
     """The schedule that a feed-forward product runs with (see include/igc_ffn.h)."""
-    out = (ctypes.c_int32 * 6)()
+    out = (ctypes.c_int32 * 7)()
     _check(lib().igc_plan_ffn(int(op), int(M), int(N), int(K), int(count), int(sms), out),
            "igc_plan_ffn")
     return dict(zip(_PLAN_FFN_FIELDS, (int(v) for v in out)))

@@ -278,7 +278,7 @@ int igc_check_device_status(igc_stream_t stream) {
 uint64_t igc_last_device_status(void) { return igc::g_last_status.load(); }
 
 int igc_set_tile_width(int bn) {
-  if (bn != 0 && bn != 128 && bn != 224 && bn != 256) return -1;
+  if (bn != 0 && bn != 128 && bn != 192 && bn != 224 && bn != 256) return -1;
   const int old = igc::t_tile_width;
   igc::t_tile_width = bn;
   return old;

@@ -54,18 +54,6 @@ int ffn_kernel_setup(const DeviceInfo& dev, int* max_clusters) {
   return rc[d];
 }
 
-// Estimated time of the schedule at tile width bn (in units of one 256-wide tile):
-// rounds over the CTA pairs, a last round of column halves counting one half, times
-// the width over its relative rate (kBnEff's measurements).
-inline double ffn_cost(long long tiles_m, long long N, int out_n, bool halves, double eff,
-                       int clusters) {
-  const long long tiles = tiles_m * ((N + out_n - 1) / out_n);
-  const long long rem = tiles % clusters;
-  const double rounds = static_cast<double>(tiles / clusters) +
-                        (rem == 0 ? 0.0 : (halves && 2 * rem <= clusters ? 0.5 : 1.0));
-  return rounds * out_n / eff;
-}
-
 template <FfnOp kOp, int BN>
 int ffn_launch_bn(const DeviceInfo& dev, const FfnOperands& ops, const CUtensorMap* out_maps,
                   FfnParams p, cudaStream_t stream) {
@@ -160,46 +148,6 @@ inline int ffn_map_b(CUtensorMap* map, const FfnProblem& q, int i, bool mn, int 
             : ffn_operand_map(map, q.dtype, q.B[i], q.N, q.K, box_rows);
 }
 
-// 256-row tiles: chooses the tile width, encodes the maps and launches.
-template <FfnOp kOp>
-int ffn_launch_tiles(const DeviceInfo& dev, const FfnProblem& q, int clusters,
-                     cudaStream_t stream) {
-  FfnParams p = {};
-  p.M = static_cast<int>(q.M), p.N = static_cast<int>(q.N);
-  p.kb_seg = static_cast<int>((q.K + kFfnKS - 1) / kFfnKS);
-  p.segs = q.segs, p.srcs = q.srcs;
-  p.late_wait = q.late_wait;
-  p.bf16 = q.dtype == IGC_BF16;
-  p.act = q.act;
-  p.bias0 = q.bias[0], p.bias1 = q.bias[1], p.bias_f32 = q.bias_dtype == IGC_F32;
-  p.R = q.R.ptr, p.ldr = q.R.ld, p.r_vec = rows_aligned(q.R.ptr, q.R.ld, 2, 16);
-  const long long tm = (static_cast<long long>(p.M) + BM - 1) / BM * p.srcs;
-  const int wide = FfnCfg<kOp, 256>::kOutN, narrow = FfnCfg<kOp, 128>::kOutN;
-  int bn = ffn_cost(tm, p.N, wide, true, kBnEff[0], clusters) <=
-                   ffn_cost(tm, p.N, narrow, false, kBnEff[2], clusters)
-               ? 256
-               : 128;
-  bn = tile_width_override() == 128 || tile_width_override() == 256 ? tile_width_override() : bn;
-  FfnOperands ops = {};
-  int rc = IGC_OK;
-  for (int i = 0; i < q.count_a && rc == IGC_OK; ++i)
-    rc = ffn_map_a(&ops.a[i], q, i, ffn_a_mn(kOp), ffn_a_mn(kOp) ? kFfnKS : BM_CTA);
-  for (int i = 0; i < q.count_b && rc == IGC_OK; ++i)
-    rc = ffn_map_b(&ops.b[i], q, i, ffn_b_mn(kOp), ffn_b_mn(kOp) ? kFfnKS : bn / 4);
-  if (rc != IGC_OK) return rc;
-  CUtensorMap out_maps[3] = {};
-  for (int i = 0; i < 3; ++i) ffn_set_out(p, out_maps, i, q.out[i]);
-  return bn == 256 ? ffn_launch_bn<kOp, 256>(dev, ops, out_maps, p, stream)
-                   : ffn_launch_bn<kOp, 128>(dev, ops, out_maps, p, stream);
-}
-
-// ---------------------------------------------------------------------------
-// small outputs: 128-column blocks shared by clusters that split k
-// ---------------------------------------------------------------------------
-constexpr size_t kSmallSmemTwo = 110 * 1024;  // two CTAs on an SM
-constexpr size_t kSmallSmemOne = 224 * 1024;
-constexpr size_t kSmemPerSm = 228 * 1024;
-
 // Estimated times in microseconds, for choosing between schedules (measured on GB300: a
 // CTA takes in about 65 bytes a nanosecond through TMA, two on an SM 95 together, one with
 // twice the stages 85; an SM reads about 40 from the shared memory of the other CTAs of
@@ -215,6 +163,89 @@ double operand_bytes(const FfnProblem& q) {
          (static_cast<double>(q.N) * (kOp == FfnOp::Gated ? 2 : 1) +
           static_cast<double>(q.M) * q.srcs);
 }
+
+// The tile width of a problem and the estimated time of its schedule: rounds over the CTA
+// pairs, each as long as a 128-deep stage's MMAs (0.6 us at 256 columns; narrower tiles run
+// at 0.88 and 0.83 of the rate) or its operands' way into an SM: about 165 bytes a nanosecond
+// (the large boxes of this kernel), half of that where rows do not start on 128-byte lines.
+// At 256 a last round that fills at most half of the pairs runs as column halves, 0.53 of a
+// whole one.
+struct TilePlan {
+  int bn = 256;
+  double us = 1e30;
+};
+
+template <FfnOp kOp>
+TilePlan tile_plan(const FfnProblem& q, int clusters) {
+  bool lines = true;
+  for (int i = 0; i < q.count_a; ++i) lines = lines && rows_aligned(q.A[i].ptr, q.A[i].ld, 2, 128);
+  for (int i = 0; i < q.count_b; ++i) lines = lines && rows_aligned(q.B[i].ptr, q.B[i].ld, 2, 128);
+  const double rate = lines ? 165e3 : 82e3;
+  const double stages = static_cast<double>((q.K + kFfnKS - 1) / kFfnKS) * q.segs;
+  const long long tiles_m = (q.M + BM - 1) / BM * q.srcs;
+  constexpr int kWidths[] = {256, 192, 128};
+  constexpr double kEff[] = {1.0, 0.88, 0.83};
+  // 192 is built for linear_act alone: half of it is no whole number of epilogue boxes
+  // (Gated) or of MN-major groups (the gradients, which would load a quarter more)
+  auto built = [](int bn) { return bn != 192 || kOp == FfnOp::Linear; };
+  const int width = tile_width_override();
+  const bool forced = width == 256 || width == 128 || (width == 192 && built(192));
+  TilePlan best;
+  for (int i = 0; i < 3; ++i) {
+    const int bn = kWidths[i], out_n = kOp == FfnOp::Gated ? bn / 2 : bn;
+    if (!built(bn) || (forced && bn != width)) continue;
+    const long long tiles = tiles_m * ((q.N + out_n - 1) / out_n);
+    const long long full = tiles / clusters, rem = tiles % clusters;
+    const bool halves = bn == 256 && rem > 0 && 2 * rem <= clusters;
+    const double whole = std::max(0.6 * bn / 256 / kEff[i], (32768.0 + 128.0 * bn) / rate);
+    const double half = std::max(0.32, 49152.0 / rate);
+    const double busy = stages * (static_cast<double>(full) * whole +
+                                  (rem == 0 ? 0.0 : (halves ? half : whole)));
+    // streaming from DRAM takes CTAs: about 35 bytes a nanosecond each
+    const double pairs = full > 0 ? clusters : static_cast<double>(halves ? 2 * rem : rem);
+    const double dram = operand_bytes<kOp>(q) / std::min(kDramRate, 2.0 * pairs * 35e3);
+    const double us = kUsFixed + 1.0 + std::max(busy, dram);
+    if (us < best.us * 0.999) {
+      best.bn = bn;
+      best.us = us;
+    }
+  }
+  return best;
+}
+
+// 256-row tiles: encodes the maps and launches.
+template <FfnOp kOp>
+int ffn_launch_tiles(const DeviceInfo& dev, const FfnProblem& q, int bn, cudaStream_t stream) {
+  FfnParams p = {};
+  p.M = static_cast<int>(q.M), p.N = static_cast<int>(q.N);
+  p.kb_seg = static_cast<int>((q.K + kFfnKS - 1) / kFfnKS);
+  p.segs = q.segs, p.srcs = q.srcs;
+  p.late_wait = q.late_wait;
+  p.bf16 = q.dtype == IGC_BF16;
+  p.act = q.act;
+  p.bias0 = q.bias[0], p.bias1 = q.bias[1], p.bias_f32 = q.bias_dtype == IGC_F32;
+  p.R = q.R.ptr, p.ldr = q.R.ld, p.r_vec = rows_aligned(q.R.ptr, q.R.ld, 2, 16);
+  FfnOperands ops = {};
+  int rc = IGC_OK;
+  for (int i = 0; i < q.count_a && rc == IGC_OK; ++i)
+    rc = ffn_map_a(&ops.a[i], q, i, ffn_a_mn(kOp), ffn_a_mn(kOp) ? kFfnKS : BM_CTA);
+  for (int i = 0; i < q.count_b && rc == IGC_OK; ++i)
+    rc = ffn_map_b(&ops.b[i], q, i, ffn_b_mn(kOp), ffn_b_mn(kOp) ? kFfnKS : bn / 4);
+  if (rc != IGC_OK) return rc;
+  CUtensorMap out_maps[3] = {};
+  for (int i = 0; i < 3; ++i) ffn_set_out(p, out_maps, i, q.out[i]);
+  if constexpr (kOp == FfnOp::Linear)
+    if (bn == 192) return ffn_launch_bn<kOp, 192>(dev, ops, out_maps, p, stream);
+  return bn == 256 ? ffn_launch_bn<kOp, 256>(dev, ops, out_maps, p, stream)
+                   : ffn_launch_bn<kOp, 128>(dev, ops, out_maps, p, stream);
+}
+
+// ---------------------------------------------------------------------------
+// small outputs: 128-column blocks shared by clusters that split k
+// ---------------------------------------------------------------------------
+constexpr size_t kSmallSmemTwo = 110 * 1024;  // two CTAs on an SM
+constexpr size_t kSmallSmemOne = 224 * 1024;
+constexpr size_t kSmemPerSm = 228 * 1024;
 
 struct SmallPlan {
   int m_blocks = 1, mt = 16, split = 1;
@@ -276,29 +307,6 @@ SmallPlan small_plan(const FfnProblem& q, int sms) {
     }
   }
   return best;
-}
-
-// The same estimate for the 256-row tiles: rounds of the schedule, each 128-deep stage as
-// long as its MMAs or its operands' way into an SM: about 165 bytes a nanosecond (the
-// large boxes of this kernel), half of that where rows do not start on 128-byte lines.
-template <FfnOp kOp>
-double tiles_us(const FfnProblem& q, int clusters) {
-  const int out_n = FfnCfg<kOp, 256>::kOutN;
-  const long long tiles = (q.M + BM - 1) / BM * q.srcs * ((q.N + out_n - 1) / out_n);
-  const long long full = tiles / clusters, rem = tiles % clusters;
-  bool lines = true;
-  for (int i = 0; i < q.count_a; ++i) lines = lines && rows_aligned(q.A[i].ptr, q.A[i].ld, 2, 128);
-  for (int i = 0; i < q.count_b; ++i) lines = lines && rows_aligned(q.B[i].ptr, q.B[i].ld, 2, 128);
-  const double rate = lines ? 165e3 : 82e3;
-  const double whole = std::max(0.53, 65536 / rate), half = std::max(0.27, 49152 / rate);
-  const double stages = static_cast<double>((q.K + kFfnKS - 1) / kFfnKS) * q.segs;
-  const bool halves = rem > 0 && 2 * rem <= clusters;
-  const double busy = stages * (static_cast<double>(full) * whole +
-                                (rem == 0 ? 0.0 : (halves ? half : whole)));
-  // streaming from DRAM takes CTAs: about 35 bytes a nanosecond each
-  const double pairs = full > 0 ? clusters : static_cast<double>(halves ? 2 * rem : rem);
-  const double dram = operand_bytes<kOp>(q) / std::min(kDramRate, 2.0 * pairs * 35e3);
-  return kUsFixed + 1.0 + std::max(busy, dram);
 }
 
 template <FfnOp kOp>
@@ -392,9 +400,8 @@ int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const SmallPlan
 
 // Which of the two kernels runs a problem: the one with the shorter estimate, unless the
 // calling thread forced a tile width (igc_set_tile_width).
-template <FfnOp kOp>
-bool ffn_takes_small(const FfnProblem& q, const SmallPlan& plan, int clusters) {
-  return plan.us < tiles_us<kOp>(q, clusters) && tile_width_override() == 0;
+inline bool ffn_takes_small(const SmallPlan& small, const TilePlan& tiles) {
+  return small.us < tiles.us && tile_width_override() == 0;
 }
 
 template <FfnOp kOp>
@@ -402,22 +409,25 @@ int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, cudaStream_t stream) 
   int clusters = 0;
   const int rc = ffn_kernel_setup<kOp, 256>(dev, &clusters);
   if (rc != IGC_OK) return rc;
-  const SmallPlan plan = small_plan<kOp>(q, dev.sm_count);
-  return ffn_takes_small<kOp>(q, plan, clusters) ? ffn_launch_small<kOp>(dev, q, plan, stream)
-                                                 : ffn_launch_tiles<kOp>(dev, q, clusters, stream);
+  const SmallPlan small = small_plan<kOp>(q, dev.sm_count);
+  const TilePlan tiles = tile_plan<kOp>(q, clusters);
+  return ffn_takes_small(small, tiles) ? ffn_launch_small<kOp>(dev, q, small, stream)
+                                       : ffn_launch_tiles<kOp>(dev, q, tiles.bn, stream);
 }
 
 // igc_plan_ffn for one product (see igc_ffn.h).
 template <FfnOp kOp>
 void ffn_plan(const FfnProblem& q, int sms, int32_t* out) {
-  const SmallPlan plan = small_plan<kOp>(q, sms);
-  const bool small = ffn_takes_small<kOp>(q, plan, sms / 2);
-  out[0] = small;
-  out[1] = small ? plan.mt : BM;
-  out[2] = small ? plan.m_blocks : static_cast<int32_t>((q.M + BM - 1) / BM);
-  out[3] = small ? plan.split : 1;
-  out[4] = static_cast<int32_t>(plan.us * 1000);
-  out[5] = static_cast<int32_t>(tiles_us<kOp>(q, sms / 2) * 1000);
+  const SmallPlan small = small_plan<kOp>(q, sms);
+  const TilePlan tiles = tile_plan<kOp>(q, sms / 2);
+  const bool is_small = ffn_takes_small(small, tiles);
+  out[0] = is_small;
+  out[1] = is_small ? small.mt : BM;
+  out[2] = is_small ? small.m_blocks : static_cast<int32_t>((q.M + BM - 1) / BM);
+  out[3] = is_small ? kSkRows : tiles.bn;
+  out[4] = is_small ? small.split : 1;
+  out[5] = static_cast<int32_t>(std::min(small.us * 1000, 2e9));
+  out[6] = static_cast<int32_t>(std::min(tiles.us * 1000, 2e9));
 }
 
 }  // namespace igc

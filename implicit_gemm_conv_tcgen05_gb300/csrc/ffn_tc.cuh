@@ -49,9 +49,11 @@ constexpr int kFfnBox = 64;  // columns of one epilogue box (128 bytes of a 16-b
 
 template <FfnOp kOp, int BN>
 struct FfnCfg {
-  static_assert(BN == 256 || BN == 128, "BN");
   static constexpr int kOutN = kOp == FfnOp::Gated ? BN / 2 : BN;  // output columns of a tile
+  static_assert(BN % 64 == 0 && BN <= 256 && kOutN % kFfnBox == 0, "BN");
   static constexpr uint32_t kStageA = kAtomABytes * kFfnAtoms;
+  // MN-major atoms hold a CTA's BN/2 rows of B in groups of 64
+  static_assert(!ffn_b_mn(kOp) || BN % 128 == 0, "BN");
   static constexpr uint32_t kAtomB = BN / 2 * BK * 2;
   static constexpr uint32_t kStageB = kAtomB * kFfnAtoms;
   static constexpr uint32_t kStageBytes = kStageA + kStageB;
@@ -60,7 +62,8 @@ struct FfnCfg {
           ? 8
           : static_cast<int>((kSmemBudget - 2048 - kStagingBytes) / kStageBytes);
   static constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + 1024;
-  static constexpr uint32_t kTmemCols = 2 * BN;
+  static constexpr uint32_t kAccStride = BN <= 128 ? 128 : 256;  // columns of an accumulator
+  static constexpr uint32_t kTmemCols = 2 * kAccStride;
   static constexpr bool kHalves = BN == 256;  // column-half units in the last round
 };
 
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         tc_fence_after();
         if (lane == 0) {
           ffn_mma_stage<kOp, BN>(
-              tmem_base + static_cast<uint32_t>(acc) * BN,
+              tmem_base + static_cast<uint32_t>(acc) * Cfg::kAccStride,
               adesc0 + ((static_cast<uint32_t>(stage) * Cfg::kStageA) >> 4),
               bdesc0 + ((static_cast<uint32_t>(stage) * Cfg::kStageB) >> 4), idesc, kb > 0);
           umma_commit_2cta_multicast(&empty[stage], 0x3);
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         goto epi_done;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                             static_cast<uint32_t>(acc) * BN;
+                             static_cast<uint32_t>(acc) * Cfg::kAccStride;
       for (int b = first_box; b < w.cols / kFfnBox && w.n0 + b * kFfnBox < p.N; b += 2) {
         if (b != first_box) ffn_fetch<kOp>(p, st, w.n0 + b * kFfnBox, f);
         ffn_epilogue_box<kOp>(p, &tmO0, &tmO1, &tmO2, st,

@@ -26,9 +26,9 @@ def generator(*key):
     return torch.Generator(device="cuda").manual_seed(abs(hash(key)) % (1 << 31))
 
 
-@pytest.fixture(params=[0, 128, 256], ids=["auto", "tiles128", "tiles256"])
+@pytest.fixture(params=[0, 128, 192, 256], ids=["auto", "tiles128", "tiles192", "tiles256"])
 def width(request):
-    """The schedule chosen per problem, and the 256-row tiles of either width forced."""
+    """The schedule chosen per problem, and the 256-row tiles of each width forced."""
     igc.igc_set_tile_width(request.param)
     yield request.param
     igc.igc_set_tile_width(0)
@@ -235,7 +235,7 @@ def test_backward_small_integers_bit_exact(dtype):
         return torch.randint(-2, 3, (r, c), generator=gen, device="cuda").to(dtype)
 
     x, w, dy = ints(M, K), ints(N, K), ints(M, N)
-    for width in (0, 128, 256):
+    for width in (0, 128, 192, 256):
         dX = torch.empty((M, K), device="cuda", dtype=dtype)
         dW = torch.empty((N, K), device="cuda", dtype=F32)
         db = torch.empty(N, device="cuda")
