@@ -2,7 +2,7 @@
 
     python -m implicit_gemm_conv_tcgen05_gb300.build [--force] [--ptxas-verbose]
 
-Each .cu translation unit under csrc/ is compiled in parallel to an object
+Each .cu translation unit under csrc/ and csrc/ffn/ is compiled in parallel to an object
 file, then linked into _build/libigc.so (CUDA runtime linked statically, so
 the library loads without a GPU; the driver API is reached through the
 runtime's driver entry point).  No GPU is needed to build.
@@ -20,13 +20,14 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+FFN = os.path.join(CSRC, "ffn")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libigc.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
-                     "-I" + INCLUDE, "-I" + CSRC]
+                     "-I" + INCLUDE, "-I" + CSRC, "-I" + FFN]
 
 
 def _nvcc() -> str:
@@ -37,13 +38,13 @@ def _nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(FFN, "*.cu")))
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + \
-        [os.path.abspath(__file__)]
+    headers = [h for d in (CSRC, FFN, INCLUDE) for pat in ("*.cuh", "*.h")
+               for h in glob.glob(os.path.join(d, pat))]
+    return _sources() + headers + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
@@ -54,7 +55,7 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
-    """Compile every csrc/*.cu and link _build/libigc.so; returns its path."""
+    """Compile every csrc/*.cu and csrc/ffn/*.cu and link _build/libigc.so; returns its path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

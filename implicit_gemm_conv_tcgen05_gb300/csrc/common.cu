@@ -200,23 +200,6 @@ int encode_tiled_2d_swizzle(CUtensorMap* map, CUtensorMapDataType dtype, const v
   return IGC_OK;
 }
 
-int encode_tiled_2d_fresh(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
-                          uint64_t inner, uint64_t rows, uint64_t row_stride_bytes,
-                          uint32_t box_inner, uint32_t box_rows) {
-  load_encoders();
-  if (!g_encode_tiled) return IGC_ERR_CUDA;
-  cuuint64_t dims[2] = {inner, rows};
-  cuuint64_t strides[1] = {row_stride_bytes};
-  cuuint32_t box[2] = {box_inner, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return g_encode_tiled(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? IGC_OK
-             : IGC_ERR_CUDA;
-}
-
 int encode_im2col_nhwc(CUtensorMap* map, const void* base, int N, int H, int W, int C,
                        int lower_h, int lower_w, int upper_h, int upper_w, uint32_t channels,
                        uint32_t pixels, int stride_h, int stride_w) {
@@ -278,7 +261,7 @@ int igc_check_device_status(igc_stream_t stream) {
 uint64_t igc_last_device_status(void) { return igc::g_last_status.load(); }
 
 int igc_set_tile_width(int bn) {
-  if (bn != 0 && bn != 128 && bn != 192 && bn != 224 && bn != 256) return -1;
+  if (bn != 0 && bn != 128 && bn != 224 && bn != 256) return -1;
   const int old = igc::t_tile_width;
   igc::t_tile_width = bn;
   return old;

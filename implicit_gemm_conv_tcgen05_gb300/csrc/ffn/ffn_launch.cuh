@@ -189,7 +189,7 @@ TilePlan tile_plan(const FfnProblem& q, int clusters) {
   // (Gated) or of MN-major groups (the gradients, which would load a quarter more)
   auto built = [](int bn) { return bn != 192 || kOp == FfnOp::Linear; };
   const int width = tile_width_override();
-  const bool forced = width == 256 || width == 128 || (width == 192 && built(192));
+  const bool forced = width == 256 || width == 128;
   TilePlan best;
   for (int i = 0; i < 3; ++i) {
     const int bn = kWidths[i], out_n = kOp == FfnOp::Gated ? bn / 2 : bn;

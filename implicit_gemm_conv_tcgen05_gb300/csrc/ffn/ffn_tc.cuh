@@ -31,6 +31,7 @@
 #pragma once
 
 #include "ffn_act.cuh"
+#include "ffn_ptx.cuh"
 #include "gemm_tc.cuh"
 
 namespace igc {
@@ -96,19 +97,6 @@ struct FfnParams {
   unsigned long long wait_limit_ns;
   unsigned long long* status;
 };
-
-// Matrix descriptor of an MN-major operand tile written by TMA with 128-byte
-// swizzling: rows (one k each) of 64 outputs, 8-k groups 1024 bytes apart, groups of
-// 64 outputs lbo bytes apart (fields as for make_sw128_kmajor_desc).
-__device__ __forceinline__ uint64_t make_sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
 
 // Programmatic dependent launch.  A kernel normally waits for the one before it in the
 // stream (kernel B) before it touches memory.  With `late` it shares no memory with B

@@ -22,10 +22,9 @@ extern "C" {
 /*
  * Tuning and test hook: the output tile width (columns of B per CTA pair) of
  * every GEMM / convolution launched after this call.  0 (the default) picks it
- * per problem; 128, 192, 224 or 256 force it where the operation is built for it
- * (the integer paths have 128 and 256, the feed-forward products of igc_ffn.h 128
- * and 256 and linear_act 192 too, and any forced width takes them to their 256-row
- * tiles; a width an operation lacks is ignored for it).  Results do not depend on the width beyond fp32 rounding order
+ * per problem; 128, 224 or 256 force it where the operation is built for it
+ * (the integer paths have 128 and 256; a width an operation lacks is ignored
+ * for it).  Results do not depend on the width beyond fp32 rounding order
  * (integer results are identical).  Returns the previous setting, or -1 (and
  * changes nothing) for any other value.  Thread-local: it applies to the calls
  * of the thread that set it and to no other thread's.

@@ -28,6 +28,10 @@
  *    *_workspace_size function gives, not shared with a concurrent call; nothing
  *    in one need survive between calls.
  *  - Results do not vary from run to run: every sum has a fixed order.
+ *  - Schedule: each product runs on 256-row tiles or, for few rows or small outputs, on
+ *    the kernel for those, whichever is estimated to be done sooner (igc_plan_ffn).  A
+ *    width set through igc_set_tile_width (igc_debug.h) takes the calling thread's later
+ *    products to the 256-row tiles, 128 or 256 columns wide where it is one of these.
  */
 #ifndef IGC_FFN_H
 #define IGC_FFN_H

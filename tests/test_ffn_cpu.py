@@ -222,7 +222,8 @@ def test_plans():
     assert igc.igc_plan_ffn(gw, 64, 100, 100)["rows"] % 64 == 0
     # 15 x 3 tiles of 256 columns and 15 x 4 of 192 are one round on 76 pairs either way:
     # the narrower ones are done sooner; many rounds take the wider ones
-    assert igc.igc_plan_ffn(lin, 3630, 702, 2944)["columns"] == 192
+    for shape in ((3630, 702, 2944), (2000, 1300, 200), (1800, 1501, 264)):
+        assert igc.igc_plan_ffn(lin, *shape)["columns"] == 192
     assert igc.igc_plan_ffn(lin, 8192, 8192, 8192)["columns"] == 256
     # a forced tile width is always the tiles
     igc.igc_set_tile_width(128)

@@ -83,7 +83,7 @@ def test_forward_small_integers_bit_exact(M):
     gen = generator(M, 32)
     x, wg, wu = (torch.randint(-2, 3, (n, K), generator=gen, device="cuda").to(BF16)
                  for n in (M, F, F))
-    for width in (0, 128, 192, 256):
+    for width in (0, 128, 256):
         G, U = (torch.empty((M, F), device="cuda", dtype=BF16) for _ in range(2))
         igc.igc_set_tile_width(width)
         try:

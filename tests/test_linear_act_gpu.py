@@ -26,9 +26,9 @@ def generator(*key):
     return torch.Generator(device="cuda").manual_seed(abs(hash(key)) % (1 << 31))
 
 
-@pytest.fixture(params=[0, 128, 192, 256], ids=["auto", "tiles128", "tiles192", "tiles256"])
+@pytest.fixture(params=[0, 128, 256], ids=["auto", "tiles128", "tiles256"])
 def width(request):
-    """The schedule chosen per problem, and the 256-row tiles of each width forced."""
+    """The schedule chosen per problem, and the 256-row tiles of either width forced."""
     igc.igc_set_tile_width(request.param)
     yield request.param
     igc.igc_set_tile_width(0)
@@ -50,7 +50,8 @@ def make(M, N, K, dtype, bias, residual, seed, pad=0):
 SHAPES = [(1, 1, 1), (1, 64, 64), (1, 1000, 777), (2, 5, 8), (3, 129, 200), (15, 128, 1024),
           (16, 64, 4096), (17, 300, 72), (64, 640, 520), (127, 257, 130), (128, 384, 2048),
           (129, 300, 72), (200, 1, 64), (256, 256, 256), (257, 513, 1000), (333, 1000, 2056),
-          (640, 2304, 192), (1, 20000, 64), (5, 256, 16384)]
+          (640, 2304, 192), (1, 20000, 64), (5, 256, 16384),
+          (2000, 1300, 200), (1800, 1501, 264)]   # the last two take 192-wide tiles
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
@@ -235,7 +236,7 @@ def test_backward_small_integers_bit_exact(dtype):
         return torch.randint(-2, 3, (r, c), generator=gen, device="cuda").to(dtype)
 
     x, w, dy = ints(M, K), ints(N, K), ints(M, N)
-    for width in (0, 128, 192, 256):
+    for width in (0, 128, 256):
         dX = torch.empty((M, K), device="cuda", dtype=dtype)
         dW = torch.empty((N, K), device="cuda", dtype=F32)
         db = torch.empty(N, device="cuda")
