@@ -339,3 +339,90 @@ def test_backward_is_repeatable_on_a_side_stream():
     torch.cuda.synchronize()
     check_device_ok()
     assert torch.equal(outs[0], outs[1]) and torch.equal(db[0], db[1])
+
+
+def test_backward_offsets_past_32_bits():
+    """Every matrix's rows lie further apart than 2^31 elements allow in all."""
+    gen = generator(25)
+    M, N, K = 6, 40, 72
+    stride = (1 << 31) // M + 1024 - ((1 << 31) // M) % 8
+    view = torch.empty(stride * M, device="cuda", dtype=BF16).view(M, stride)
+    dy, z, x, dX = (view[:, o:o + n] for o, n in ((0, N), (512, N), (1024, K), (1536, K)))
+    for t, n in ((dy, N), (z, N), (x, K)):
+        t.copy_(torch.randn((M, n), generator=gen, device="cuda"))
+    w = matrix(gen, N, K, BF16, K ** -0.5)
+    dW = torch.empty((N, K), device="cuda")
+    db = torch.empty(N, device="cuda")
+    igc.linear_act_backward(dy, x, w, act="gelu", Z=z, dX=dX, dW=dW, dbias=db)
+    check_device_ok()
+    dz, ez = ref.linear_dz(d(dy), d(z), "gelu")
+    wx, ww, wb = ref.grads([dz], [ez], d(x), [d(w)], BF16, F32, F32)
+    ref.check(dX, wx[0], "dX")
+    ref.check(dW, ww[0], "dW")
+    ref.check(db, wb[0], "db")
+
+
+def test_backward_from_threads_on_one_stream():
+    """Calls of several host threads interleave on one stream; each has its own workspace."""
+    import threading
+    gen = generator(26)
+    shapes = [(300, 200, 136), (70, 520, 264), (600, 72, 328), (128, 300, 200)]
+    cases, results = [], {}
+    for M, N, K in shapes:
+        x, w = matrix(gen, M, K, BF16), matrix(gen, N, K, BF16, K ** -0.5)
+        dy, z = matrix(gen, M, N, BF16), matrix(gen, M, N, BF16)
+        alone = igc.linear_act_backward(dy, x, w, act="silu", Z=z)[:2]
+        cases.append((x, w, dy, z, [t.clone() for t in alone]))
+    torch.cuda.synchronize()
+
+    def work(i):
+        x, w, dy, z, _ = cases[i]
+        results[i] = [igc.linear_act_backward(dy, x, w, act="silu", Z=z)[:2] for _ in range(30)]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    check_device_ok()
+    for i, case in enumerate(cases):
+        for dX, dW in results[i]:
+            assert torch.equal(dX, case[4][0]) and torch.equal(dW, case[4][1])
+
+
+def test_backward_replays_in_a_graph_beside_eager_calls():
+    """A captured call keeps its own workspace: eager calls in between, larger ones among
+    them, do not disturb its replays."""
+    gen = generator(27)
+    M, N, K = 200, 136, 264
+    x, w = matrix(gen, M, K, F16), matrix(gen, N, K, F16, K ** -0.5)
+    dy, z = matrix(gen, M, N, F16), matrix(gen, M, N, F16)
+    dX, dW = (torch.empty(s, device="cuda", dtype=F16) for s in ((M, K), (N, K)))
+    db = torch.empty(N, device="cuda")
+    igc.linear_act_backward(dy, x, w, act="gelu", Z=z, dX=dX, dW=dW, dbias=db)
+    want = [t.clone() for t in (dX, dW, db)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        igc.linear_act_backward(dy, x, w, act="gelu", Z=z, dX=dX, dW=dW, dbias=db)
+    big = [matrix(gen, 900, n, F16) for n in (700, 520)]
+    wbig = matrix(gen, 700, 520, F16, 0.05)
+    for _ in range(3):
+        for t in (dX, dW, db):
+            t.zero_()
+        igc.linear_act_backward(big[0], big[1], wbig, act="gelu", Z=big[0])
+        graph.replay()
+        igc.linear_act_backward(big[0], big[1], wbig, act="gelu", Z=big[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((dX, dW, db), want))
+    check_device_ok()
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_forward_overflow_is_infinite(M):
+    x = torch.full((M, 64), 200.0, device="cuda", dtype=F16)
+    w = torch.full((40, 64), 200.0, device="cuda", dtype=F16)
+    Y = torch.empty((M, 40), device="cuda", dtype=F32)
+    Z = torch.empty((M, 40), device="cuda", dtype=F16)
+    igc.linear_act(x, w, Y=Y, Z=Z)
+    check_device_ok()
+    assert bool((Y == 64 * 40000.0).all()) and bool(torch.isposinf(Z).all())
