@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "ffn_host.h"
@@ -151,10 +152,11 @@ inline int ffn_map_b(CUtensorMap* map, const FfnProblem& q, int i, bool mn, int 
 // Estimated times in microseconds, for choosing between schedules (measured on GB300: a
 // CTA takes in about 65 bytes a nanosecond through TMA, two on an SM 95 together, one with
 // twice the stages 85; an SM reads about 40 from the shared memory of the other CTAs of
-// its cluster; DRAM gives 6600 once enough CTAs stream; a launch and a CTA's set-up, first
-// loads and last stores take about 3.5 us).
+// its cluster; back-to-back calls get 4.4 TB/s from DRAM with 64 streaming CTAs each, 6.0
+// with 128 and 7.3 with 256; a launch and a CTA's set-up, first loads and last stores take
+// about 3.5 us, a further wave of CTAs about 4).
 constexpr double kUsFixed = 3.5, kCtaRate = 65e3, kTwoCtaRate = 95e3, kDeepCtaRate = 85e3,
-                 kDsmemPerSm = 40e3, kDramRate = 6.6e6, kDramPerCta = 48e3;
+                 kDsmemPerSm = 40e3, kDramMost = 9.3e6, kDramRate = 6.6e6, kUsWave = 4.0;
 
 // Bytes of the operands, each read once.
 template <FfnOp kOp>
@@ -247,6 +249,20 @@ constexpr size_t kSmallSmemTwo = 110 * 1024;  // two CTAs on an SM
 constexpr size_t kSmallSmemOne = 224 * 1024;
 constexpr size_t kSmemPerSm = 228 * 1024;
 
+// Clusters of 1 .. kSkMaxSplit CTAs that run at once with one CTA on an SM (they stay
+// within a GPC, whose SMs a larger cluster does not fill).
+struct ClusterSlots {
+  int clusters[kSkMaxSplit + 1];
+};
+
+// A GB300's 152 SMs, scaled to another number: what igc_plan_ffn works with.
+inline ClusterSlots default_slots(int sms) {
+  constexpr int k152[kSkMaxSplit + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+  ClusterSlots s = {};
+  for (int i = 1; i <= kSkMaxSplit; ++i) s.clusters[i] = std::max(1, k152[i] * sms / 152);
+  return s;
+}
+
 struct SmallPlan {
   int m_blocks = 1, mt = 16, split = 1;
   double us = 1e30;
@@ -264,7 +280,7 @@ inline bool small_two_fit(int mt) {
 // combinations.  Fewer rows and more CTAs mean more SMs at work on shorter parts, but W
 // is read once per block of rows and each CTA's partial sums cross the cluster.
 template <FfnOp kOp>
-SmallPlan small_plan(const FfnProblem& q, int sms) {
+SmallPlan small_plan(const FfnProblem& q, int sms, const ClusterSlots& at_once) {
   constexpr int kOutT = kOp == FfnOp::Gated ? kSkRows / 2 : kSkRows;
   constexpr int kRowStep = ffn_a_mn(kOp) ? 64 : 16;
   const int atoms = static_cast<int>((q.K + BK - 1) / BK) * q.segs;
@@ -278,15 +294,15 @@ SmallPlan small_plan(const FfnProblem& q, int sms) {
     last_mt = mt;
     const double blocks = static_cast<double>((q.N + kOutT - 1) / kOutT) *
                           static_cast<double>(mb) * q.srcs;
-    for (int split = 1; split <= kSkMaxSplit && (split == 1 || atoms >= 2 * split); split *= 2) {
+    for (int split = 1; split <= kSkMaxSplit && (split == 1 || atoms >= 2 * split); ++split) {
+      if (split == 7) continue;  // (clusters of 7 waste a GPC's SMs as those of 8 do)
       const bool two = small_two_fit(mt);
-      // clusters of 4 and 8 do not pack the SMs fully
-      const double packed = split == 8 ? (two ? 0.85 : 0.8) : (split == 4 ? 0.9 : 1.0);
-      const double slots = (two ? 2.0 : 1.0) * sms * packed;
+      // (two to an SM, a cluster's CTAs find place more easily)
+      const double alone = static_cast<double>(at_once.clusters[split] * split);
+      const double slots = two ? 2.0 * sms * (split > 2 ? 0.9 : 1.0) : alone;
       const double ctas = blocks * split;
-      const double waves = ctas <= slots ? 1.0 : static_cast<double>(static_cast<long long>(
-                                                     (ctas + slots - 1) / slots));
-      const bool pairs = two && ctas > 0.9 * sms;  // two CTAs on an SM
+      const double waves = std::ceil(ctas / slots);
+      const bool pairs = two && ctas > alone;  // two CTAs on some SMs
       const double rate = pairs ? kTwoCtaRate / 2 : (two ? kCtaRate : kDeepCtaRate);
       const double load =
           static_cast<double>((atoms + split - 1) / split) * BK * 2.0 * (kSkRows + mt) / rate;
@@ -294,10 +310,10 @@ SmallPlan small_plan(const FfnProblem& q, int sms) {
           static_cast<double>(small_part_bytes(mt)) /
               (split > 1 ? (pairs ? kDsmemPerSm / 2 : kDsmemPerSm) : rate) +
           (split > 1 ? 0.3 : 0.0);
-      const double dram =
-          unique / std::min(kDramRate, std::min(ctas, slots) * kDramPerCta);
+      const double streams = ctas / waves;
+      const double dram = unique / (kDramMost * streams / (streams + 70.0));
       const double busy = std::max(waves * load, dram);
-      const double us = kUsFixed + busy + waves * join;
+      const double us = kUsFixed + busy + waves * join + (waves - 1.0) * kUsWave;
       if (us < best.us) {
         best.m_blocks = static_cast<int>(mb);
         best.mt = mt;
@@ -309,23 +325,53 @@ SmallPlan small_plan(const FfnProblem& q, int sms) {
   return best;
 }
 
+// Sets the kernel's shared-memory attribute and asks how many of its clusters run at once
+// (cached per device).
+template <FfnOp kOp>
+int small_setup(const DeviceInfo& dev, const ClusterSlots** slots) {
+  static std::once_flag once[64];
+  static int rcs[64];
+  static ClusterSlots table[64];
+  const int d = dev.device;
+  std::call_once(once[d], [&] {
+    auto kern = igc_ffn_small_kernel<kOp>;
+    rcs[d] = IGC_ERR_CUDA;
+    if (dev.smem_optin < kSmallSmemOne + 1024) {
+      rcs[d] = IGC_ERR_UNSUPPORTED;
+      return;
+    }
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmallSmemOne)) != cudaSuccess)
+      return;
+    table[d] = default_slots(dev.sm_count);
+    for (int s = 2; s <= kSkMaxSplit; ++s) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(s * dev.sm_count), 1, 1);
+      cfg.blockDim = dim3(kSkThreads, 1, 1);
+      cfg.dynamicSmemBytes = kSmallSmemOne;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0)
+        table[d].clusters[s] = n;
+      else
+        (void)cudaGetLastError();
+    }
+    rcs[d] = IGC_OK;
+  });
+  *slots = &table[d];
+  return rcs[d];
+}
+
 template <FfnOp kOp>
 int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const SmallPlan& plan,
                      cudaStream_t stream) {
-  static std::once_flag once[64];
-  static int rcs[64];
   auto kern = igc_ffn_small_kernel<kOp>;
-  std::call_once(once[dev.device], [&] {
-    rcs[dev.device] =
-        dev.smem_optin < kSmallSmemOne + 1024
-            ? IGC_ERR_UNSUPPORTED
-            : (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kSmallSmemOne)) == cudaSuccess
-                   ? IGC_OK
-                   : IGC_ERR_CUDA);
-  });
-  if (rcs[dev.device] != IGC_OK) return rcs[dev.device];
-
   constexpr int kOutT = kOp == FfnOp::Gated ? kSkRows / 2 : kSkRows;
   SmallParams p = {};
   p.M = static_cast<int>(q.M), p.N = static_cast<int>(q.N);
@@ -407,9 +453,12 @@ inline bool ffn_takes_small(const SmallPlan& small, const TilePlan& tiles) {
 template <FfnOp kOp>
 int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, cudaStream_t stream) {
   int clusters = 0;
-  const int rc = ffn_kernel_setup<kOp, 256>(dev, &clusters);
+  int rc = ffn_kernel_setup<kOp, 256>(dev, &clusters);
   if (rc != IGC_OK) return rc;
-  const SmallPlan small = small_plan<kOp>(q, dev.sm_count);
+  const ClusterSlots* slots = nullptr;
+  rc = small_setup<kOp>(dev, &slots);
+  if (rc != IGC_OK) return rc;
+  const SmallPlan small = small_plan<kOp>(q, dev.sm_count, *slots);
   const TilePlan tiles = tile_plan<kOp>(q, clusters);
   return ffn_takes_small(small, tiles) ? ffn_launch_small<kOp>(dev, q, small, stream)
                                        : ffn_launch_tiles<kOp>(dev, q, tiles.bn, stream);
@@ -418,7 +467,7 @@ int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, cudaStream_t stream) 
 // igc_plan_ffn for one product (see igc_ffn.h).
 template <FfnOp kOp>
 void ffn_plan(const FfnProblem& q, int sms, int32_t* out) {
-  const SmallPlan small = small_plan<kOp>(q, sms);
+  const SmallPlan small = small_plan<kOp>(q, sms, default_slots(sms));
   const TilePlan tiles = tile_plan<kOp>(q, sms / 2);
   const bool is_small = ffn_takes_small(small, tiles);
   out[0] = is_small;

@@ -241,19 +241,17 @@ struct FfnFetched {
   uint4 res[8];
 };
 
-// The residual's box where 16-byte loads cannot take it (rows not 16-byte aligned, or
-// columns past N): a row at a time through the staging buffer, a column per lane.
-// (Loads of one element of every lane's own row, 64 of them, took 12 us more on
-// 3630 x 702 x 2944 fp16.)
+// The residual's box where rows are not 16-byte aligned: a row at a time through the
+// staging buffer, a column per lane.
 __device__ __forceinline__ void ffn_gather_residual(const FfnParams& p, const Stager& st, int n0,
                                                     FfnFetched& f) {
   st.begin();
   const uint16_t* src = static_cast<const uint16_t*>(p.R);
   const int rows = min(32, st.M - st.row0);
-  for (int r0 = 0; r0 < rows; r0 += 8) {
-    uint16_t e[8][2];
+  for (int r0 = 0; r0 < rows; r0 += 16) {
+    uint16_t e[16][2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 16; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int n = n0 + st.lane + 32 * h;
@@ -262,7 +260,7 @@ __device__ __forceinline__ void ffn_gather_residual(const FfnParams& p, const St
                       : static_cast<uint16_t>(0);
       }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 16; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<uint16_t*>(st.buf + ffn_staged(r0 + j, st.lane + 32 * h)) = e[j][h];
@@ -288,12 +286,31 @@ __device__ __forceinline__ void ffn_fetch(const FfnParams& p, const Stager& st, 
   }
   if constexpr (kOp == FfnOp::Linear) {
     if (p.R == nullptr) return;
-    if (p.r_vec && n0 + kFfnBox <= p.N) {
+    if (p.r_vec) {
       const int m = st.row0 + st.lane;
-      const uint4* r = reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(p.R) + static_cast<long long>(m) * p.ldr + n0);
+      const int cols = m < p.M ? p.N - n0 : 0;
+      const uint16_t* r =
+          static_cast<const uint16_t*>(p.R) + static_cast<long long>(m) * p.ldr + n0;
+      if (cols >= kFfnBox) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f.res[k] = m < p.M ? r[k] : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < 8; ++k) f.res[k] = reinterpret_cast<const uint4*>(r)[k];
+      } else {
+        // 16 bytes at a time, the row's last columns, where they do not fill 16, singly
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          if (8 * k + 8 <= cols) {
+            const uint4 q = reinterpret_cast<const uint4*>(r)[k];
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+          } else if (8 * k < cols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (8 * k + i < cols)
+                w[i / 2] |= static_cast<uint32_t>(r[8 * k + i]) << (16 * (i & 1));
+          }
+          f.res[k] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
     } else {
       ffn_gather_residual(p, st, n0, f);
     }
