@@ -103,13 +103,35 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
     rc = ffn_dact(a, gated, stream);
     if (rc != IGC_OK) return rc;
   }
+  GradArgs g;
+  g.M = M, g.N = N, g.K = K, g.dtype = dtype, g.count = n;
+  g.D = D, g.W = W, g.X = X, g.dX = dX, g.dW = dW;
+  if (want_x || want_w) {
+    // Tiles of both products that fit the SMs together run side by side; dX on the kernel
+    // for small outputs, which spreads over all SMs, leaves those of dW no room (509 x 1001 x
+    // 777 fp16: 9.3 and 8.2 us alone on tiles and 9.9 together, 16.2 with dX on the other
+    // kernel).  Decided by the sizes alone, for operands with closely packed rows, so that
+    // a gradient does not depend on which others are asked for.
+    const Mat d{nullptr, padded(N), dtype}, x{nullptr, padded(K), dtype};
+    const Mat ds[2] = {d, d}, xs[2] = {x, x};
+    GradArgs sizes = g;
+    sizes.D = ds, sizes.W = xs, sizes.X = x, sizes.dX = x, sizes.dW = xs;
+    GradEstimate ex, ew;
+    rc = ffn_estimate_x(dev, sizes, &ex);
+    if (rc == IGC_OK) rc = ffn_estimate_w(dev, sizes, &ew);
+    if (rc != IGC_OK) return rc;
+    const double together = ex.tiles_us > ew.tiles_us ? ex.tiles_us : ew.tiles_us;
+    g.tiles_only = ex.small && !ew.small &&
+                   ex.tile_ctas + ew.tile_ctas <= dev.sm_count &&
+                   together < ex.best_us + ew.best_us - 3.0;
+  }
   if (want_x) {
-    rc = ffn_grad_x(dev, M, N, K, dtype, n, D, W, dX, after_first, stream);
+    rc = ffn_grad_x(dev, g, after_first, stream);
     if (rc != IGC_OK) return rc;
     after_first = true;
   }
   if (want_w) {
-    rc = ffn_grad_w(dev, M, N, K, dtype, n, D, X, dW, after_first, stream);
+    rc = ffn_grad_w(dev, g, after_first, stream);
     if (rc != IGC_OK) return rc;
     after_first = true;
   }

@@ -4,15 +4,26 @@
 
 namespace igc {
 
-int ffn_grad_w(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
-               const Mat* D, const Mat& X, const Mat* dW, bool late_wait,
-               cudaStream_t stream) {
+namespace {
+
+FfnProblem problem(const GradArgs& a) {
   FfnProblem q;
-  q.late_wait = late_wait;
-  q.M = N, q.N = K, q.K = M, q.dtype = dtype;
-  q.srcs = q.count_a = count;
-  for (int i = 0; i < count; ++i) q.A[i] = D[i], q.out[i] = dW[i];
-  q.B[0] = X;
+  q.M = a.N, q.N = a.K, q.K = a.M, q.dtype = a.dtype;
+  q.srcs = q.count_a = a.count;
+  for (int i = 0; i < a.count; ++i) q.A[i] = a.D[i], q.out[i] = a.dW[i];
+  q.B[0] = a.X;
+  return q;
+}
+
+}  // namespace
+
+int ffn_estimate_w(const DeviceInfo& dev, const GradArgs& a, GradEstimate* e) {
+  return ffn_estimate<FfnOp::GradW>(dev, problem(a), e);
+}
+
+int ffn_grad_w(const DeviceInfo& dev, const GradArgs& a, bool late_wait, cudaStream_t stream) {
+  FfnProblem q = problem(a);
+  q.late_wait = late_wait, q.tiles_only = a.tiles_only;
   return ffn_launch<FfnOp::GradW>(dev, q, stream);
 }
 

@@ -4,15 +4,26 @@
 
 namespace igc {
 
-int ffn_grad_x(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
-               const Mat* D, const Mat* W, const Mat& dX, bool late_wait,
-               cudaStream_t stream) {
+namespace {
+
+FfnProblem problem(const GradArgs& a) {
   FfnProblem q;
-  q.late_wait = late_wait;
-  q.M = M, q.N = K, q.K = N, q.dtype = dtype;
-  q.segs = q.count_a = q.count_b = count;
-  for (int i = 0; i < count; ++i) q.A[i] = D[i], q.B[i] = W[i];
-  q.out[0] = dX;
+  q.M = a.M, q.N = a.K, q.K = a.N, q.dtype = a.dtype;
+  q.segs = q.count_a = q.count_b = a.count;
+  for (int i = 0; i < a.count; ++i) q.A[i] = a.D[i], q.B[i] = a.W[i];
+  q.out[0] = a.dX;
+  return q;
+}
+
+}  // namespace
+
+int ffn_estimate_x(const DeviceInfo& dev, const GradArgs& a, GradEstimate* e) {
+  return ffn_estimate<FfnOp::GradX>(dev, problem(a), e);
+}
+
+int ffn_grad_x(const DeviceInfo& dev, const GradArgs& a, bool late_wait, cudaStream_t stream) {
+  FfnProblem q = problem(a);
+  q.late_wait = late_wait, q.tiles_only = a.tiles_only;
   return ffn_launch<FfnOp::GradX>(dev, q, stream);
 }
 

@@ -40,13 +40,31 @@ struct Mat {
   int dtype = IGC_F32;
 };
 
-// dX = sum_s D[s] W[s]: D[s] M x N, W[s] N x K, dX M x K (ffn_gradx.cu).  late_wait: the
-// kernel may run beside the one before it in the stream (ffn_dependency_wait, ffn_tc.cuh).
-int ffn_grad_x(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
-               const Mat* D, const Mat* W, const Mat& dX, bool late_wait, cudaStream_t stream);
-// dW[s] = D[s]^T X: X M x K, dW[s] N x K (ffn_gradw.cu)
-int ffn_grad_w(const DeviceInfo& dev, int64_t M, int64_t N, int64_t K, int dtype, int count,
-               const Mat* D, const Mat& X, const Mat* dW, bool late_wait, cudaStream_t stream);
+// The products of a backward pass: dX = sum_s D[s] W[s] (ffn_gradx.cu) and dW[s] = D[s]^T X
+// (ffn_gradw.cu), D[s] M x N, W[s] and dW[s] N x K, X and dX M x K, s < count.
+struct GradArgs {
+  int64_t M = 0, N = 0, K = 0;
+  int dtype = IGC_BF16;
+  int count = 1;
+  const Mat* D = nullptr;
+  const Mat* W = nullptr;
+  Mat X, dX;
+  const Mat* dW = nullptr;
+  bool tiles_only = false;  // on the 256-row tiles whatever the estimate
+};
+// An estimate of a product's time, on the kernel it would take (small: the one for small
+// outputs) and on the tiles, and the CTAs that the tiles take.
+struct GradEstimate {
+  bool small = false;
+  double best_us = 0.0, tiles_us = 0.0;
+  int tile_ctas = 0;
+};
+int ffn_estimate_x(const DeviceInfo& dev, const GradArgs& a, GradEstimate* e);
+int ffn_estimate_w(const DeviceInfo& dev, const GradArgs& a, GradEstimate* e);
+// late_wait: the kernel may run beside the one before it in the stream
+// (ffn_dependency_wait, ffn_tc.cuh).
+int ffn_grad_x(const DeviceInfo& dev, const GradArgs& a, bool late_wait, cudaStream_t stream);
+int ffn_grad_w(const DeviceInfo& dev, const GradArgs& a, bool late_wait, cudaStream_t stream);
 
 // Forward passes over the fp32 pre-activations of a contraction of length zero
 // (the biases alone), and the backward passes over stored pre-activations (ffn_dact.cu).

@@ -137,6 +137,7 @@ struct FfnProblem {
   int bias_dtype = IGC_F32;
   Mat R;
   bool late_wait = false;       // see ffn_dependency_wait
+  bool tiles_only = false;      // 256-row tiles whatever the estimate
 };
 
 // Stored extents of operand i: MN-major operands have k as their rows.
@@ -174,6 +175,7 @@ double operand_bytes(const FfnProblem& q) {
 // whole one.
 struct TilePlan {
   int bn = 256;
+  int ctas = 0;
   double us = 1e30;
 };
 
@@ -209,6 +211,7 @@ TilePlan tile_plan(const FfnProblem& q, int clusters) {
     const double us = kUsFixed + 1.0 + std::max(busy, dram);
     if (us < best.us * 0.999) {
       best.bn = bn;
+      best.ctas = 2 * static_cast<int>(full > 0 ? clusters : (halves ? 2 * rem : rem));
       best.us = us;
     }
   }
@@ -451,17 +454,39 @@ inline bool ffn_takes_small(const SmallPlan& small, const TilePlan& tiles) {
 }
 
 template <FfnOp kOp>
-int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, cudaStream_t stream) {
+int ffn_plans(const DeviceInfo& dev, const FfnProblem& q, SmallPlan* small, TilePlan* tiles) {
   int clusters = 0;
   int rc = ffn_kernel_setup<kOp, 256>(dev, &clusters);
   if (rc != IGC_OK) return rc;
   const ClusterSlots* slots = nullptr;
   rc = small_setup<kOp>(dev, &slots);
   if (rc != IGC_OK) return rc;
-  const SmallPlan small = small_plan<kOp>(q, dev.sm_count, *slots);
-  const TilePlan tiles = tile_plan<kOp>(q, clusters);
+  *tiles = tile_plan<kOp>(q, clusters);
+  if (!q.tiles_only) *small = small_plan<kOp>(q, dev.sm_count, *slots);
+  return IGC_OK;
+}
+
+template <FfnOp kOp>
+int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, cudaStream_t stream) {
+  SmallPlan small;
+  TilePlan tiles;
+  const int rc = ffn_plans<kOp>(dev, q, &small, &tiles);
+  if (rc != IGC_OK) return rc;
   return ffn_takes_small(small, tiles) ? ffn_launch_small<kOp>(dev, q, small, stream)
                                        : ffn_launch_tiles<kOp>(dev, q, tiles.bn, stream);
+}
+
+// What ffn_grad_x and ffn_grad_w decide by (ffn_host.h).
+template <FfnOp kOp>
+int ffn_estimate(const DeviceInfo& dev, const FfnProblem& q, GradEstimate* e) {
+  SmallPlan small;
+  TilePlan tiles;
+  const int rc = ffn_plans<kOp>(dev, q, &small, &tiles);
+  e->small = ffn_takes_small(small, tiles);
+  e->tiles_us = tiles.us;
+  e->best_us = e->small ? small.us : tiles.us;
+  e->tile_ctas = tiles.ctas;
+  return rc;
 }
 
 // igc_plan_ffn for one product (see igc_ffn.h).
