@@ -1,5 +1,7 @@
 // linear_act_backward and gated_ffn_backward: the pass through the activation (and the
 // bias gradients), then the two products of the tensor cores.
+#include <algorithm>
+
 #include "ffn_host.h"
 #include "launch.cuh"
 
@@ -107,33 +109,28 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
   g.M = M, g.N = N, g.K = K, g.dtype = dtype, g.count = n;
   g.D = D, g.W = W, g.X = X, g.dX = dX, g.dW = dW;
   if (want_x || want_w) {
+    ProductPlan px, pw;
+    rc = ffn_plan_x(dev, g, &px);
+    if (rc == IGC_OK) rc = ffn_plan_w(dev, g, &pw);
+    if (rc != IGC_OK) return rc;
     // Tiles of both products that fit the SMs together run side by side; dX on the kernel
     // for small outputs, which spreads over all SMs, leaves those of dW no room (509 x 1001 x
     // 777 fp16: 9.3 and 8.2 us alone on tiles and 9.9 together, 16.2 with dX on the other
-    // kernel).  Decided by the sizes alone, for operands with closely packed rows, so that
-    // a gradient does not depend on which others are asked for.
-    const Mat d{nullptr, padded(N), dtype}, x{nullptr, padded(K), dtype};
-    const Mat ds[2] = {d, d}, xs[2] = {x, x};
-    GradArgs sizes = g;
-    sizes.D = ds, sizes.W = xs, sizes.X = x, sizes.dX = x, sizes.dW = xs;
-    GradEstimate ex, ew;
-    rc = ffn_estimate_x(dev, sizes, &ex);
-    if (rc == IGC_OK) rc = ffn_estimate_w(dev, sizes, &ew);
-    if (rc != IGC_OK) return rc;
-    const double together = ex.tiles_us > ew.tiles_us ? ex.tiles_us : ew.tiles_us;
-    g.tiles_only = ex.small && !ew.small &&
-                   ex.tile_ctas + ew.tile_ctas <= dev.sm_count &&
-                   together < ex.best_us + ew.best_us - 3.0;
-  }
-  if (want_x) {
-    rc = ffn_grad_x(dev, g, after_first, stream);
-    if (rc != IGC_OK) return rc;
-    after_first = true;
-  }
-  if (want_w) {
-    rc = ffn_grad_w(dev, g, after_first, stream);
-    if (rc != IGC_OK) return rc;
-    after_first = true;
+    // kernel).  Decided whether or not both are asked for, so that a gradient does not
+    // depend on that.
+    if (px.small && !pw.small && px.tile_ctas + pw.tile_ctas <= dev.sm_count &&
+        std::max(px.tiles_us, pw.tiles_us) < px.best_us + pw.best_us - 3.0)
+      px.small = false;
+    if (want_x) {
+      rc = ffn_grad_x(dev, g, px, after_first, stream);
+      if (rc != IGC_OK) return rc;
+      after_first = true;
+    }
+    if (want_w) {
+      rc = ffn_grad_w(dev, g, pw, after_first, stream);
+      if (rc != IGC_OK) return rc;
+      after_first = true;
+    }
   }
   if (want_b) rc = ffn_dact_sums(a, gated, after_first, stream);
   return rc;

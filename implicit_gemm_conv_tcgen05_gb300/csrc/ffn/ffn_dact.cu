@@ -11,6 +11,9 @@
 // second kernel adds the chunks in order (no atomics).  Up to 512 rows, a cluster of up to
 // 8 blocks covers a column block's rows and adds its sums through distributed shared memory
 // instead: one launch less (2 to 3 us of host time in calls that take about 22).
+//
+// Bound by memory: gated 8192 x 16384 without sums 190 us, 1.34 GB at 7.1 TB/s; linear 4096 x
+// 8192, tanh-GELU with sums, 37 us, 201 MB at 5.4 TB/s (27 instructions an element).
 #include "ffn_act.cuh"
 #include "ffn_host.h"
 #include "ffn_tc.cuh"

@@ -6,25 +6,29 @@ namespace igc {
 
 namespace {
 
-FfnProblem problem(const GradArgs& a) {
+FfnProblem sizes(const GradArgs& a) {
   FfnProblem q;
   q.M = a.N, q.N = a.K, q.K = a.M, q.dtype = a.dtype;
   q.srcs = q.count_a = a.count;
-  for (int i = 0; i < a.count; ++i) q.A[i] = a.D[i], q.out[i] = a.dW[i];
-  q.B[0] = a.X;
   return q;
 }
 
 }  // namespace
 
-int ffn_estimate_w(const DeviceInfo& dev, const GradArgs& a, GradEstimate* e) {
-  return ffn_estimate<FfnOp::GradW>(dev, problem(a), e);
+int ffn_plan_w(const DeviceInfo& dev, const GradArgs& a, ProductPlan* plan) {
+  FfnProblem q = sizes(a);
+  for (int i = 0; i < a.count; ++i) q.A[i] = packed_rows(a.N);
+  q.B[0] = packed_rows(a.K);
+  return ffn_plan<FfnOp::GradW>(dev, q, plan);
 }
 
-int ffn_grad_w(const DeviceInfo& dev, const GradArgs& a, bool late_wait, cudaStream_t stream) {
-  FfnProblem q = problem(a);
-  q.late_wait = late_wait, q.tiles_only = a.tiles_only;
-  return ffn_launch<FfnOp::GradW>(dev, q, stream);
+int ffn_grad_w(const DeviceInfo& dev, const GradArgs& a, const ProductPlan& plan, bool late_wait,
+               cudaStream_t stream) {
+  FfnProblem q = sizes(a);
+  for (int i = 0; i < a.count; ++i) q.A[i] = a.D[i], q.out[i] = a.dW[i];
+  q.B[0] = a.X;
+  q.late_wait = late_wait;
+  return ffn_launch<FfnOp::GradW>(dev, q, plan, stream);
 }
 
 }  // namespace igc

@@ -40,8 +40,19 @@ struct Mat {
   int dtype = IGC_F32;
 };
 
+// How a product runs: on the kernel for small outputs (mt rows to a block, m_blocks of
+// them, split CTAs to each) or on 256-row tiles of bn columns (tile_ctas CTAs); the
+// estimated times of the better one and of the tiles.
+struct ProductPlan {
+  bool small = false;
+  int mt = 16, m_blocks = 1, split = 1;
+  int bn = 256, tile_ctas = 0;
+  double best_us = 0.0, tiles_us = 0.0;
+};
+
 // The products of a backward pass: dX = sum_s D[s] W[s] (ffn_gradx.cu) and dW[s] = D[s]^T X
-// (ffn_gradw.cu), D[s] M x N, W[s] and dW[s] N x K, X and dX M x K, s < count.
+// (ffn_gradw.cu), D[s] M x N, W[s] and dW[s] N x K, X and dX M x K, s < count.  The plans go
+// by the sizes alone, as of operands with closely packed rows.
 struct GradArgs {
   int64_t M = 0, N = 0, K = 0;
   int dtype = IGC_BF16;
@@ -50,21 +61,15 @@ struct GradArgs {
   const Mat* W = nullptr;
   Mat X, dX;
   const Mat* dW = nullptr;
-  bool tiles_only = false;  // on the 256-row tiles whatever the estimate
 };
-// An estimate of a product's time, on the kernel it would take (small: the one for small
-// outputs) and on the tiles, and the CTAs that the tiles take.
-struct GradEstimate {
-  bool small = false;
-  double best_us = 0.0, tiles_us = 0.0;
-  int tile_ctas = 0;
-};
-int ffn_estimate_x(const DeviceInfo& dev, const GradArgs& a, GradEstimate* e);
-int ffn_estimate_w(const DeviceInfo& dev, const GradArgs& a, GradEstimate* e);
+int ffn_plan_x(const DeviceInfo& dev, const GradArgs& a, ProductPlan* plan);
+int ffn_plan_w(const DeviceInfo& dev, const GradArgs& a, ProductPlan* plan);
 // late_wait: the kernel may run beside the one before it in the stream
 // (ffn_dependency_wait, ffn_tc.cuh).
-int ffn_grad_x(const DeviceInfo& dev, const GradArgs& a, bool late_wait, cudaStream_t stream);
-int ffn_grad_w(const DeviceInfo& dev, const GradArgs& a, bool late_wait, cudaStream_t stream);
+int ffn_grad_x(const DeviceInfo& dev, const GradArgs& a, const ProductPlan& plan, bool late_wait,
+               cudaStream_t stream);
+int ffn_grad_w(const DeviceInfo& dev, const GradArgs& a, const ProductPlan& plan, bool late_wait,
+               cudaStream_t stream);
 
 // Forward passes over the fp32 pre-activations of a contraction of length zero
 // (the biases alone), and the backward passes over stored pre-activations (ffn_dact.cu).

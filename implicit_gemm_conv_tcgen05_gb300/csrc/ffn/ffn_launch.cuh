@@ -137,8 +137,15 @@ struct FfnProblem {
   int bias_dtype = IGC_F32;
   Mat R;
   bool late_wait = false;       // see ffn_dependency_wait
-  bool tiles_only = false;      // 256-row tiles whatever the estimate
 };
+
+// An operand of `cols` columns that a plan takes to start on a 16-byte boundary and to be
+// closely packed.
+inline Mat packed_rows(int64_t cols) {
+  Mat m;
+  m.ld = (cols + 7) / 8 * 8;
+  return m;
+}
 
 // Stored extents of operand i: MN-major operands have k as their rows.
 inline int ffn_map_a(CUtensorMap* map, const FfnProblem& q, int i, bool mn, int box_rows) {
@@ -372,7 +379,7 @@ int small_setup(const DeviceInfo& dev, const ClusterSlots** slots) {
 }
 
 template <FfnOp kOp>
-int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const SmallPlan& plan,
+int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const ProductPlan& plan,
                      cudaStream_t stream) {
   auto kern = igc_ffn_small_kernel<kOp>;
   constexpr int kOutT = kOp == FfnOp::Gated ? kSkRows / 2 : kSkRows;
@@ -449,59 +456,47 @@ int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const SmallPlan
 
 // Which of the two kernels runs a problem: the one with the shorter estimate, unless the
 // calling thread forced a tile width (igc_set_tile_width).
-inline bool ffn_takes_small(const SmallPlan& small, const TilePlan& tiles) {
-  return small.us < tiles.us && tile_width_override() == 0;
+inline ProductPlan join_plans(const SmallPlan& small, const TilePlan& tiles) {
+  ProductPlan p;
+  p.small = small.us < tiles.us && tile_width_override() == 0;
+  p.mt = small.mt, p.m_blocks = small.m_blocks, p.split = small.split;
+  p.bn = tiles.bn, p.tile_ctas = tiles.ctas;
+  p.tiles_us = tiles.us;
+  p.best_us = p.small ? small.us : tiles.us;
+  return p;
 }
 
 template <FfnOp kOp>
-int ffn_plans(const DeviceInfo& dev, const FfnProblem& q, SmallPlan* small, TilePlan* tiles) {
+int ffn_plan(const DeviceInfo& dev, const FfnProblem& q, ProductPlan* plan) {
   int clusters = 0;
   int rc = ffn_kernel_setup<kOp, 256>(dev, &clusters);
   if (rc != IGC_OK) return rc;
   const ClusterSlots* slots = nullptr;
   rc = small_setup<kOp>(dev, &slots);
   if (rc != IGC_OK) return rc;
-  *tiles = tile_plan<kOp>(q, clusters);
-  if (!q.tiles_only) *small = small_plan<kOp>(q, dev.sm_count, *slots);
+  *plan = join_plans(small_plan<kOp>(q, dev.sm_count, *slots), tile_plan<kOp>(q, clusters));
   return IGC_OK;
 }
 
 template <FfnOp kOp>
-int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, cudaStream_t stream) {
-  SmallPlan small;
-  TilePlan tiles;
-  const int rc = ffn_plans<kOp>(dev, q, &small, &tiles);
-  if (rc != IGC_OK) return rc;
-  return ffn_takes_small(small, tiles) ? ffn_launch_small<kOp>(dev, q, small, stream)
-                                       : ffn_launch_tiles<kOp>(dev, q, tiles.bn, stream);
-}
-
-// What ffn_grad_x and ffn_grad_w decide by (ffn_host.h).
-template <FfnOp kOp>
-int ffn_estimate(const DeviceInfo& dev, const FfnProblem& q, GradEstimate* e) {
-  SmallPlan small;
-  TilePlan tiles;
-  const int rc = ffn_plans<kOp>(dev, q, &small, &tiles);
-  e->small = ffn_takes_small(small, tiles);
-  e->tiles_us = tiles.us;
-  e->best_us = e->small ? small.us : tiles.us;
-  e->tile_ctas = tiles.ctas;
-  return rc;
+int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, const ProductPlan& plan,
+               cudaStream_t stream) {
+  return plan.small ? ffn_launch_small<kOp>(dev, q, plan, stream)
+                    : ffn_launch_tiles<kOp>(dev, q, plan.bn, stream);
 }
 
 // igc_plan_ffn for one product (see igc_ffn.h).
 template <FfnOp kOp>
-void ffn_plan(const FfnProblem& q, int sms, int32_t* out) {
+void ffn_plan_host(const FfnProblem& q, int sms, int32_t* out) {
   const SmallPlan small = small_plan<kOp>(q, sms, default_slots(sms));
-  const TilePlan tiles = tile_plan<kOp>(q, sms / 2);
-  const bool is_small = ffn_takes_small(small, tiles);
-  out[0] = is_small;
-  out[1] = is_small ? small.mt : BM;
-  out[2] = is_small ? small.m_blocks : static_cast<int32_t>((q.M + BM - 1) / BM);
-  out[3] = is_small ? kSkRows : tiles.bn;
-  out[4] = is_small ? small.split : 1;
+  const ProductPlan p = join_plans(small, tile_plan<kOp>(q, sms / 2));
+  out[0] = p.small;
+  out[1] = p.small ? p.mt : BM;
+  out[2] = p.small ? p.m_blocks : static_cast<int32_t>((q.M + BM - 1) / BM);
+  out[3] = p.small ? kSkRows : p.bn;
+  out[4] = p.small ? p.split : 1;
   out[5] = static_cast<int32_t>(std::min(small.us * 1000, 2e9));
-  out[6] = static_cast<int32_t>(std::min(tiles.us * 1000, 2e9));
+  out[6] = static_cast<int32_t>(std::min(p.tiles_us * 1000, 2e9));
 }
 
 }  // namespace igc

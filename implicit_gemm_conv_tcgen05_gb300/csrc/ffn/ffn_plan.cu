@@ -1,5 +1,6 @@
-// Tensor maps of the feed-forward launches, and igc_plan_ffn: the kernel and schedule that a product of the feed-forward operators runs
-// with, from the launches' own decision functions, on the host.
+// Tensor maps of the feed-forward launches, and igc_plan_ffn: the kernel and schedule that
+// a product of the feed-forward operators runs with, from the launches' own decision
+// functions, on the host.
 #include "ffn_launch.cuh"
 
 namespace igc {
@@ -57,15 +58,15 @@ extern "C" int igc_plan_ffn(int op, int64_t M, int64_t N, int64_t K, int count, 
   FfnProblem q;
   q.M = M, q.N = N, q.K = K;
   switch (op) {
-    case IGC_PLAN_FFN_LINEAR: ffn_plan<FfnOp::Linear>(q, sms, out); return IGC_OK;
-    case IGC_PLAN_FFN_GATED: ffn_plan<FfnOp::Gated>(q, sms, out); return IGC_OK;
+    case IGC_PLAN_FFN_LINEAR: ffn_plan_host<FfnOp::Linear>(q, sms, out); return IGC_OK;
+    case IGC_PLAN_FFN_GATED: ffn_plan_host<FfnOp::Gated>(q, sms, out); return IGC_OK;
     case IGC_PLAN_FFN_GRAD_X:
       q.N = K, q.K = N, q.segs = count;
-      ffn_plan<FfnOp::GradX>(q, sms, out);
+      ffn_plan_host<FfnOp::GradX>(q, sms, out);
       return IGC_OK;
     case IGC_PLAN_FFN_GRAD_W:
       q.M = N, q.N = K, q.K = M, q.srcs = count;
-      ffn_plan<FfnOp::GradW>(q, sms, out);
+      ffn_plan_host<FfnOp::GradW>(q, sms, out);
       return IGC_OK;
     default: return IGC_ERR_INVALID_ARG;
   }

@@ -16,6 +16,11 @@
 // after a cluster barrier every CTA adds up a share of the outputs over the S partial sums
 // (distributed shared memory, in the order of r: no atomics, no workspace, the same
 // result every time) and applies the epilogue.
+//
+// What bounds it: DRAM for few rows (one token through 4096 x 16384 bf16 weights, 134 MB:
+// 21.2 us back to back, 6.3 TB/s; gated 48 x 16384 x 4096, 268 MB: 43.7 us), the SMs' intake
+// from L2 from some 64 rows on, where X weighs as much as W (128 x 8192 x 8192: 27.8 us),
+// and latency for small outputs (333 x 1000 x 2056: 10 us).
 #pragma once
 
 #include "ffn_act.cuh"
@@ -325,7 +330,8 @@ __global__ void __launch_bounds__(kSkThreads)
   }
   __syncwarp();
 
-  // Partial sums to shared memory: part[m][w] for output row m and column w of the block.  The MMAs are done (so every copy has landed and been read): the ring is free.
+  // Partial sums to shared memory: part[m][w] for output row m and column w of the block.
+  // The MMAs are done (so every copy has landed and been read): the ring is free.
   const bool ok = __all_sync(0xffffffffu, mbar_wait(&done, 0, lim, &abort_flag, p.status,
                                                     kSiteSkDone));
   tc_fence_after();

@@ -43,5 +43,7 @@ extern "C" int gated_ffn(int64_t M, int64_t F, int64_t K, int dtype, const void*
   q.B[0] = {Wg, ldw, dtype}, q.B[1] = {Wu, ldw, dtype}, q.count_b = 2;
   for (int i = 0; i < 3; ++i) q.out[i] = outs[i];
   q.act = act, q.bias[0] = bg, q.bias[1] = bu, q.bias_dtype = bias_dtype;
-  return ffn_launch<FfnOp::Gated>(dev, q, stream);
+  ProductPlan plan;
+  rc = ffn_plan<FfnOp::Gated>(dev, q, &plan);
+  return rc == IGC_OK ? ffn_launch<FfnOp::Gated>(dev, q, plan, stream) : rc;
 }

@@ -41,5 +41,7 @@ extern "C" int linear_act(int64_t M, int64_t N, int64_t K, int dtype, const void
   q.out[0] = outs[0], q.out[1] = outs[1];
   q.act = act, q.bias[0] = bias, q.bias_dtype = bias_dtype;
   q.R = {R, ldr, dtype};
-  return ffn_launch<FfnOp::Linear>(dev, q, stream);
+  ProductPlan plan;
+  rc = ffn_plan<FfnOp::Linear>(dev, q, &plan);
+  return rc == IGC_OK ? ffn_launch<FfnOp::Linear>(dev, q, plan, stream) : rc;
 }
