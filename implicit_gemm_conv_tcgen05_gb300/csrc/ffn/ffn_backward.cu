@@ -81,9 +81,24 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
   const bool identity = !gated && act == IGC_ACT_NONE;
   const bool copy = (want_x || want_w) && (!identity || !operand_ok(dO.ptr, dO.ld));
   Mat D[2] = {{dO.ptr, dO.ld, dtype}, {}};
-  // The three results after it read what the activation's pass wrote and nothing of one
-  // another: each but the first may run beside the one before it (late_wait).
-  bool after_first = false;
+  // Plans of both products, whether or not both are asked for, so that a gradient does not
+  // depend on that.  Tiles of both that fit the SMs together run side by side; dX on the
+  // kernel for small outputs, which spreads over all SMs, leaves those of dW no room (509 x
+  // 1001 x 777 fp16: 9.3 and 8.2 us alone on tiles and 9.9 together, 16.2 with dX on the
+  // other kernel).
+  GradArgs g;
+  g.M = M, g.N = N, g.K = K, g.dtype = dtype, g.count = n;
+  g.D = D, g.W = W, g.X = X, g.dX = dX, g.dW = dW;
+  ProductPlan px, pw;
+  if (want_x || want_w) {
+    rc = ffn_plan_x(dev, g, &px);
+    if (rc == IGC_OK) rc = ffn_plan_w(dev, g, &pw);
+    if (rc != IGC_OK) return rc;
+    if (px.small && !pw.small && px.tile_ctas + pw.tile_ctas <= dev.sm_count &&
+        std::max(px.tiles_us, pw.tiles_us) < px.best_us + pw.best_us - 3.0)
+      px.small = false;
+  }
+
   DactArgs a;
   if (copy || want_b) {
     if (workspace == nullptr || workspace_bytes < need ||
@@ -105,32 +120,18 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
     rc = ffn_dact(a, gated, stream);
     if (rc != IGC_OK) return rc;
   }
-  GradArgs g;
-  g.M = M, g.N = N, g.K = K, g.dtype = dtype, g.count = n;
-  g.D = D, g.W = W, g.X = X, g.dX = dX, g.dW = dW;
-  if (want_x || want_w) {
-    ProductPlan px, pw;
-    rc = ffn_plan_x(dev, g, &px);
-    if (rc == IGC_OK) rc = ffn_plan_w(dev, g, &pw);
+  // What follows reads what the activation's pass wrote and nothing of one another: each
+  // kernel but the first may run beside the one before it (late_wait).
+  bool after_first = false;
+  if (want_x) {
+    rc = ffn_grad_x(dev, g, px, after_first, stream);
     if (rc != IGC_OK) return rc;
-    // Tiles of both products that fit the SMs together run side by side; dX on the kernel
-    // for small outputs, which spreads over all SMs, leaves those of dW no room (509 x 1001 x
-    // 777 fp16: 9.3 and 8.2 us alone on tiles and 9.9 together, 16.2 with dX on the other
-    // kernel).  Decided whether or not both are asked for, so that a gradient does not
-    // depend on that.
-    if (px.small && !pw.small && px.tile_ctas + pw.tile_ctas <= dev.sm_count &&
-        std::max(px.tiles_us, pw.tiles_us) < px.best_us + pw.best_us - 3.0)
-      px.small = false;
-    if (want_x) {
-      rc = ffn_grad_x(dev, g, px, after_first, stream);
-      if (rc != IGC_OK) return rc;
-      after_first = true;
-    }
-    if (want_w) {
-      rc = ffn_grad_w(dev, g, pw, after_first, stream);
-      if (rc != IGC_OK) return rc;
-      after_first = true;
-    }
+    after_first = true;
+  }
+  if (want_w) {
+    rc = ffn_grad_w(dev, g, pw, after_first, stream);
+    if (rc != IGC_OK) return rc;
+    after_first = true;
   }
   if (want_b) rc = ffn_dact_sums(a, gated, after_first, stream);
   return rc;
