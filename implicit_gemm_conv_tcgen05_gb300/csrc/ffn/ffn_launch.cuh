@@ -106,6 +106,7 @@ inline void ffn_set_out(FfnParams& p, CUtensorMap* maps, int i, const Mat& m) {
   o.tma = 0;
   if (m.ptr == nullptr) return;
   const size_t es = elem_size(m.dtype);
+  o.whole = static_cast<size_t>(p.N) * es % 16 == 0;
   if (rows_aligned(m.ptr, m.ld, es, 16))
     o.tma = encode_tiled_2d_fresh(&maps[i], map_type(m.dtype), m.ptr,
                                   static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M),

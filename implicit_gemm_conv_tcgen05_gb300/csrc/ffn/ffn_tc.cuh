@@ -80,8 +80,9 @@ struct FfnCfg {
 struct FfnOut {
   void* ptr;
   long long ld;
-  int f32;  // fp32 elements, else 16-bit
-  int tma;  // written by bulk tensor stores
+  int f32;    // fp32 elements, else 16-bit
+  int tma;    // written by bulk tensor stores
+  int whole;  // rows of whole 16-byte pieces
 };
 
 struct FfnParams {
@@ -203,9 +204,9 @@ __device__ __forceinline__ int ffn_staged(int r, int c) {
   return r * 128 + ((((c >> 3) ^ (r & 7)) << 4) | ((c & 7) << 1));
 }
 
-// Stores a box whose rows TMA cannot address, from the staging buffer: a row at a time, a
-// column per lane, so that a warp's stores fall into the few sectors of one row.  kWords:
-// fp32 (32 columns), else 16-bit (64 columns).
+// Stores a box that TMA cannot store, from the staging buffer: a row at a time, a column
+// per lane, so that a warp's stores fall into the few sectors of one row.  kWords: fp32 (32
+// columns), else 16-bit (64 columns).
 template <bool kWords>
 __device__ __forceinline__ void ffn_store_rows(const FfnOut& o, const Stager& st, int n0) {
   __syncwarp();
@@ -228,6 +229,8 @@ __device__ __forceinline__ void ffn_store_rows(const FfnOut& o, const Stager& st
 }
 
 // Stores one box: the 128 bytes of this lane's row (64 16-bit or 32 fp32 columns from n0).
+// TMA leaves out what lies past the last column in pieces of 16 bytes only: a box with a
+// broken last piece would be written past the matrix, so it goes row by row.
 template <bool kWords>
 __device__ __forceinline__ void ffn_store_box(const FfnOut& o, const CUtensorMap* map,
                                               const Stager& st, int n0, const uint32_t (&v)[32]) {
@@ -235,7 +238,7 @@ __device__ __forceinline__ void ffn_store_box(const FfnOut& o, const CUtensorMap
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     st.put(k, make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
-  if (o.tma)
+  if (o.tma && (o.whole || n0 + (kWords ? kFfnBox / 2 : kFfnBox) <= st.N))
     st.issue(map, n0);
   else
     ffn_store_rows<kWords>(o, st, n0);

@@ -6,7 +6,8 @@ import torch
 import ffn_reference as ref
 import implicit_gemm_conv_tcgen05_gb300 as igc
 from gpu_helpers import check_device_ok
-from test_linear_act_gpu import BF16, F16, F32, d, generator, matrix, width  # noqa: F401
+from test_linear_act_gpu import (BF16, F16, F32, d, generator, matrix,  # noqa: F401
+                                 padded_out, width)
 
 pytestmark = pytest.mark.gpu
 
@@ -180,3 +181,27 @@ def test_backward_against_differences(name):
         ds, _ = ref.gated_dgu(d(c), d(G), d(U), name)
         spread = float(max(t.abs().max() for t in ds)) * base[at].numel() ** 0.5
         assert abs(got - want) <= 40 * 2.0 ** -11 * (terms + spread), (at, got, want)
+
+
+@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("F", [1, 67, 130, 133])
+def test_padding_of_outputs_is_kept(M, F, width):
+    """As for linear_act: nothing past the last column is written."""
+    x, wg, wu, bg, bu = make(M, F, 96, BF16, True, 70)
+    (H, hb), (G, gb), (U, ub) = (padded_out(M, F, BF16) for _ in range(3))
+    igc.gated_ffn(x, wg, wu, bg=bg, bu=bu, H=H, G=G, U=U)
+    gen = generator(M, F, 71)
+    x2 = matrix(gen, M, F, BF16)
+    wg2, wu2 = (matrix(gen, 72, F, BF16) for _ in range(2))
+    dh, g, u = (matrix(gen, M, 72, BF16) for _ in range(3))
+    (dX, xb), (dWg, wgb), (dWu, wub) = (padded_out(r, F, BF16) for r in (M, 72, 72))
+    igc.gated_ffn_backward(dh, g, u, x2, wg2, wu2, dX=dX, dWg=dWg, dWu=dWu)
+    check_device_ok()
+    wh, wG, wU = ref.gated(d(x), d(wg), d(wu), d(bg), d(bu), "silu", BF16)
+    ds, es = ref.gated_dgu(d(dh), d(g), d(u), "silu")
+    wx, ww, _ = ref.grads(ds, es, d(x2), [d(wg2), d(wu2)], BF16, BF16, F32)
+    for got, want, buf, what in ((H, wh, hb, "H"), (G, wG, gb, "G"), (U, wU, ub, "U"),
+                                 (dX, wx[0], xb, "dX"), (dWg, ww[0], wgb, "dWg"),
+                                 (dWu, ww[1], wub, "dWu")):
+        ref.check(got, want, what)
+        assert bool((buf[:, F:] == 9.0).all()), what

@@ -426,3 +426,32 @@ def test_forward_overflow_is_infinite(M):
     igc.linear_act(x, w, Y=Y, Z=Z)
     check_device_ok()
     assert bool((Y == 64 * 40000.0).all()) and bool(torch.isposinf(Z).all())
+
+
+def padded_out(rows, cols, dtype):
+    """An output whose rows are padded to 16 bytes and a little more, and the buffer."""
+    buf = torch.full((rows, -(-cols // 8) * 8 + 8), 9.0, device="cuda", dtype=dtype)
+    return buf[:, :cols], buf
+
+
+@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("n", [1, 3, 67, 129, 130, 133, 260])
+def test_padding_of_outputs_is_kept(M, n, width):
+    """Outputs with 16-byte aligned rows whose last columns do not fill 16 bytes: nothing
+    past them is written, in either direction's outputs."""
+    for dtype in (BF16, F32):
+        x, w, b, _ = make(M, n, 96, BF16, True, False, 30)
+        (Y, yb), (Z, zb) = padded_out(M, n, dtype), padded_out(M, n, BF16)
+        igc.linear_act(x, w, bias=b, act="silu", Y=Y, Z=Z)
+        gen = generator(M, n, 31)
+        x2, w2 = matrix(gen, M, n, BF16), matrix(gen, 72, n, BF16)
+        dy = matrix(gen, M, 72, BF16)
+        (dX, xb), (dW, wb) = padded_out(M, n, BF16), padded_out(72, n, dtype)
+        igc.linear_act_backward(dy, x2, w2, dX=dX, dW=dW)
+        check_device_ok()
+        want_y, want_z = ref.linear(d(x), d(w), d(b), "silu", None, dtype, BF16)
+        wx, ww, _ = ref.grads([d(dy)], [0 * d(dy)], d(x2), [d(w2)], BF16, dtype, F32)
+        for got, want, buf, what in ((Y, want_y, yb, "Y"), (Z, want_z, zb, "Z"),
+                                     (dX, wx[0], xb, "dX"), (dW, ww[0], wb, "dW")):
+            ref.check(got, want, what)
+            assert bool((buf[:, n:] == 9.0).all()), what
