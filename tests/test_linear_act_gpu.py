@@ -362,8 +362,10 @@ def test_backward_offsets_past_32_bits():
     ref.check(db, wb[0], "db")
 
 
-def test_backward_from_threads_on_one_stream():
-    """Calls of several host threads interleave on one stream; each has its own workspace."""
+@pytest.mark.parametrize("own_streams", [False, True])
+def test_backward_from_threads(own_streams):
+    """Calls of several host threads interleave on one stream, or run on streams of their
+    own; each thread has its own workspace."""
     import threading
     gen = generator(26)
     shapes = [(300, 200, 136), (70, 520, 264), (600, 72, 328), (128, 300, 200)]
@@ -377,7 +379,10 @@ def test_backward_from_threads_on_one_stream():
 
     def work(i):
         x, w, dy, z, _ = cases[i]
-        results[i] = [igc.linear_act_backward(dy, x, w, act="silu", Z=z)[:2] for _ in range(30)]
+        stream = torch.cuda.Stream() if own_streams else torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            results[i] = [igc.linear_act_backward(dy, x, w, act="silu", Z=z)[:2]
+                          for _ in range(30)]
 
     threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
     for t in threads:
