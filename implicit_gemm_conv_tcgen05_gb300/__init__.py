@@ -142,6 +142,8 @@ def lib() -> ctypes.CDLL:
             L.igc_plan_ffn.argtypes = [i32, i64, i64, i64, i32, i32,
                                        ctypes.POINTER(ctypes.c_int32)]
             L.igc_plan_ffn.restype = i32
+            L.igc_ffn_cta_resources.argtypes = L.igc_plan_ffn.argtypes
+            L.igc_ffn_cta_resources.restype = i32
             L.igc_version.argtypes = []
             L.igc_version.restype = ctypes.c_char_p
             _lib = L
@@ -840,6 +842,15 @@ def igc_plan_ffn(op: int, M: int, N: int, K: int, count: int = 1, sms: int = 152
     _check(lib().igc_plan_ffn(int(op), int(M), int(N), int(K), int(count), int(sms), out),
            "igc_plan_ffn")
     return dict(zip(_PLAN_FFN_FIELDS, (int(v) for v in out)))
+
+
+def _ffn_cta_resources(op: int, M: int, N: int, K: int, count: int = 1, sms: int = 152):
+    """(tensor-memory columns, bytes of dynamic shared memory) of a CTA of the kernel that
+    igc_plan_ffn answers."""
+    out = (ctypes.c_int32 * 2)()
+    _check(lib().igc_ffn_cta_resources(int(op), int(M), int(N), int(K), int(count), int(sms),
+                                       out), "igc_ffn_cta_resources")
+    return int(out[0]), int(out[1])
 
 
 def grad_norm_clip_workspace_size(count: int) -> int:

@@ -103,3 +103,9 @@ int ffn_dact(const DactArgs& a, bool gated, cudaStream_t stream);
 int ffn_dact_sums(const DactArgs& a, bool gated, bool late_wait, cudaStream_t stream);
 
 }  // namespace igc
+
+// For tests, through the binding: what a CTA of the kernel that igc_plan_ffn answers (the
+// same arguments) takes of an SM: out[0] tensor-memory columns, out[1] bytes of dynamic
+// shared memory.
+extern "C" int igc_ffn_cta_resources(int op, int64_t M, int64_t N, int64_t K, int count, int sms,
+                                     int32_t* out);

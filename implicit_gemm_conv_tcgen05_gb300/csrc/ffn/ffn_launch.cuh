@@ -258,7 +258,6 @@ int ffn_launch_tiles(const DeviceInfo& dev, const FfnProblem& q, int bn, cudaStr
 // ---------------------------------------------------------------------------
 constexpr size_t kSmallSmemTwo = 110 * 1024;  // two CTAs on an SM
 constexpr size_t kSmallSmemOne = 224 * 1024;
-constexpr size_t kSmemPerSm = 228 * 1024;
 
 // Clusters of 1 .. kSkMaxSplit CTAs that run at once with one CTA on an SM (they stay
 // within a GPC, whose SMs a larger cluster does not fill).
@@ -285,6 +284,28 @@ inline size_t small_part_bytes(int mt) { return static_cast<size_t>(mt) * kSkRow
 inline bool small_two_fit(int mt) {
   return small_part_bytes(mt) <= kSmallSmemTwo - 1024 &&
          3 * small_stage_bytes(mt) <= kSmallSmemTwo - 1024;
+}
+
+// What a CTA of the kernel takes: its 64-k blocks, ring stages, tensor-memory columns and
+// dynamic shared memory.
+struct SmallShape {
+  int per_cta = 1, stages = 1;
+  uint32_t tmem_cols = 32;
+  size_t smem = 0;
+};
+
+inline SmallShape small_shape(int mt, int atoms, int split) {
+  SmallShape s;
+  while (s.tmem_cols < static_cast<uint32_t>(mt)) s.tmem_cols *= 2;
+  s.per_cta = (atoms + split - 1) / split;
+  const size_t stage = small_stage_bytes(mt);
+  const size_t budget = (small_two_fit(mt) ? kSmallSmemTwo : kSmallSmemOne) - 1024;
+  const size_t stages = std::min(std::min(budget / stage, static_cast<size_t>(kSkMaxStages)),
+                                 static_cast<size_t>(s.per_cta));
+  s.stages = static_cast<int>(stages);
+  s.smem = std::max(1024 + std::max(stages * stage, small_part_bytes(mt)),
+                    tmem_smem_floor(s.tmem_cols));
+  return s;
 }
 
 // The number of output rows of a block and of CTAs that share one: the cheapest of the
@@ -388,25 +409,13 @@ int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const ProductPl
   p.M = static_cast<int>(q.M), p.N = static_cast<int>(q.N);
   p.m_blocks = plan.m_blocks;
   p.mt = plan.mt;
-  p.tmem_cols = 32;
-  while (p.tmem_cols < static_cast<uint32_t>(p.mt)) p.tmem_cols *= 2;
   p.atoms_seg = static_cast<int>((q.K + BK - 1) / BK);
   p.atoms = p.atoms_seg * q.segs;
   const long long blocks = (q.N + kOutT - 1) / kOutT * p.m_blocks * q.srcs;
   p.split = plan.split;
-  p.per_cta = (p.atoms + p.split - 1) / p.split;
   if (blocks * p.split > 0x7fffffffLL) return IGC_ERR_UNSUPPORTED;
-  const size_t stage = small_stage_bytes(p.mt), part = small_part_bytes(p.mt);
-  const size_t budget = (small_two_fit(p.mt) ? kSmallSmemTwo : kSmallSmemOne) - 1024;
-  size_t stages = budget / stage;
-  if (stages > kSkMaxStages) stages = kSkMaxStages;
-  if (stages > static_cast<size_t>(p.per_cta)) stages = static_cast<size_t>(p.per_cta);
-  p.stages = static_cast<int>(stages);
-  const size_t ring = stages * stage;
-  // No more CTAs on an SM than its 512 tensor-memory columns serve: a CTA waiting for
-  // columns that CTAs of other clusters hold, while those wait for its own cluster, would
-  // never get them.
-  const size_t spread = kSmemPerSm / (512 / p.tmem_cols + 1);
+  const SmallShape shape = small_shape(p.mt, p.atoms, p.split);
+  p.per_cta = shape.per_cta, p.stages = shape.stages, p.tmem_cols = shape.tmem_cols;
   p.late_wait = q.late_wait;
   // Weights past half of the L2 are gone before they are read again: marked to be evicted
   // first, they leave the lines that the next kernel prefetches alone (134 MB, one token:
@@ -437,7 +446,7 @@ int ffn_launch_small(const DeviceInfo& dev, const FfnProblem& q, const ProductPl
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks * p.split), 1, 1);
   cfg.blockDim = dim3(kSkThreads, 1, 1);
-  cfg.dynamicSmemBytes = std::max(1024 + std::max(ring, part), spread);
+  cfg.dynamicSmemBytes = shape.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -498,6 +507,22 @@ void ffn_plan_host(const FfnProblem& q, int sms, int32_t* out) {
   out[4] = p.small ? p.split : 1;
   out[5] = static_cast<int32_t>(std::min(small.us * 1000, 2e9));
   out[6] = static_cast<int32_t>(std::min(p.tiles_us * 1000, 2e9));
+}
+
+// Tensor-memory columns and dynamic shared memory of a CTA of that product's kernel.
+template <FfnOp kOp>
+void ffn_resources_host(const FfnProblem& q, const int32_t* plan, int32_t* out) {
+  if (plan[0]) {
+    const int atoms = static_cast<int>((q.K + BK - 1) / BK) * q.segs;
+    const SmallShape s = small_shape(plan[1], atoms, plan[4]);
+    out[0] = static_cast<int32_t>(s.tmem_cols), out[1] = static_cast<int32_t>(s.smem);
+  } else if (plan[3] == 256) {
+    out[0] = FfnCfg<kOp, 256>::kTmemCols, out[1] = FfnCfg<kOp, 256>::kSmemBytes;
+  } else if (plan[3] == 128) {
+    out[0] = FfnCfg<kOp, 128>::kTmemCols, out[1] = FfnCfg<kOp, 128>::kSmemBytes;
+  } else if constexpr (kOp == FfnOp::Linear) {
+    out[0] = FfnCfg<kOp, 192>::kTmemCols, out[1] = FfnCfg<kOp, 192>::kSmemBytes;
+  }
 }
 
 }  // namespace igc

@@ -50,24 +50,47 @@ int encode_tiled_2d_fresh(CUtensorMap* map, CUtensorMapDataType dtype, const voi
 
 using namespace igc;
 
-extern "C" int igc_plan_ffn(int op, int64_t M, int64_t N, int64_t K, int count, int sms,
-                            int32_t* out) {
-  if (out == nullptr || M <= 0 || N <= 0 || K <= 0 || sms < 2 || count < 1 || count > 2)
-    return IGC_ERR_INVALID_ARG;
+namespace {
+
+// igc_plan_ffn's plan and, where res is given, what a CTA of its kernel takes.
+int plan_host(int op, int64_t M, int64_t N, int64_t K, int count, int sms, int32_t* out,
+              int32_t* res) {
+  if (M <= 0 || N <= 0 || K <= 0 || sms < 2 || count < 1 || count > 2) return IGC_ERR_INVALID_ARG;
   if (!fits32(M) || !fits32(N) || !fits32(K)) return IGC_ERR_UNSUPPORTED;
   FfnProblem q;
   q.M = M, q.N = N, q.K = K;
   switch (op) {
-    case IGC_PLAN_FFN_LINEAR: ffn_plan_host<FfnOp::Linear>(q, sms, out); return IGC_OK;
-    case IGC_PLAN_FFN_GATED: ffn_plan_host<FfnOp::Gated>(q, sms, out); return IGC_OK;
+    case IGC_PLAN_FFN_LINEAR:
+      ffn_plan_host<FfnOp::Linear>(q, sms, out);
+      if (res != nullptr) ffn_resources_host<FfnOp::Linear>(q, out, res);
+      return IGC_OK;
+    case IGC_PLAN_FFN_GATED:
+      ffn_plan_host<FfnOp::Gated>(q, sms, out);
+      if (res != nullptr) ffn_resources_host<FfnOp::Gated>(q, out, res);
+      return IGC_OK;
     case IGC_PLAN_FFN_GRAD_X:
       q.N = K, q.K = N, q.segs = count;
       ffn_plan_host<FfnOp::GradX>(q, sms, out);
+      if (res != nullptr) ffn_resources_host<FfnOp::GradX>(q, out, res);
       return IGC_OK;
     case IGC_PLAN_FFN_GRAD_W:
       q.M = N, q.N = K, q.K = M, q.srcs = count;
       ffn_plan_host<FfnOp::GradW>(q, sms, out);
+      if (res != nullptr) ffn_resources_host<FfnOp::GradW>(q, out, res);
       return IGC_OK;
     default: return IGC_ERR_INVALID_ARG;
   }
+}
+
+}  // namespace
+
+extern "C" int igc_plan_ffn(int op, int64_t M, int64_t N, int64_t K, int count, int sms,
+                            int32_t* out) {
+  return out == nullptr ? IGC_ERR_INVALID_ARG : plan_host(op, M, N, K, count, sms, out, nullptr);
+}
+
+extern "C" int igc_ffn_cta_resources(int op, int64_t M, int64_t N, int64_t K, int count, int sms,
+                                     int32_t* out) {
+  int32_t plan[7];
+  return out == nullptr ? IGC_ERR_INVALID_ARG : plan_host(op, M, N, K, count, sms, plan, out);
 }

@@ -353,15 +353,15 @@ __global__ void __launch_bounds__(kSkThreads)
           part[(c + i) * kSkRows + quad * 32 + lane] = __uint_as_float(r[i]);
     }
   }
+  // The columns go back before anything is waited for in another CTA: no CTA of this kernel
+  // holds columns while it needs one that may itself still be waiting for some.
   tc_fence_before();
-  if (p.split > 1)
-    cluster_sync();
-  else
-    __syncthreads();
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_1cta(tmem, p.tmem_cols);
   }
+  if (p.split > 1) cluster_sync();
 
   // Outputs: 4 columns per step, the steps dealt over the cluster's threads.  A thread
   // takes several steps at a time (more of them where few partial sums are added), so that

@@ -56,6 +56,14 @@ constexpr int kFfnAtoms = 2;                       // 128-deep stages
 constexpr int kFfnKS = BK * kFfnAtoms;
 constexpr int kFfnBox = 64;  // columns of one epilogue box (128 bytes of a 16-bit output)
 
+// Least dynamic shared memory of a CTA that allocates `cols` columns of tensor memory.  An
+// SM has 512 of them, an allocation waits without limit for too few, and CTAs of any launch,
+// those of other streams among them, may share the SM.  So shared memory is asked for in
+// proportion: columns come in 32s, CTAs that together want more than 512 want 544 at least,
+// and 544 columns' worth is the whole of an SM's 228 KB, without what a CTA needs besides.
+constexpr size_t kSmemPerSm = 228 * 1024;
+constexpr size_t tmem_smem_floor(uint32_t cols) { return (kSmemPerSm * cols + 543) / 544; }
+
 template <FfnOp kOp, int BN>
 struct FfnCfg {
   static constexpr int kOutN = kOp == FfnOp::Gated ? BN / 2 : BN;  // output columns of a tile
@@ -70,9 +78,12 @@ struct FfnCfg {
       static_cast<int>((kSmemBudget - 2048 - kStagingBytes) / kStageBytes) > 8
           ? 8
           : static_cast<int>((kSmemBudget - 2048 - kStagingBytes) / kStageBytes);
-  static constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kStagingBytes + 1024;
   static constexpr uint32_t kAccStride = BN <= 128 ? 128 : 256;  // columns of an accumulator
   static constexpr uint32_t kTmemCols = 2 * kAccStride;
+  static constexpr size_t kSmemUsed = 1024 + kStages * kStageBytes + kStagingBytes + 1024;
+  static constexpr size_t kSmemBytes =
+      kSmemUsed > tmem_smem_floor(kTmemCols) ? kSmemUsed : tmem_smem_floor(kTmemCols);
+  static_assert(kSmemBytes <= kSmemBudget, "shared memory");
   static constexpr bool kHalves = BN == 256;  // column-half units in the last round
 };
 
