@@ -64,11 +64,13 @@ __device__ __forceinline__ void act_grad_f32(float z, float& f, float& d) {
     f = z * cdf;
     d = fmaf(z * kInvSqrt2Pi, exp2_approx((-0.5f * kLog2E) * z * z), cdf);
   } else if constexpr (kAct == IGC_ACT_GELU_TANH) {
-    // s (1 - s) is 0 long before z^2 reaches the bound, which keeps its factor finite
+    // s (1 - s) is 0 long before z^2 reaches the bound.  It meets z first and the polynomial
+    // then: both products stay finite for every finite z (z times the polynomial would not
+    // from 1.6e27 on, and infinity times 0 is NaN)
     const float z2 = fminf(z * z, 1e12f);
     const float s = sigmoid2(gelu_tanh_arg(z, z2));
     f = z * s;
-    d = fmaf(z * fmaf(6.0f * kGeluC * kGeluA, z2, 2.0f * kGeluC), fmaf(-s, s, s), s);
+    d = fmaf(z * fmaf(-s, s, s), fmaf(6.0f * kGeluC * kGeluA, z2, 2.0f * kGeluC), s);
   } else if constexpr (kAct == IGC_ACT_SILU) {
     const float s = sigmoid2(kLog2E * z);
     f = z * s;
