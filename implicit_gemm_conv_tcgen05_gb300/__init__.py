@@ -16,6 +16,7 @@ import ctypes
 import os
 import re
 import threading
+import weakref
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
@@ -631,19 +632,40 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-# Workspaces up to this size are kept for the next call of the same thread on the same
-# current stream (asking the allocator for one costs as much host time as the launches of
-# a small call); larger ones go back to the allocator when the call returns.
+# Workspaces up to this size are kept for the next call of the same thread on the default
+# stream (asking the allocator for one costs 3 to 6 us of host time in calls that take about
+# 20); larger ones go back to the allocator when the call returns.  Only the default stream's:
+# it is never destroyed, so its handle cannot come to name another stream, and a thread keeps
+# one workspace per device however many streams it uses.
 _KEPT_WORKSPACE_BYTES = 32 * 1024 * 1024
-_kept = threading.local()
+
+
+class _Kept:
+    """A thread's workspace for the default stream of each device."""
+
+    def __init__(self):
+        self.by_device = {}
+        with _lock:
+            _all_kept.add(self)
+
+
+_thread = threading.local()
+_all_kept = weakref.WeakSet()
+
+
+def release_workspaces():
+    """Gives the workspaces that the binding keeps between calls (at most 32 MB per thread
+    and device) back to torch's allocator, those of every thread; later calls get new ones."""
+    with _lock:
+        for kept in _all_kept:
+            kept.by_device.clear()
 
 
 def _workspace(workspace, need, like, stream):
-    """The workspace of a call: the one given, one kept by this thread for the current
+    """The workspace of a call: the one given, the one that this thread keeps for the default
     stream, or a new one.  Calls on one stream use it in stream order; another thread's
-    calls, which could come between a call's launches, have their own.  A call on a stream
-    named by the caller and one under graph capture (the graph goes on using it) get a new
-    one."""
+    calls, which could come between a call's launches, have their own.  A call on any other
+    stream and one under graph capture (the graph goes on using it) get a new one."""
     torch = _torch()
     if workspace is not None:
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -652,14 +674,18 @@ def _workspace(workspace, need, like, stream):
             raise ValueError("workspace is on another device")
         return workspace
     need = max(need, 1)
-    if stream is not None or need > _KEPT_WORKSPACE_BYTES or \
+    dev = like.get_device()
+    if stream is not None or need > _KEPT_WORKSPACE_BYTES or _handle(None, dev) != 0 or \
             torch.cuda.is_current_stream_capturing():
         return _new((need,), torch.uint8, like.device, stream)
-    dev = like.get_device()
-    key = (dev, _handle(None, dev))
-    kept = _kept.__dict__.get(key)
+    try:
+        by_device = _thread.kept.by_device
+    except AttributeError:
+        _thread.kept = _Kept()
+        by_device = _thread.kept.by_device
+    kept = by_device.get(dev)
     if kept is None or kept.numel() < need:
-        kept = _kept.__dict__[key] = _new((need,), torch.uint8, like.device, None)
+        kept = by_device[dev] = _new((need,), torch.uint8, like.device, None)
     return kept
 
 
