@@ -121,7 +121,7 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
     if (rc != IGC_OK) return rc;
   }
   // What follows reads what the activation's pass wrote and nothing of one another: each
-  // kernel but the first may run beside the one before it (late_wait).
+  // kernel but the first may run beside those before it (late_wait, ffn_dependency_wait).
   bool after_first = false;
   if (want_x) {
     rc = ffn_grad_x(dev, g, px, after_first, stream);

@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(256) sum_chunks_kernel(const float* partial0,
   const int n = blockIdx.x * 32 + lane;
   float t = 0.0f;
   if (n < N)
-    for (int c = warp; c < chunks; c += 8) t += partial[static_cast<long long>(c) * N + n];
+    // (from L2: with a late wait nothing has told this SM's L1 of the new sums)
+    for (int c = warp; c < chunks; c += 8) t += __ldcg(partial + static_cast<long long>(c) * N + n);
   red[warp][lane] = t;
   __syncthreads();
   if (warp == 0 && n < N) {

@@ -119,10 +119,14 @@ struct FfnParams {
 };
 
 // Programmatic dependent launch.  A kernel normally waits for the one before it in the
-// stream (kernel B) before it touches memory.  With `late` it shares no memory with B
-// that either of them writes, and B waited early itself: then everything before B is
-// complete once B's blocks have let this kernel start, and it may run beside B.  It still
-// waits for B before it ends, so that its own completion means B's to what comes next.
+// stream before it touches memory.  With `late` it may run beside it: they share no memory
+// that either of them writes, and what it does read is complete when it starts.  In a
+// backward pass A, B, C, D (the activation's pass, dX, dW, the bias sums) C and D are late
+// and read what A wrote.  B waits for A and lets C start only then, from every block; so C
+// starts after A's end, and D, which C's blocks let start, after that.  Both pass over A's
+// results in L2 (TMA, __ldcg), which is where a finished kernel's stores are.  A late kernel
+// waits for the one before it at its end: D's end means C's, C's means B's, so whatever
+// follows D in the stream finds all of them complete.
 __device__ __forceinline__ void ffn_dependency_wait(bool late) {
   if (!late) grid_dependency_wait();
   grid_dependents_launch();
