@@ -1,7 +1,5 @@
 // linear_act_backward and gated_ffn_backward: the pass through the activation (and the
 // bias gradients), then the two products of the tensor cores.
-#include <algorithm>
-
 #include "ffn_host.h"
 #include "launch.cuh"
 
@@ -82,10 +80,7 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
   const bool copy = (want_x || want_w) && (!identity || !operand_ok(dO.ptr, dO.ld));
   Mat D[2] = {{dO.ptr, dO.ld, dtype}, {}};
   // Plans of both products, whether or not both are asked for, so that a gradient does not
-  // depend on that.  Tiles of both that fit the SMs together run side by side; dX on the
-  // kernel for small outputs, which spreads over all SMs, leaves those of dW no room (509 x
-  // 1001 x 777 fp16: 9.3 and 8.2 us alone on tiles and 9.9 together, 16.2 with dX on the
-  // other kernel).
+  // depend on that.
   GradArgs g;
   g.M = M, g.N = N, g.K = K, g.dtype = dtype, g.count = n;
   g.D = D, g.W = W, g.X = X, g.dX = dX, g.dW = dW;
@@ -94,9 +89,7 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
     rc = ffn_plan_x(dev, g, &px);
     if (rc == IGC_OK) rc = ffn_plan_w(dev, g, &pw);
     if (rc != IGC_OK) return rc;
-    if (px.small && !pw.small && px.tile_ctas + pw.tile_ctas <= dev.sm_count &&
-        std::max(px.tiles_us, pw.tiles_us) < px.best_us + pw.best_us - 3.0)
-      px.small = false;
+    if (grad_x_beside_w(px, pw, dev.sm_count)) px.small = false;
   }
 
   DactArgs a;

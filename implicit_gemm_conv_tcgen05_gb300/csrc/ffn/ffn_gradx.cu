@@ -4,26 +4,13 @@
 
 namespace igc {
 
-namespace {
-
-FfnProblem sizes(const GradArgs& a) {
-  FfnProblem q;
-  q.M = a.M, q.N = a.K, q.K = a.N, q.dtype = a.dtype;
-  q.segs = q.count_a = q.count_b = a.count;
-  return q;
-}
-
-}  // namespace
-
 int ffn_plan_x(const DeviceInfo& dev, const GradArgs& a, ProductPlan* plan) {
-  FfnProblem q = sizes(a);
-  for (int i = 0; i < a.count; ++i) q.A[i] = packed_rows(a.N), q.B[i] = packed_rows(a.K);
-  return ffn_plan<FfnOp::GradX>(dev, q, plan);
+  return ffn_plan<FfnOp::GradX>(dev, grad_x_problem(a.M, a.N, a.K, a.dtype, a.count), plan);
 }
 
 int ffn_grad_x(const DeviceInfo& dev, const GradArgs& a, const ProductPlan& plan, bool late_wait,
                cudaStream_t stream) {
-  FfnProblem q = sizes(a);
+  FfnProblem q = grad_x_problem(a.M, a.N, a.K, a.dtype, a.count);
   for (int i = 0; i < a.count; ++i) q.A[i] = a.D[i], q.B[i] = a.W[i];
   q.out[0] = a.dX;
   q.late_wait = late_wait;

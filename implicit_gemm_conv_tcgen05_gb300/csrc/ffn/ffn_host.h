@@ -42,13 +42,24 @@ struct Mat {
 
 // How a product runs: on the kernel for small outputs (mt rows to a block, m_blocks of
 // them, split CTAs to each) or on 256-row tiles of bn columns (tile_ctas CTAs); the
-// estimated times of the better one and of the tiles.
+// estimated times of both.
 struct ProductPlan {
   bool small = false;
   int mt = 16, m_blocks = 1, split = 1;
   int bn = 256, tile_ctas = 0;
-  double best_us = 0.0, tiles_us = 0.0;
+  double small_us = 0.0, tiles_us = 0.0;
 };
+
+// Whether the dX of a backward pass goes to the tiles though the kernel for small outputs
+// is estimated faster.  Tiles of both products that fit the SMs together run side by side;
+// dX on the kernel for small outputs, which spreads over all SMs, leaves those of dW no room
+// (509 x 1001 x 777 fp16: 9.3 and 8.2 us alone on tiles and 9.9 together, 16.2 with dX on the
+// other kernel).
+inline bool grad_x_beside_w(const ProductPlan& x, const ProductPlan& w, int sms) {
+  const double beside = x.tiles_us > w.tiles_us ? x.tiles_us : w.tiles_us;
+  return x.small && !w.small && x.tile_ctas + w.tile_ctas <= sms &&
+         beside < x.small_us + w.tiles_us - 3.0;
+}
 
 // The products of a backward pass: dX = sum_s D[s] W[s] (ffn_gradx.cu) and dW[s] = D[s]^T X
 // (ffn_gradw.cu), D[s] M x N, W[s] and dW[s] N x K, X and dX M x K, s < count.  The plans go

@@ -148,6 +148,24 @@ inline Mat packed_rows(int64_t cols) {
   return m;
 }
 
+// The products of a backward pass as they are planned: dX = sum_s D[s] W[s] and
+// dW[s] = D[s]^T X over closely packed operands (D M x N, W N x K, X M x K).
+inline FfnProblem grad_x_problem(int64_t M, int64_t N, int64_t K, int dtype, int count) {
+  FfnProblem q;
+  q.M = M, q.N = K, q.K = N, q.dtype = dtype;
+  q.segs = q.count_a = q.count_b = count;
+  for (int i = 0; i < count; ++i) q.A[i] = packed_rows(N), q.B[i] = packed_rows(K);
+  return q;
+}
+inline FfnProblem grad_w_problem(int64_t M, int64_t N, int64_t K, int dtype, int count) {
+  FfnProblem q;
+  q.M = N, q.N = K, q.K = M, q.dtype = dtype;
+  q.srcs = q.count_a = count;
+  for (int i = 0; i < count; ++i) q.A[i] = packed_rows(N);
+  q.B[0] = packed_rows(K);
+  return q;
+}
+
 // Stored extents of operand i: MN-major operands have k as their rows.
 inline int ffn_map_a(CUtensorMap* map, const FfnProblem& q, int i, bool mn, int box_rows) {
   return mn ? ffn_operand_map(map, q.dtype, q.A[i], q.K, q.M, box_rows)
@@ -471,8 +489,7 @@ inline ProductPlan join_plans(const SmallPlan& small, const TilePlan& tiles) {
   p.small = small.us < tiles.us && tile_width_override() == 0;
   p.mt = small.mt, p.m_blocks = small.m_blocks, p.split = small.split;
   p.bn = tiles.bn, p.tile_ctas = tiles.ctas;
-  p.tiles_us = tiles.us;
-  p.best_us = p.small ? small.us : tiles.us;
+  p.small_us = small.us, p.tiles_us = tiles.us;
   return p;
 }
 
@@ -495,30 +512,33 @@ int ffn_launch(const DeviceInfo& dev, const FfnProblem& q, const ProductPlan& pl
                     : ffn_launch_tiles<kOp>(dev, q, plan.bn, stream);
 }
 
-// igc_plan_ffn for one product (see igc_ffn.h).
+// The plan of a product on a GPU of `sms` SMs.
 template <FfnOp kOp>
-void ffn_plan_host(const FfnProblem& q, int sms, int32_t* out) {
-  const SmallPlan small = small_plan<kOp>(q, sms, default_slots(sms));
-  const ProductPlan p = join_plans(small, tile_plan<kOp>(q, sms / 2));
+ProductPlan ffn_plan_host(const FfnProblem& q, int sms) {
+  return join_plans(small_plan<kOp>(q, sms, default_slots(sms)), tile_plan<kOp>(q, sms / 2));
+}
+
+// It in igc_plan_ffn's form (see igc_ffn.h).
+inline void ffn_plan_out(const FfnProblem& q, const ProductPlan& p, int32_t* out) {
   out[0] = p.small;
   out[1] = p.small ? p.mt : BM;
   out[2] = p.small ? p.m_blocks : static_cast<int32_t>((q.M + BM - 1) / BM);
   out[3] = p.small ? kSkRows : p.bn;
   out[4] = p.small ? p.split : 1;
-  out[5] = static_cast<int32_t>(std::min(small.us * 1000, 2e9));
+  out[5] = static_cast<int32_t>(std::min(p.small_us * 1000, 2e9));
   out[6] = static_cast<int32_t>(std::min(p.tiles_us * 1000, 2e9));
 }
 
 // Tensor-memory columns and dynamic shared memory of a CTA of that product's kernel.
 template <FfnOp kOp>
-void ffn_resources_host(const FfnProblem& q, const int32_t* plan, int32_t* out) {
-  if (plan[0]) {
+void ffn_resources_host(const FfnProblem& q, const ProductPlan& p, int32_t* out) {
+  if (p.small) {
     const int atoms = static_cast<int>((q.K + BK - 1) / BK) * q.segs;
-    const SmallShape s = small_shape(plan[1], atoms, plan[4]);
+    const SmallShape s = small_shape(p.mt, atoms, p.split);
     out[0] = static_cast<int32_t>(s.tmem_cols), out[1] = static_cast<int32_t>(s.smem);
-  } else if (plan[3] == 256) {
+  } else if (p.bn == 256) {
     out[0] = FfnCfg<kOp, 256>::kTmemCols, out[1] = FfnCfg<kOp, 256>::kSmemBytes;
-  } else if (plan[3] == 128) {
+  } else if (p.bn == 128) {
     out[0] = FfnCfg<kOp, 128>::kTmemCols, out[1] = FfnCfg<kOp, 128>::kSmemBytes;
   } else if constexpr (kOp == FfnOp::Linear) {
     out[0] = FfnCfg<kOp, 192>::kTmemCols, out[1] = FfnCfg<kOp, 192>::kSmemBytes;

@@ -173,15 +173,16 @@ int grad_norm_clip(int64_t count, const void *const *grads, const int64_t *sizes
  * `sms` SMs, computed on the host by the launches' own decision functions.
  *
  *  op     IGC_PLAN_FFN_LINEAR, _GATED (the forward products), _GRAD_X, _GRAD_W (the
- *         products of the backward passes); M, N (or F), K are the operator's sizes,
- *         rows taken to start on 128-byte lines (a call's forward product goes by its own
- *         operands' alignment, the products of a backward pass by their sizes alone).
+ *         products of the backward passes); M, N (or F), K are the operator's sizes.  A
+ *         call's forward product goes by its own operands' alignment too; here their rows
+ *         are taken to start on 128-byte lines.  The products of a backward pass go by the
+ *         sizes alone, in the call and here.
  *  count  1 for linear_act_backward's products, 2 for gated_ffn_backward's.
  *  out    int32[7]: 0 = 256-row tiles, 1 = the kernel for small outputs; output rows of a
  *         tile or block; their number; its columns of the MMA (of both weights for _GATED);
  *         CTAs that share the contraction of a block; the estimated times of the small and
- *         of the tile kernel in nanoseconds.  (A backward pass takes dX to the tiles where
- *         its own then run beside dW's.)
+ *         of the tile kernel in nanoseconds.  The shorter of these is the choice, but for
+ *         _GRAD_X, which also goes to the tiles where its own then run beside dW's.
  */
 #define IGC_PLAN_FFN_LINEAR 0
 #define IGC_PLAN_FFN_GATED 1
