@@ -110,6 +110,8 @@ constexpr uint32_t kBarrierBytes = 1536;
 // swizzle, the layout of a TMA box) and writes them with one bulk tensor store.
 constexpr uint32_t kStagingWarpBytes = 32 * 128;
 constexpr uint32_t kStagingBytes = kEpiWarps * kStagingWarpBytes;
+// KParams::tma_out: an output (shifted by its slot) whose rows are no whole 16-byte pieces
+constexpr int kTmaRagged = 16;
 constexpr size_t kSmemBudget = 227 * 1024;
 constexpr int kIntChunkKb = 1024 / KS;  // stages per exact fp32 accumulation chunk (1024 k)
 
@@ -277,7 +279,8 @@ struct KParams {
   float scale;
   const float* scale_col;
   // bit i set: output i is written by TMA stores through tensor map tmO<i>
-  // (float modes: 0 = out, 1 = out_f32; integer modes: 0 = c32, 1 = c8, 2 = yf)
+  // (float modes: 0 = out, 1 = out_f32; integer modes: 0 = c32, 1 = c8, 2 = yf);
+  // kTmaRagged << i: its rows are no whole 16-byte pieces (tma_cols)
   int tma_out;
   // dequantised float output of the int8 path: y = ((fp32(C32) * dq_row_i) * dq_col_j) + bias_j
   float* yf;
@@ -914,6 +917,13 @@ __device__ __forceinline__ void store_cols_f32(float* out, long long ldo, int N,
   }
 }
 
+// Whether the nc columns from n0 of output `slot` go by TMA stores.  These clip a row
+// at N in 16-byte pieces, so where the last one is broken the columns that reach N go
+// by direct stores.
+__device__ __forceinline__ bool tma_cols(const KParams& p, int slot, int n0, int nc) {
+  return ((p.tma_out >> slot) & 1) && (!(p.tma_out & (kTmaRagged << slot)) || n0 + nc <= p.N);
+}
+
 // One epilogue warp's staging buffer: lane l owns row l (128 bytes) of a 32-row
 // TMA box; 16-byte chunk k of the row sits at chunk k ^ (l % 8) (128-byte swizzle).
 struct Stager {
@@ -989,7 +999,7 @@ __device__ __forceinline__ void store_row_float(const KParams& p, const CUtensor
   const int boxed32 = nvalid / 32 * 32;  // columns stored by whole 32-bit boxes
   const bool in_row = m < p.M;
   if (p.out != nullptr) {
-    const bool tma = p.tma_out & 1;
+    const bool tma = tma_cols(p, 0, n0, NC);
     if (p.out_type == kOutF16) {
       if (tma) stage_store_16bit<NC, false>(st, &tmO0, n0, v, nvalid);
       if (in_row)
@@ -1006,7 +1016,7 @@ __device__ __forceinline__ void store_row_float(const KParams& p, const CUtensor
     }
   }
   if (p.out_f32 != nullptr) {
-    const bool tma = p.tma_out & 2;
+    const bool tma = tma_cols(p, 1, n0, NC);
     if (tma) stage_store_u32<NC>(st, &tmO1, n0, v, nvalid);
     if (in_row)
       store_cols_f32<NC>(p.out_f32, p.ldo32, p.N, m, n0, p.vec_ok, tma ? boxed32 : 0, nvalid, v);
@@ -1181,11 +1191,13 @@ __device__ __forceinline__ void store_row_int_v(const KParams& p, const CUtensor
                                                 const uint32_t (&sum)[NC], const IntRow& r,
                                                 const ColVecs<NC>& V) {
   const bool in_row = m < p.M;
-  const bool full = p.vec_ok && (n0 + NC <= p.N);
+  // a direct 16-byte store of group j's columns stays inside the row
+  auto vec = [&](int j) { return p.vec_ok && n0 + (j + 1) * kG <= p.N; };
   // int8 (requantised)
   if (p.c8) {
+    const bool tma8 = NC >= 128 && tma_cols(p, 1, n0, NC);
     if constexpr (NC >= 128) {
-      if (p.tma_out & 2) {
+      if (tma8) {
 #pragma unroll
         for (int b = 0; b < NC / 128; ++b) {
           st.begin();
@@ -1201,7 +1213,7 @@ __device__ __forceinline__ void store_row_int_v(const KParams& p, const CUtensor
         }
       }
     }
-    if (!(NC >= 128 && (p.tma_out & 2))) {
+    if (!tma8) {
       // every lane computes (the column values are shuffled across the warp);
       // rows past M store nothing
       int8_t* row8 = p.c8 + static_cast<size_t>(in_row ? m : 0) * p.ldc8 + n0;
@@ -1212,7 +1224,7 @@ __device__ __forceinline__ void store_row_int_v(const KParams& p, const CUtensor
         int_group<NC>(p, r, V, sum, j, c);
         int8_group<NC>(p, V, j, c, w);
         if (!in_row) continue;
-        if (full) {
+        if (vec(j)) {
           reinterpret_cast<uint4*>(row8)[j] = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
@@ -1229,7 +1241,7 @@ __device__ __forceinline__ void store_row_int_v(const KParams& p, const CUtensor
   for (int o = 0; o < (kDequant ? 2 : 1); ++o) {
     void* outp = o == 0 ? static_cast<void*>(p.c32) : static_cast<void*>(p.yf);
     if (outp == nullptr) continue;
-    const bool tma = (p.tma_out >> (o == 0 ? 0 : 2)) & 1;
+    const bool tma = tma_cols(p, o == 0 ? 0 : 2, n0, NC);
     const CUtensorMap* map = o == 0 ? &tmO0 : &tmO2;
     const long long ld = o == 0 ? p.ldc32 : p.ldyf;
     uint32_t* row = reinterpret_cast<uint32_t*>(outp) + static_cast<size_t>(in_row ? m : 0) * ld + n0;
@@ -1253,7 +1265,7 @@ __device__ __forceinline__ void store_row_int_v(const KParams& p, const CUtensor
           for (int i = 0; i < 4; ++i)
             st.put(g * 4 + i, make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]));
         } else if (in_row) {
-          if (full) {
+          if (vec(j)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               reinterpret_cast<uint4*>(row + j * kG)[i] =

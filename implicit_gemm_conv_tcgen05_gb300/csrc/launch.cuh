@@ -76,7 +76,8 @@ int kernel_setup(const DeviceInfo& dev, int* max_clusters) {
 }
 
 // Tensor maps of the outputs written by bulk tensor stores from the epilogue's
-// staging buffers; bit i of mask enables map i (the others are never read).
+// staging buffers; bit i of mask enables map i (the others are never read), bit
+// kTmaRagged << i marks an output whose rows are no whole 16-byte pieces.
 struct OutMaps {
   CUtensorMap map[3] = {};
   int mask = 0;
@@ -85,14 +86,17 @@ struct OutMaps {
 // Enables output slot `slot` (an M x N row-major matrix, row stride ld elements
 // of esize bytes) for bulk tensor stores when its base and row stride are
 // 16-byte aligned; boxes are 32 rows x 128 bytes, 128-byte swizzled.  Otherwise
-// the slot stays on direct stores.
+// the slot stays on direct stores.  The bulk stores clip at N in 16-byte pieces: a
+// broken last piece would be written past the row's end, so a slot whose rows have
+// one is marked (kTmaRagged) and its last columns go by direct stores.
 inline void add_out_map(OutMaps& o, int slot, CUtensorMapDataType dtype, const void* ptr,
                         long long ld, long long M, long long N, size_t esize) {
   if (ptr == nullptr || !vec_store_ok(ptr, ld, esize)) return;
   if (encode_tiled_2d(&o.map[slot], dtype, ptr, static_cast<uint64_t>(N),
                       static_cast<uint64_t>(M), static_cast<uint64_t>(ld) * esize,
                       static_cast<uint32_t>(128 / esize), 32) == IGC_OK)
-    o.mask |= 1 << slot;
+    o.mask |= (1 << slot) |
+              (static_cast<unsigned long long>(N) * esize % 16 != 0 ? kTmaRagged << slot : 0);
 }
 
 // First unit index of the column-half tail: when the last round of the schedule

@@ -29,9 +29,10 @@
  *    igc_check_device_status() reports it as IGC_ERR_DEVICE_TIMEOUT.
  *  - Alignment: operand base pointers must be 16-byte aligned and operand row
  *    strides (in bytes) multiples of 16 (TMA rules), else IGC_ERR_MISALIGNED.
- *    Outputs may have any alignment; outputs whose base and row stride are
- *    16-byte aligned are written by TMA bulk tensor stores, others by direct
- *    stores.
+ *    Outputs may have any alignment (of their elements); outputs whose base and
+ *    row stride are 16-byte aligned are written by TMA bulk tensor stores, others
+ *    by direct stores.  Nothing past an output's last column is written: row
+ *    strides may skip columns that belong to something else.
  *  - Device: an sm_103 GPU (GB300); any other returns IGC_ERR_UNSUPPORTED.
  *  - Calls are stateless and re-entrant; concurrent calls on different streams
  *    are independent (each gemm_s8_zp call needs its own workspace).  The
