@@ -183,6 +183,18 @@ int encode_tiled_2d_swizzle(CUtensorMap* map, CUtensorMapDataType dtype, const v
     *map = slot.map;
     return IGC_OK;
   }
+  const int rc = encode_tiled_2d_fresh(map, dtype, base, inner, rows, row_stride_bytes, box_inner,
+                                       box_rows, swizzle);
+  if (rc != IGC_OK) return rc;
+  slot.key = key;
+  slot.map = *map;
+  slot.valid = true;
+  return IGC_OK;
+}
+
+int encode_tiled_2d_fresh(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                          uint64_t inner, uint64_t rows, uint64_t row_stride_bytes,
+                          uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
   load_encoders();
   if (!g_encode_tiled) return IGC_ERR_CUDA;
   cuuint64_t dims[2] = {inner, rows};
@@ -193,11 +205,7 @@ int encode_tiled_2d_swizzle(CUtensorMap* map, CUtensorMapDataType dtype, const v
                               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return IGC_ERR_CUDA;
-  slot.key = key;
-  slot.map = *map;
-  slot.valid = true;
-  return IGC_OK;
+  return r == CUDA_SUCCESS ? IGC_OK : IGC_ERR_CUDA;
 }
 
 int encode_im2col_nhwc(CUtensorMap* map, const void* base, int N, int H, int W, int C,

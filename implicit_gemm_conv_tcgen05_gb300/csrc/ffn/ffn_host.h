@@ -27,12 +27,6 @@ inline bool rows_aligned(const void* p, int64_t ld, size_t esize, size_t to) {
 // An M x N 16-bit operand that TMA reads.
 inline bool operand_ok(const void* p, int64_t ld) { return rows_aligned(p, ld, 2, 16); }
 
-// A tensor map of a row-major matrix, 128-byte swizzled (encode_tiled_2d without its store
-// of recent maps: nothing is kept from one call to the next).  In ffn_plan.cu.
-int encode_tiled_2d_fresh(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
-                          uint64_t inner, uint64_t rows, uint64_t row_stride_bytes,
-                          uint32_t box_inner, uint32_t box_rows);
-
 // A matrix of the interface: pointer, row stride, element type.
 struct Mat {
   const void* ptr = nullptr;

@@ -1,52 +1,6 @@
-// Tensor maps of the feed-forward launches, and igc_plan_ffn: the kernel and schedule that
-// a product of the feed-forward operators runs with, from the launches' own decision
-// functions, on the host.
+// igc_plan_ffn: the kernel and schedule that a product of the feed-forward operators runs
+// with, from the launches' own decision functions, on the host.
 #include "ffn_launch.cuh"
-
-namespace igc {
-
-namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled through the runtime (the library does not link libcuda).
-EncodeTiledFn encoder() {
-  static std::once_flag once;
-  static EncodeTiledFn fn = nullptr;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
-}  // namespace
-
-int encode_tiled_2d_fresh(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
-                          uint64_t inner, uint64_t rows, uint64_t row_stride_bytes,
-                          uint32_t box_inner, uint32_t box_rows) {
-  const EncodeTiledFn encode = encoder();
-  if (encode == nullptr) return IGC_ERR_CUDA;
-  const cuuint64_t dims[2] = {inner, rows};
-  const cuuint64_t strides[1] = {row_stride_bytes};
-  const cuuint32_t box[2] = {box_inner, box_rows};
-  const cuuint32_t steps[2] = {1, 1};
-  return encode(map, dtype, 2, const_cast<void*>(base), dims, strides, box, steps,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? IGC_OK
-             : IGC_ERR_CUDA;
-}
-
-}  // namespace igc
 
 using namespace igc;
 

@@ -50,6 +50,12 @@ int encode_tiled_2d_swizzle(CUtensorMap* map, CUtensorMapDataType dtype, const v
                             uint64_t inner, uint64_t rows, uint64_t row_stride_bytes,
                             uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// The same, encoded anew each time (the two above keep the calling thread's recent maps).
+int encode_tiled_2d_fresh(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                          uint64_t inner, uint64_t rows, uint64_t row_stride_bytes,
+                          uint32_t box_inner, uint32_t box_rows,
+                          CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+
 int encode_im2col_nhwc(CUtensorMap* map, const void* base, int N, int H, int W, int C,
                        int lower_h, int lower_w, int upper_h, int upper_w, uint32_t channels,
                        uint32_t pixels, int stride_h, int stride_w);
