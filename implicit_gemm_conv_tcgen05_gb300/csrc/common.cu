@@ -239,7 +239,7 @@ const char* igc_status_string(int status) {
   switch (status) {
     case IGC_OK: return "ok";
     case IGC_ERR_INVALID_ARG: return "invalid argument";
-    case IGC_ERR_MISALIGNED: return "operand pointer or row stride not 16-byte aligned";
+    case IGC_ERR_MISALIGNED: return "a pointer or row stride is not aligned as the call asks (operands: 16 bytes)";
     case IGC_ERR_UNSUPPORTED: return "unsupported shape, parameter or device";
     case IGC_ERR_CUDA: return "CUDA runtime or driver call failed";
     case IGC_ERR_DEVICE_TIMEOUT: return "a kernel pipeline wait timed out";

@@ -60,7 +60,14 @@ int backward(int64_t M, int64_t N, int64_t K, int dtype, int act, bool gated, co
     if (want_w && !operand_ok(X.ptr, X.ld)) return IGC_ERR_MISALIGNED;
     for (int i = 0; i < n; ++i)
       if (want_x && !operand_ok(W[i].ptr, W[i].ld)) return IGC_ERR_MISALIGNED;
+    if (!elements_aligned(dO, U) || ((gated || act != IGC_ACT_NONE) && !elements_aligned(Z)))
+      return IGC_ERR_MISALIGNED;
   }
+  if ((want_x && !elements_aligned(dX)) ||
+      (want_b && !elements_aligned(Mat{db[0], N, db_dtype}, Mat{db[1], N, db_dtype})))
+    return IGC_ERR_MISALIGNED;
+  for (int i = 0; i < n; ++i)
+    if (want_w && !elements_aligned(dW[i])) return IGC_ERR_MISALIGNED;
 
   DeviceInfo dev;
   int rc = current_device(&dev);

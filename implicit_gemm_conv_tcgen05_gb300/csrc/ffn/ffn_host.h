@@ -34,6 +34,13 @@ struct Mat {
   int dtype = IGC_F32;
 };
 
+// Whether every matrix or vector starts on a boundary of its elements (null ones do): loads
+// and stores of whole elements fault the GPU elsewhere.
+template <typename... M>
+bool elements_aligned(const M&... m) {
+  return ((reinterpret_cast<uintptr_t>(m.ptr) % elem_size(m.dtype) == 0) && ...);
+}
+
 // How a product runs: on the kernel for small outputs (mt rows to a block, m_blocks of
 // them, split CTAs to each) or on 256-row tiles of bn columns (tile_ctas CTAs); the
 // estimated times of both.

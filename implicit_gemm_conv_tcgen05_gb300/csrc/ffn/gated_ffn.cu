@@ -24,12 +24,15 @@ extern "C" int gated_ffn(int64_t M, int64_t F, int64_t K, int dtype, const void*
   if (!fits32(M) || !fits32(F) || !fits32(K)) return IGC_ERR_UNSUPPORTED;
   if (K > 0 && (!operand_ok(X, ldx) || !operand_ok(Wg, ldw) || !operand_ok(Wu, ldw)))
     return IGC_ERR_MISALIGNED;
+  const Mat outs[3] = {{H, ldh, dtype}, {G, ldgu, dtype}, {U, ldgu, dtype}};
+  if (!elements_aligned(outs[0], outs[1], outs[2], Mat{bg, F, bias_dtype},
+                        Mat{bu, F, bias_dtype}))
+    return IGC_ERR_MISALIGNED;
 
   DeviceInfo dev;
   int rc = current_device(&dev);
   if (rc != IGC_OK) return rc;
 
-  const Mat outs[3] = {{H, ldh, dtype}, {G, ldgu, dtype}, {U, ldgu, dtype}};
   if (K == 0) {
     PointwiseArgs a;
     a.M = M, a.N = F, a.dtype = dtype, a.act = act;

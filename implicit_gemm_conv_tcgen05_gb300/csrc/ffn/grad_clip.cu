@@ -332,6 +332,7 @@ int grad_norm_clip(int64_t count, const void* const* grads, const int64_t* sizes
   if (count > 0 && (grads == nullptr || sizes == nullptr || dtypes == nullptr))
     return IGC_ERR_INVALID_ARG;
   if (count > 0x3fffffff) return IGC_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(norm) % sizeof(float) != 0) return IGC_ERR_MISALIGNED;
   for (int64_t i = 0; i < count; ++i) {
     if (sizes[i] < 0) return IGC_ERR_INVALID_ARG;
     if (dtypes[i] != IGC_F32 && !is_operand_type(dtypes[i])) return IGC_ERR_INVALID_ARG;

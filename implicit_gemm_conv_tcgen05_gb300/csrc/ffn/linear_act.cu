@@ -21,12 +21,14 @@ extern "C" int linear_act(int64_t M, int64_t N, int64_t K, int dtype, const void
   if (R == Y && (ldr != ldy || y_dtype != dtype)) return IGC_ERR_INVALID_ARG;
   if (!fits32(M) || !fits32(N) || !fits32(K)) return IGC_ERR_UNSUPPORTED;
   if (K > 0 && (!operand_ok(X, ldx) || !operand_ok(W, ldw))) return IGC_ERR_MISALIGNED;
+  const Mat outs[2] = {{Y, ldy, y_dtype}, {Z, ldz, dtype}};
+  if (!elements_aligned(outs[0], outs[1], Mat{R, ldr, dtype}, Mat{bias, N, bias_dtype}))
+    return IGC_ERR_MISALIGNED;
 
   DeviceInfo dev;
   int rc = current_device(&dev);
   if (rc != IGC_OK) return rc;
 
-  const Mat outs[2] = {{Y, ldy, y_dtype}, {Z, ldz, dtype}};
   if (K == 0) {
     PointwiseArgs a;
     a.M = M, a.N = N, a.dtype = dtype, a.act = act;

@@ -61,7 +61,8 @@ typedef struct CUstream_st *igc_stream_t;
 /* status codes */
 #define IGC_OK 0
 #define IGC_ERR_INVALID_ARG 1    /* null required pointer, negative size, ld < K, no output */
-#define IGC_ERR_MISALIGNED 2     /* operand pointer / row stride breaks the 16-byte TMA rules */
+#define IGC_ERR_MISALIGNED 2     /* operand pointer / row stride breaks the 16-byte TMA rules, or a
+                                     pointer is no multiple of its element size (igc_ffn.h) */
 #define IGC_ERR_UNSUPPORTED 3    /* shape or device outside what the kernels implement */
 #define IGC_ERR_CUDA 4           /* a CUDA runtime / driver call failed */
 #define IGC_ERR_DEVICE_TIMEOUT 5 /* a kernel's bounded pipeline wait gave up */

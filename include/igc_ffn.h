@@ -10,8 +10,9 @@
  *    fp32; a result is rounded once, to nearest even, where it is stored.
  *  - Matrices are row-major with a row stride (ld*) in elements, at least their
  *    number of columns.  X, W, Wg and Wu, which are read by TMA, must be 16-byte
- *    aligned with row strides that are multiples of 8 (else IGC_ERR_MISALIGNED);
- *    every other matrix and every vector may have any alignment and stride.
+ *    aligned with row strides that are multiples of 8; every other matrix and
+ *    every vector may start at any multiple of its element's size and have any
+ *    stride.  Anything else is IGC_ERR_MISALIGNED.
  *  - Sizes: any M, N, F, K >= 0 that fit 32 bits.  An empty output is a no-op.
  *    A contraction of length zero is an empty sum: zeros.
  *  - Aliasing: outputs must not overlap inputs or each other (the kernels of a call
