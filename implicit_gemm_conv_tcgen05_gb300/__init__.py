@@ -536,6 +536,9 @@ def conv2d_nhwc_s8_zp(x, w, zX, zW=0, zW_k=None, y32=None, y8=None, scale=0.0, s
 
 # ---------------------------------------------------------------------------
 # feed-forward operators (include/igc_ffn.h)
+#
+# None of them takes part in autograd: results carry no history, also of tensors that
+# require a gradient; the *_backward functions are called for the gradients.
 # ---------------------------------------------------------------------------
 
 _ACTS = {"none": IGC_ACT_NONE, "relu": IGC_ACT_RELU, "gelu": IGC_ACT_GELU,
@@ -692,8 +695,9 @@ def _workspace(workspace, need, like, stream):
 def linear_act(X, W, bias=None, act="none", residual=None, Y=None, Z=None, stream=None):
     """Y = act(X W^T + bias) + residual; X (M,K), W (N,K), residual and Z (M,N) of one
     type (fp16 or bf16), Y (M,N) of that type or fp32, bias (N) of that type or fp32.
-    Z, if given, receives the pre-activation for linear_act_backward.  residual may be
-    Y itself.  Returns Y (allocated if None)."""
+    Z, if given, receives the pre-activation for linear_act_backward, which is to be
+    called for the gradients: the result has no autograd history.  residual may be Y
+    itself.  Returns Y (allocated if None)."""
     dtype = X.dtype
     dt = _operand_code(X, "X")
     code = _act_code(act)
@@ -726,7 +730,8 @@ def linear_act_backward(dY, X, W, act="none", Z=None, dX=None, dW=None, dbias=No
     """Gradients of linear_act from dY (M,N) and the pre-activation Z (M,N) that it kept
     (not needed without an activation): dX (M,K), dW (N,K), dbias (N).  The ones given
     are computed (X is needed for dW, W for dX; the other may be None); with none
-    given, dX and dW are allocated.  dW and dbias may be fp32.  Returns (dX, dW, dbias)."""
+    given, dX and dW are allocated.  dW and dbias may be fp32.  No tensor's .grad is
+    touched.  Returns (dX, dW, dbias)."""
     dtype = dY.dtype
     dt = _operand_code(dY, "dY")
     code = _act_code(act)
@@ -770,7 +775,8 @@ def gated_ffn(X, Wg, Wu, bg=None, bu=None, act="silu", H=None, G=None, U=None, s
     """H = act(X Wg^T + bg) * (X Wu^T + bu); X (M,K), Wg and Wu (F,K) with one row stride
     (two matrices, or the halves of a (2F,K) one), H (M,F), all of one type (fp16 or
     bf16); bg and bu (F) of that type or fp32.  G and U, if given, receive the two
-    pre-activations for gated_ffn_backward.  Returns H (allocated if None)."""
+    pre-activations for gated_ffn_backward, which is to be called for the gradients: the
+    result has no autograd history.  Returns H (allocated if None)."""
     dtype = X.dtype
     dt = _operand_code(X, "X")
     code = _act_code(act)
@@ -810,8 +816,8 @@ def gated_ffn_backward(dH, G, U, X, Wg, Wu, act="silu", dX=None, dWg=None, dWu=N
     """Gradients of gated_ffn from dH (M,F) and the pre-activations G and U (M,F) that it
     kept: dX (M,K), dWg and dWu (F,K), dbg and dbu (F).  The ones given are computed
     (the pairs go together; X is needed for the weights', Wg and Wu for dX); with none
-    given, dX, dWg and dWu are allocated.  The weights' and biases' may be fp32.
-    Returns (dX, dWg, dWu, dbg, dbu)."""
+    given, dX, dWg and dWu are allocated.  The weights' and biases' may be fp32.  No
+    tensor's .grad is touched.  Returns (dX, dWg, dWu, dbg, dbu)."""
     dtype = dH.dtype
     dt = _operand_code(dH, "dH")
     code = _act_code(act)

@@ -25,6 +25,9 @@
  *      IGC_ACT_GELU       z (1 + erf(z / sqrt(2))) / 2
  *      IGC_ACT_GELU_TANH  z (1 + tanh(c (z + 0.044715 z^3))) / 2
  *      IGC_ACT_SILU       z / (1 + exp(-z))
+ *    They are computed in fp32 with approximate exponentials and reciprocals (relative errors
+ *    of 2^-22 and 2^-23) and are within 1e-5 |z|, their derivatives within 1e-5 (1 + |z|):
+ *    no more than the rounding of a 16-bit result hides, but visible in an fp32 Y.
  *  - Workspaces: 256-byte aligned device memory of at least the size that the
  *    *_workspace_size function gives, not shared with a concurrent call; nothing
  *    in one need survive between calls.
@@ -85,7 +88,9 @@ int linear_act(int64_t M, int64_t N, int64_t K, int dtype,
  *  dbias    device vector of N elements of type dbias_dtype (IGC_F32 or dtype).
  *
  *  dZ is rounded to dtype before the two products (it is an operand of the tensor
- *  cores); dbias sums the unrounded values in fp32.
+ *  cores), to the type's precision and range: in fp16 a dZ past 65504 is infinite and one
+ *  below 2^-25 is 0, and so is its part in dX and dW.  dbias sums the unrounded values in
+ *  fp32.
  */
 size_t linear_act_backward_workspace_size(int64_t M, int64_t N, int64_t K);
 int linear_act_backward(int64_t M, int64_t N, int64_t K, int dtype,
@@ -132,8 +137,9 @@ int gated_ffn(int64_t M, int64_t F, int64_t K, int dtype,
  *  dWg, dWu device F x K of type dw_dtype (IGC_F32 or dtype), row stride lddw.
  *  dbg, dbu device vectors of F elements of type dbias_dtype (IGC_F32 or dtype).
  *
- *  dG and dU are rounded to dtype before the products; dbg and dbu sum the unrounded
- *  values in fp32.
+ *  dG and dU are rounded to dtype before the products, with the range that dZ has in
+ *  linear_act_backward: fp16 gradients want a loss scale that keeps dH U act'(G) within
+ *  65504.  dbg and dbu sum the unrounded values in fp32.
  */
 size_t gated_ffn_backward_workspace_size(int64_t M, int64_t F, int64_t K);
 int gated_ffn_backward(int64_t M, int64_t F, int64_t K, int dtype,
