@@ -57,7 +57,7 @@ struct ProductPlan {
 // Both gradients, device time with this rule and without, in us (linear; g: gated, with the
 // activation's pass): 509 x 1001 x 777 10.6 and 16.2, 77 x 486 x 2638 9.1 and 12.5, 603 x
 // 976 x 769 10.9 and 10.6, g 350 x 432 x 1407 12.8 and 17.2, g 1907 x 2489 x 467 31.9 and 39.7;
-// of 21 sizes that it holds for it was the faster at 20.  dX by itself would be 2 to 8 us
+// of 21 sizes that it holds for it was the faster at 20.  dX by itself would be up to 8 us
 // faster on the other kernel there (9.9 and 7.8 at the first size) and stays on the tiles, so
 // that its bits do not depend on what else is asked for.
 inline bool grad_x_beside_w(const ProductPlan& x, const ProductPlan& w, int sms) {

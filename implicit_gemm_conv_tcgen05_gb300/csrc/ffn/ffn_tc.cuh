@@ -28,8 +28,9 @@
 // and every box that the epilogue moves through shared memory costs the main loop a little.
 // Measured (bf16, bursts): 8192^3 without an epilogue 565 us, 1945 TFLOP/s (the vendor
 // library 558); tanh-GELU + 4, residual + 13, Z kept + 17.  Gated 8192 x 16384 x 4096 with G
-// and U kept 1125 us, 1955 TFLOP/s; its dX and dW 1120 us each.  Under the power limit of a
-// long run: 684, 1286 and 2825 us (the whole backward pass).
+// and U kept 1132 us, 1943 TFLOP/s (the vendor's product alone 1090); its dX and dW 1120 us each.
+// Under the power limit of a long run: 687 to 706, 1279 to 1318 and 2795 to 2887 us (the whole
+// backward pass).
 //
 // Warps (384 threads): 0 TMA producer, 1 tensor-memory owner and (leader CTA) MMA
 // issuer, 2-3 idle, 4-11 epilogue.  Two accumulators let the epilogue of one tile
