@@ -10,7 +10,7 @@ from test_ffn_cpu import clip, gated, gated_bwd, linear, linear_bwd
 
 MISALIGNED = igc.IGC_ERR_MISALIGNED
 F32, F16 = igc.IGC_F32, igc.IGC_F16
-P, Q, R, S, T = (ctypes.c_void_p((1 << 24) * i) for i in range(1, 6))
+P, Q = (ctypes.c_void_p((1 << 24) * i) for i in (1, 2))
 
 
 def off(p, by):
