@@ -23,6 +23,7 @@ _ROOT = os.path.dirname(_PKG)
 HEADER = os.path.join(_ROOT, "include", "igc.h")
 DEBUG_HEADER = os.path.join(_ROOT, "include", "igc_debug.h")
 FFN_HEADER = os.path.join(_ROOT, "include", "igc_ffn.h")
+LAYERS_HEADER = os.path.join(_ROOT, "include", "igc_layers.h")
 
 IGC_OK = 0
 IGC_ERR_INVALID_ARG = 1
@@ -145,6 +146,27 @@ def lib() -> ctypes.CDLL:
             L.igc_plan_ffn.restype = i32
             L.igc_ffn_cta_resources.argtypes = L.igc_plan_ffn.argtypes
             L.igc_ffn_cta_resources.restype = i32
+            f64, u64 = ctypes.c_double, ctypes.c_uint64
+            L.dropout_add.argtypes = [i64, i64, vp, i64, i32, vp, i64, f64, u64, u64, vp, vp, i64,
+                                      i32, vp]
+            L.dropout_add.restype = i32
+            L.layer_norm.argtypes = [i64, i64, i32, vp, i64, vp, i64, i32, f64, u64, u64, vp, vp,
+                                     vp, i32, f32, vp, i64, vp, i64, vp, vp, vp]
+            L.layer_norm.restype = i32
+            L.layer_norm_backward.argtypes = [i64, i64, i32, vp, i64, vp, i64, i32, vp, vp, vp,
+                                              i32, vp, i64, f64, u64, u64, vp, vp, i64, vp, i64,
+                                              vp, vp, i32, vp, sz, vp]
+            L.layer_norm_backward.restype = i32
+            L.layer_norm_backward_workspace_size.argtypes = [i64, i64]
+            L.layer_norm_backward_workspace_size.restype = sz
+            L.embedding_lookup.argtypes = [i64, i64, i64, vp, i32, vp, i64, i32, f32, vp, i64, i32,
+                                           vp]
+            L.embedding_lookup.restype = i32
+            L.embedding_backward.argtypes = [i64, i64, i64, vp, i32, vp, i64, i32, f32, i32, vp,
+                                             i64, i32, vp, sz, vp]
+            L.embedding_backward.restype = i32
+            L.embedding_backward_workspace_size.argtypes = [i64, i64, i64]
+            L.embedding_backward_workspace_size.restype = sz
             L.igc_version.argtypes = []
             L.igc_version.restype = ctypes.c_char_p
             _lib = L
@@ -939,3 +961,243 @@ def grad_norm_clip(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=Non
                               ws.numel(), _handle(stream, dev))
     _check(rc, "grad_norm_clip")
     return norm
+
+
+# ---------------------------------------------------------------------------
+# embedding, layer norm and dropout (include/igc_layers.h)
+#
+# As the feed-forward operators they take no part in autograd: the *_backward functions are
+# called for the gradients (that of dropout_add is dropout_add on the gradient).
+# ---------------------------------------------------------------------------
+
+def _type_code(t, name):
+    code = _dtype_code(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}: fp32, fp16 or bf16 is needed")
+    return code
+
+
+def _type_or_f32(dtype):
+    f32 = _torch().float32
+    return (dtype,) if dtype is f32 else (dtype, f32)
+
+
+def _drop_args(p, seed, offset, step, dev):
+    """(p, seed, offset, pointer of step) of a call with dropout."""
+    p = float(p)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p is {p}: a probability is needed")
+    if seed is None:
+        if p > 0.0:
+            raise ValueError("seed is needed with p > 0")
+        seed = 0
+    if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
+        raise ValueError("seed and offset must be in [0, 2^64)")
+    if step is None:
+        return p, seed, offset, None
+    if step.dtype != _torch().int64 or step.numel() != 1:
+        raise ValueError("step must be a one-element int64 tensor")
+    if step.get_device() != dev:
+        raise ValueError("step is on another device")
+    return p, seed, offset, step.data_ptr()
+
+
+def _floats(v, name, n, dev):
+    """Pointer of an optional fp32 vector of n elements."""
+    return _vector(v, name, (_torch().float32,), n, dev)[0]
+
+
+def dropout_add(X, p, seed=None, offset=0, step=None, residual=None, Y=None, stream=None):
+    """Y = residual + drop(X): each element of X (M,N) is kept and scaled with probability
+    1 - p (to a multiple of 1/65536), else 0.  Which ones follows from (seed, offset, row,
+    column) and is computed again where it is needed, never stored; calls with other seeds or
+    offsets are independent.  step, a one-element int64 CUDA tensor, is added to offset when
+    the kernel runs (for captured graphs).  X, Y and residual (M,N) fp32, fp16 or bf16;
+    residual has Y's type, which is X's unless one of them is fp32.  Y may be X or residual.
+    The gradient of X is dropout_add(dY, p, seed, offset, step), that of residual dY.
+    Returns Y (allocated if None, of residual's type, else X's)."""
+    xt = _type_code(X, "X")
+    M, N = _two_dims(X, "X")
+    dev = X.get_device()
+    like = Y if Y is not None else (residual if residual is not None else X)
+    yt = _type_code(like, "Y" if like is Y else "residual")
+    if xt != yt and xt != IGC_F32 and yt != IGC_F32:
+        raise TypeError(f"X has dtype {X.dtype}, the output {like.dtype}")
+    x, ldx = _mat(X, "X", (X.dtype,), M, N, dev)
+    r, ldr = _mat(residual, "residual", (like.dtype,), M, N, dev)
+    y, ldy = _mat(Y, "Y", (like.dtype,), M, N, dev)
+    p, seed, offset, step = _drop_args(p, seed, offset, step, dev)
+    _check_device(dev, "X")
+    if Y is None:
+        Y = _new((M, N), like.dtype, X.device, stream)
+        y, ldy = Y.data_ptr(), N
+    _check(lib().dropout_add(M, N, x, ldx, xt, r, ldr, p, seed, offset, step, y, ldy, yt,
+                             _handle(stream, dev)), "dropout_add")
+    return Y
+
+
+def layer_norm(X, w=None, b=None, eps=1e-5, residual=None, p=0.0, seed=None, offset=0, step=None,
+               Y=None, S=None, mean=None, rstd=None, stream=None):
+    """S = residual + drop(X) and Y = (S - mean) rstd w + b over the rows of S, in one pass.
+    X and Y (M,N) of one type (fp32, fp16 or bf16), residual and S (M,N) of that type or
+    fp32, w and b (N) of that type or fp32.  Dropout (p, seed, offset, step) as in
+    dropout_add.  Without residual and dropout S is X, which may then be fp32 whatever Y is.
+    S, mean and rstd (M, fp32), if given, receive what layer_norm_backward needs, which is to
+    be called for the gradients: the result has no autograd history.  S may be residual
+    itself.  Returns Y (allocated if None, of X's type)."""
+    M, N = _two_dims(X, "X")
+    _type_code(X, "X")
+    dev = X.get_device()
+    dtype = X.dtype if Y is None else Y.dtype
+    dt = _dtype_code(dtype)
+    if dt is None:
+        raise TypeError(f"Y has dtype {dtype}: fp32, fp16 or bf16 is needed")
+    own, either = (dtype,), _type_or_f32(dtype)
+    drop = _drop_args(p, seed, offset, step, dev)
+    if residual is None and drop[0] == 0.0:
+        x, ldx = None, 0
+        r, ldr = _mat(X, "X", either, M, N, dev)      # the stream itself
+        s_dtype = X.dtype
+    else:
+        x, ldx = _mat(X, "X", own, M, N, dev)
+        r, ldr = _mat(residual, "residual", either, M, N, dev)
+        s_dtype = residual.dtype if residual is not None else (dtype if S is None else S.dtype)
+    s, lds = _mat(S, "S", either if residual is None and x is not None else (s_dtype,), M, N, dev)
+    y, ldy = _mat(Y, "Y", own, M, N, dev)
+    wp, wt = _vector(w, "w", either, N, dev)
+    bp, bt = _vector(b, "b", either, N, dev)
+    if w is not None and b is not None and wt != bt:
+        raise ValueError("w and b must have one type")
+    m, rs = _floats(mean, "mean", M, dev), _floats(rstd, "rstd", M, dev)
+    _check_device(dev, "X")
+    if Y is None:
+        Y = _new((M, N), dtype, X.device, stream)
+        y, ldy = Y.data_ptr(), N
+    _check(lib().layer_norm(M, N, dt, x, ldx, r, ldr, _dtype_code(s_dtype), *drop, wp, bp,
+                            wt if w is not None else bt, float(eps), s, lds, y, ldy, m, rs,
+                            _handle(stream, dev)), "layer_norm")
+    return Y
+
+
+def layer_norm_backward_workspace_size(M: int, N: int) -> int:
+    return int(lib().layer_norm_backward_workspace_size(M, N))
+
+
+def layer_norm_backward(dY, S, mean, rstd, w=None, dS_add=None, p=0.0, seed=None, offset=0,
+                        step=None, dS=None, dX=None, dw=None, db=None, workspace=None,
+                        stream=None):
+    """Gradients of layer_norm from dY (M,N) and the S (M,N), mean and rstd (M) that it kept:
+    dS (M,N), that of S and so of the residual, with dS_add (the gradient that reaches S past
+    the norm) added; dX (M,N), that of X, through the dropout of the same (p, seed, offset,
+    step); dw and db (N).  The ones given are computed; with none given, dS, dw and db are
+    allocated (dw and db in fp32).  dX has dY's type; S, dS_add and dS are of that type or
+    fp32, all the same; w, dw and db of dY's type or fp32.  dS may be dS_add itself.  No
+    tensor's .grad is touched.  Returns (dS, dX, dw, db)."""
+    dt = _type_code(dY, "dY")
+    M, N = _two_dims(dY, "dY")
+    dev = dY.get_device()
+    torch = _torch()
+    drop = _drop_args(p, seed, offset, step, dev)
+    own, either = (dY.dtype,), _type_or_f32(dY.dtype)
+    y, ldy = _mat(dY, "dY", own, M, N, dev)
+    s, lds = _mat(S, "S", either, M, N, dev)
+    stream_type = (S.dtype,)
+    a, lda = _mat(dS_add, "dS_add", stream_type, M, N, dev)
+    m, rs = _floats(mean, "mean", M, dev), _floats(rstd, "rstd", M, dev)
+    if m is None or rs is None:
+        raise ValueError("mean and rstd are needed")
+    wp, wt = _vector(w, "w", either, N, dev)
+    if dS is None and dX is None and dw is None and db is None:
+        dS = _new((M, N), S.dtype, dY.device, stream)
+        dw, db = (_new((N,), torch.float32, dY.device, stream) for _ in range(2))
+    ds, ldds = _mat(dS, "dS", stream_type, M, N, dev)
+    dx, lddx = _mat(dX, "dX", own, M, N, dev)
+    dwp, dwt = _vector(dw, "dw", either, N, dev)
+    dbp, dbt = _vector(db, "db", either, N, dev)
+    if dw is not None and db is not None and dwt != dbt:
+        raise ValueError("dw and db must have one type")
+    _check_device(dev, "dY")
+    L = lib()
+    ws, n = None, 0
+    if dw is not None or db is not None:
+        ws = _workspace(workspace, L.layer_norm_backward_workspace_size(M, N), dY, stream)
+        ws, n = ws.data_ptr(), ws.numel()
+    _check(L.layer_norm_backward(M, N, dt, y, ldy, s, lds, _dtype_code(S.dtype), m, rs, wp, wt, a,
+                                 lda, *drop, ds, ldds, dx, lddx, dwp, dbp,
+                                 dwt if dw is not None else dbt, ws, n, _handle(stream, dev)),
+           "layer_norm_backward")
+    return dS, dX, dw, db
+
+
+def _tokens(tokens, dev):
+    """(pointer, length, bytes of an element) of a vector of token ids."""
+    torch = _torch()
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"tokens has dtype {tokens.dtype}: int32 or int64 is needed")
+    if tokens.dim() != 1 or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous vector")
+    if tokens.get_device() != dev:
+        raise ValueError("tokens is on another device")
+    return tokens.data_ptr(), tokens.shape[0], tokens.element_size()
+
+
+def embedding_lookup(tokens, W, scale=1.0, Y=None, stream=None):
+    """Y[i] = scale W[tokens[i]]: tokens (M) int32 or int64, W (V,D) fp32, fp16 or bf16, Y (M,D)
+    of that type or fp32.  A token outside [0, V) gives a row of zeros.  The result has no
+    autograd history (embedding_backward).  Returns Y (allocated if None, of W's type)."""
+    wt = _type_code(W, "W")
+    V, D = _two_dims(W, "W")
+    dev = W.get_device()
+    tp, M, size = _tokens(tokens, dev)
+    w, ldw = _mat(W, "W", (W.dtype,), V, D, dev)
+    y, ldy = _mat(Y, "Y", _type_or_f32(W.dtype), M, D, dev)
+    _check_device(dev, "W")
+    if Y is None:
+        Y = _new((M, D), W.dtype, W.device, stream)
+        y, ldy = Y.data_ptr(), D
+    _check(lib().embedding_lookup(M, V, D, tp, size, w, ldw, wt, float(scale), y, ldy,
+                                  _dtype_code(Y.dtype), _handle(stream, dev)),
+           "embedding_lookup")
+    return Y
+
+
+def embedding_backward_workspace_size(M: int, V: int, D: int) -> int:
+    return int(lib().embedding_backward_workspace_size(M, V, D))
+
+
+def embedding_backward(tokens, dY, V=None, scale=1.0, dW=None, accumulate=False, workspace=None,
+                       stream=None):
+    """dW[v] = scale * sum of dY[i] over the positions i with tokens[i] = v: dY (M,D) fp32, fp16
+    or bf16, dW (V,D) of that type or fp32 (allocated in dY's type for V rows if None).  All of
+    dW is written, or with accumulate the sums are added to the rows that tokens point to.
+    Returns dW."""
+    yt = _type_code(dY, "dY")
+    M, D = _two_dims(dY, "dY")
+    dev = dY.get_device()
+    tp, n, size = _tokens(tokens, dev)
+    if n != M:
+        raise ValueError(f"tokens has {n} elements, dY {M} rows")
+    if dW is None:
+        if V is None or accumulate:
+            raise ValueError("dW is needed to accumulate" if accumulate else
+                             "V, the rows of dW, is needed without dW")
+    elif V is not None and V != _two_dims(dW, "dW")[0]:
+        raise ValueError(f"dW has {dW.shape[0]} rows, V is {V}")
+    else:
+        V = _two_dims(dW, "dW")[0]
+    y, ldy = _mat(dY, "dY", (dY.dtype,), M, D, dev)
+    w, ldw = _mat(dW, "dW", _type_or_f32(dY.dtype), V, D, dev)
+    _check_device(dev, "dY")
+    if dW is None:
+        dW = _new((V, D), dY.dtype, dY.device, stream)
+        w, ldw = dW.data_ptr(), D
+    L = lib()
+    need = L.embedding_backward_workspace_size(M, V, D)
+    ws, nbytes = None, 0
+    if need > 0:
+        ws = _workspace(workspace, need, dY, stream)
+        ws, nbytes = ws.data_ptr(), ws.numel()
+    _check(L.embedding_backward(M, V, D, tp, size, y, ldy, yt, float(scale), int(bool(accumulate)),
+                                w, ldw, _dtype_code(dW.dtype), ws, nbytes,
+                                _handle(stream, dev)), "embedding_backward")
+    return dW

@@ -2,8 +2,8 @@
 
     python -m implicit_gemm_conv_tcgen05_gb300.build [--force] [--ptxas-verbose]
 
-Each .cu translation unit under csrc/ and csrc/ffn/ is compiled in parallel to an object
-file, then linked into _build/libigc.so (CUDA runtime linked statically, so
+Each .cu translation unit under csrc/, csrc/ffn/ and csrc/layers/ is compiled in parallel to
+an object file, then linked into _build/libigc.so (CUDA runtime linked statically, so
 the library loads without a GPU; the driver API is reached through the
 runtime's driver entry point).  No GPU is needed to build.
 """
@@ -21,13 +21,14 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 FFN = os.path.join(CSRC, "ffn")
+LAYERS = os.path.join(CSRC, "layers")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libigc.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
-                     "-I" + INCLUDE, "-I" + CSRC, "-I" + FFN]
+                     "-I" + INCLUDE, "-I" + CSRC, "-I" + FFN, "-I" + LAYERS]
 
 
 def _nvcc() -> str:
@@ -38,11 +39,11 @@ def _nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(FFN, "*.cu")))
+    return sorted(s for d in (CSRC, FFN, LAYERS) for s in glob.glob(os.path.join(d, "*.cu")))
 
 
 def _deps():
-    headers = [h for d in (CSRC, FFN, INCLUDE) for pat in ("*.cuh", "*.h")
+    headers = [h for d in (CSRC, FFN, LAYERS, INCLUDE) for pat in ("*.cuh", "*.h")
                for h in glob.glob(os.path.join(d, pat))]
     return _sources() + headers + [os.path.abspath(__file__)]
 
@@ -55,7 +56,7 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True) -> str:
-    """Compile every csrc/*.cu and csrc/ffn/*.cu and link _build/libigc.so; returns its path."""
+    """Compile every .cu of csrc, csrc/ffn and csrc/layers and link _build/libigc.so; returns its path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

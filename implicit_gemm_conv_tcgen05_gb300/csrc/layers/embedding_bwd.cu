@@ -1,0 +1,482 @@
+// embedding_backward: dW[v] = scale * sum of dY[i] over the positions i of token v.
+//
+// Bound by memory: dY is read once and dW written once (a training batch touches a small part of
+// a large table: most of the time goes to the zeros of the rest).
+//
+// Few positions: one launch.  A block per position (and 1024 columns) looks through all tokens;
+// the block of a token's first position adds the rows of all its positions, in order.  Further
+// blocks write the zeros of the rows that no token points to.
+//
+// Many: the positions are sorted by token first (stable, so that a token's positions stay in
+// order), by a cluster of eight blocks with a radix sort.  Blocks then walk chunks of 32 sorted
+// positions and write each token's sum; the sums of a token that crosses a chunk's border go to
+// the workspace, and a last kernel adds them in order.  No atomics on sums.
+#include "layers_host.h"
+
+namespace igc {
+
+namespace {
+
+constexpr int kThreads = 128;       // of a block over 1024 columns
+constexpr int kSmallM = 1024;       // positions up to which one launch does
+constexpr int kChunk = 32;          // sorted positions of a block
+constexpr int kCtas = 8;            // of the sorting cluster
+constexpr int kSortThreads = 1024, kSortWarps = kCtas * (kSortThreads / 32);
+constexpr int kMaxDigit = 512;      // values of a digit of the radix sort
+
+struct EmbedParams {
+  int M, D, vec, token64, accumulate;
+  int slabs;                 // blocks of 1024 columns to a row
+  int zero_rows;             // rows of a block that writes zeros
+  long long V;
+  const void* tokens;
+  const void* dY;
+  void* dW;
+  long long lddy, lddw;
+  float scale;
+  uint32_t* keys[2];         // sorted tokens (V: none of the table's), and their positions
+  uint32_t* pos[2];
+  uint32_t* touched;         // a bit for each row of dW that a token points to
+  float* partial;            // [chunk][2][D]: sums of a chunk's first and last token
+  int digit_bits, passes;
+};
+
+__device__ __forceinline__ long long token_at(const EmbedParams& p, int i) {
+  return p.token64 ? static_cast<const long long*>(p.tokens)[i]
+                   : static_cast<const int*>(p.tokens)[i];
+}
+
+// dW[v] (8 columns) = scale * acc, added to what is there when accumulating.
+template <int kW>
+__device__ __forceinline__ void finish8(const EmbedParams& p, long long v, int n, bool vec,
+                                        const float (&acc)[8]) {
+  char* row = row_at<kW>(p.dW, v, p.lddw);
+  float out[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) out[j] = acc[j] * p.scale;
+  if (p.accumulate) {
+    float old[8];
+    unpack8<kW>(load8<kW>(row, n, p.D, vec), old);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[j] += old[j];
+  }
+  store8<kW>(row, n, p.D, vec, out);
+}
+
+template <int kY>
+__device__ __forceinline__ void add_row8(const EmbedParams& p, long long i, int n, bool vec,
+                                         float (&acc)[8]) {
+  float f[8];
+  unpack8<kY>(load8<kY>(row_at<kY>(p.dY, i, p.lddy), n, p.D, vec), f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] += f[j];
+}
+
+template <int kW>
+__device__ __forceinline__ void zero_row(const EmbedParams& p, long long v, bool vec) {
+  const float zero[8] = {};
+  char* row = row_at<kW>(p.dW, v, p.lddw);
+  for (long long n = threadIdx.x * 8; n < p.D; n += kThreads * 8)
+    store8<kW>(row, static_cast<int>(n), p.D, vec, zero);
+}
+
+// ---------------------------------------------------------------------------
+// few positions
+// ---------------------------------------------------------------------------
+template <int kY, int kW>
+__global__ void __launch_bounds__(kThreads) embed_small_kernel(const EmbedParams p) {
+  __shared__ uint32_t bits[kSmallM / 32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const bool vec = p.vec != 0;
+  const long long token_blocks = static_cast<long long>(p.M) * p.slabs;
+  if (blockIdx.x >= token_blocks) {
+    // the rows [v0, v1): bits says which a token points to
+    const long long v0 = (blockIdx.x - token_blocks) * p.zero_rows;
+    const long long v1 = min(p.V, v0 + p.zero_rows);
+    if (threadIdx.x < 2) bits[threadIdx.x] = 0;
+    __syncthreads();
+    for (int j = threadIdx.x; j < p.M; j += kThreads) {
+      const long long v = token_at(p, j);
+      if (v >= v0 && v < v1) atomicOr(&bits[(v - v0) / 32], 1u << ((v - v0) % 32));
+    }
+    __syncthreads();
+    for (long long v = v0; v < v1; ++v)
+      if (!(bits[(v - v0) / 32] >> ((v - v0) % 32) & 1u)) zero_row<kW>(p, v, vec);
+    return;
+  }
+  const int i = static_cast<int>(blockIdx.x / p.slabs);
+  const long long v = token_at(p, i);
+  if (v < 0 || v >= p.V) return;
+  // bit j: position j holds the same token
+  const int words = (p.M + 31) / 32;
+  for (int j0 = 0; j0 < words * 32; j0 += kThreads) {
+    const int j = j0 + static_cast<int>(threadIdx.x);
+    const uint32_t same = __ballot_sync(0xffffffffu, j < p.M && token_at(p, min(j, p.M - 1)) == v);
+    if (threadIdx.x % 32 == 0 && j / 32 < words) bits[j / 32] = same;
+  }
+  __syncthreads();
+  for (int k = 0; k < i / 32; ++k)
+    if (bits[k] != 0) return;
+  if (bits[i / 32] & ((1u << (i % 32)) - 1u)) return;
+  const int n = (static_cast<int>(blockIdx.x % p.slabs) * kThreads + static_cast<int>(threadIdx.x)) * 8;
+  if (n >= p.D) return;
+  float acc[8] = {};
+  for (int k = i / 32; k < words; ++k) {
+    for (uint32_t left = bits[k]; left != 0; left &= left - 1)
+      add_row8<kY>(p, k * 32 + __ffs(static_cast<int>(left)) - 1, n, vec, acc);
+  }
+  finish8<kW>(p, v, n, vec, acc);
+}
+
+// ---------------------------------------------------------------------------
+// many positions: the sort
+// ---------------------------------------------------------------------------
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
+    embed_sort_kernel(const EmbedParams p) {
+  extern __shared__ uint32_t hist[];  // [32 warps][digits]: counts, then places
+  __shared__ uint32_t total[kMaxDigit], base[kMaxDigit], scan[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int digits = 1 << p.digit_bits;
+  const uint32_t below = (1u << lane) - 1u;
+  // each warp of the cluster has a run of positions, and counts and places it by itself
+  const int run = ((p.M + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+  const long long first = static_cast<long long>(rank * (kSortThreads / 32) + warp) * run;
+  const int steps = first < p.M ? static_cast<int>((min(static_cast<long long>(run), p.M - first) + 31) / 32) : 0;
+  uint32_t* mine = hist + warp * digits;
+  if (p.touched != nullptr)
+    for (long long k = static_cast<long long>(rank) * kSortThreads + threadIdx.x;
+         k < (p.V + 31) / 32; k += kCtas * kSortThreads)
+      p.touched[k] = 0;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.digit_bits;
+    const uint32_t* keys_in = p.keys[(pass + p.passes) & 1];
+    const uint32_t* pos_in = p.pos[(pass + p.passes) & 1];
+    uint32_t* keys_out = p.keys[(pass + p.passes + 1) & 1];
+    uint32_t* pos_out = p.pos[(pass + p.passes + 1) & 1];
+    auto key_at = [&](long long i) -> uint32_t {
+      if (pass > 0) return __ldcg(keys_in + i);
+      const long long v = token_at(p, static_cast<int>(i));
+      return static_cast<uint32_t>(v >= 0 && v < p.V ? v : p.V);
+    };
+    auto digit_of = [&](uint32_t key) {
+      return (key >> shift) & static_cast<uint32_t>(digits - 1);
+    };
+    for (int d = lane; d < digits; d += 32) mine[d] = 0;
+    __syncwarp();
+    for (int k = 0; k < steps; ++k) {
+      const long long i = first + k * 32 + lane;
+      const bool valid = i < p.M;
+      const uint32_t d = valid ? digit_of(key_at(i)) : 0xffffffffu;
+      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      if (valid && (peers & below) == 0) mine[d] += __popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    // the warps' counts become places within the block's share of a digit
+    const int d = static_cast<int>(threadIdx.x);
+    if (d < digits) {
+      uint32_t sum = 0;
+      for (int w = 0; w < kSortThreads / 32; ++w) {
+        const uint32_t c = hist[w * digits + d];
+        hist[w * digits + d] = sum;
+        sum += c;
+      }
+      total[d] = sum;
+    }
+    cluster_sync();
+    // smaller digits of all blocks, then the same digit of the blocks before this one
+    uint32_t all = 0, before = 0;
+    if (d < digits) {
+#pragma unroll
+      for (int c = 0; c < kCtas; ++c) {
+        const uint32_t v =
+            ld_shared_cluster_u32(mapa_shared(smem_u32(total + d), static_cast<uint32_t>(c)));
+        all += v;
+        if (c < rank) before += v;
+      }
+    }
+    uint32_t upto = all;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    uint32_t ahead = 0;
+    for (int w = 0; w < warp; ++w) ahead += scan[w];
+    if (d < digits) base[d] = ahead + upto - all + before;
+    __syncthreads();
+    for (int k = 0; k < steps; ++k) {
+      const long long i = first + k * 32 + lane;
+      const bool valid = i < p.M;
+      uint32_t key = 0, dg = 0xffffffffu;
+      if (valid) {
+        key = key_at(i);
+        dg = digit_of(key);
+      }
+      const uint32_t peers = __match_any_sync(0xffffffffu, dg);
+      if (valid) {
+        const uint32_t at = base[dg] + mine[dg] + __popc(peers & below);
+        keys_out[at] = key;
+        pos_out[at] = pass > 0 ? __ldcg(pos_in + i) : static_cast<uint32_t>(i);
+        if (pass == 0 && p.touched != nullptr && key < p.V)
+          atomicOr(p.touched + key / 32, 1u << (key % 32));
+      }
+      __syncwarp();
+      if (valid && (peers & below) == 0) mine[dg] += __popc(peers);
+      __syncwarp();
+    }
+    cluster_sync();  // what the next pass, and a block's reads of the others' totals, rely on
+  }
+}
+
+// ---------------------------------------------------------------------------
+// many positions: the sums
+// ---------------------------------------------------------------------------
+template <int kY, int kW>
+__global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams p) {
+  __shared__ uint32_t keys[kChunk + 2], pos[kChunk];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const bool vec = p.vec != 0;
+  const int chunks = (p.M + kChunk - 1) / kChunk;
+  const long long sum_blocks = static_cast<long long>(chunks) * p.slabs;
+  if (blockIdx.x >= sum_blocks) {
+    const long long v0 = (blockIdx.x - sum_blocks) * p.zero_rows;
+    const long long v1 = min(p.V, v0 + p.zero_rows);
+    for (long long v = v0; v < v1; ++v)
+      if (!(p.touched[v / 32] >> (v % 32) & 1u)) zero_row<kW>(p, v, vec);
+    return;
+  }
+  const int c = static_cast<int>(blockIdx.x / p.slabs);
+  const long long p0 = static_cast<long long>(c) * kChunk;
+  const uint32_t none = static_cast<uint32_t>(p.V);
+  // keys[k + 1]: token of the chunk's position k; a token that is not in the table before the
+  // first position, after the last, and for what is not to be summed
+  if (threadIdx.x < kChunk + 2) {
+    const long long at = p0 + static_cast<int>(threadIdx.x) - 1;
+    keys[threadIdx.x] = at >= 0 && at < p.M ? p.keys[0][at] : none;
+    if (threadIdx.x > 0 && threadIdx.x <= kChunk) pos[threadIdx.x - 1] = at < p.M ? p.pos[0][at] : 0u;
+  }
+  __syncthreads();
+  const int n = (static_cast<int>(blockIdx.x % p.slabs) * kThreads + static_cast<int>(threadIdx.x)) * 8;
+  if (n >= p.D) return;
+  constexpr int kAhead = 8;
+  float acc[8] = {};
+  bool from_start = keys[0] == keys[1];  // the token at hand began in an earlier chunk
+  for (int k0 = 0; k0 < kChunk; k0 += kAhead) {
+    Raw8<kY> y[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (keys[k0 + k + 1] != none)
+        y[k] = load8<kY>(row_at<kY>(p.dY, pos[k0 + k], p.lddy), n, p.D, vec);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const uint32_t v = keys[k0 + k + 1];
+      if (v == none) return;  // the rest holds no tokens of the table
+      float f[8];
+      unpack8<kY>(y[k], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += f[j];
+      const bool last = k0 + k == kChunk - 1, goes_on = keys[k0 + k + 2] == v;
+      if (goes_on && !last) continue;
+      if (from_start || goes_on) {
+        float* out = p.partial + (static_cast<long long>(c) * 2 + (from_start ? 0 : 1)) * p.D;
+        store8<IGC_F32>(reinterpret_cast<char*>(out), n, p.D,
+                        (reinterpret_cast<uintptr_t>(out) & 15u) == 0, acc);
+      } else {
+        finish8<kW>(p, v, n, vec, acc);
+      }
+      from_start = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    }
+  }
+}
+
+// Tokens that cross chunks: the sum of the chunk where one begins and of those it goes on in.  A
+// block looks at eight chunks and has 256 columns, its eight warps share a token's chunks.
+template <int kW>
+__global__ void __launch_bounds__(256) embed_join_kernel(const EmbedParams p) {
+  __shared__ float tot[8][256];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const bool vec = p.vec != 0;
+  const int chunks = (p.M + kChunk - 1) / kChunk;
+  const int sub = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const long long n0 = static_cast<long long>(blockIdx.y) * 256 + lane * 8;
+  for (int c = blockIdx.x * 8; c < min(chunks, static_cast<int>(blockIdx.x) * 8 + 8); ++c) {
+    const long long p0 = static_cast<long long>(c) * kChunk, next = p0 + kChunk;
+    if (next >= p.M) return;
+    const uint32_t v = p.keys[0][next - 1];
+    if (v >= p.V || p.keys[0][next] != v) continue;          // nothing goes on
+    if (p0 > 0 && p.keys[0][p0 - 1] == v) continue;          // began earlier
+    int end = c + 1;  // the chunk that the token ends in: by halves, the tokens ascend
+    int step = 1;
+    while (end + step < chunks && p.keys[0][static_cast<long long>(end + step) * kChunk] == v) {
+      end += step;
+      step *= 2;
+    }
+    for (; step > 0; step /= 2)
+      if (end + step < chunks && p.keys[0][static_cast<long long>(end + step) * kChunk] == v)
+        end += step;
+    float acc[8] = {};
+    if (n0 < p.D) {
+      const int n = static_cast<int>(n0);
+      // the sums of chunks c (its last token's), c + 1, ... end (their first token's)
+#pragma unroll 4
+      for (int k = c + sub; k <= end; k += 8) {
+        const float* from = p.partial + (static_cast<long long>(k) * 2 + (k == c ? 1 : 0)) * p.D;
+        float f[8];
+        unpack8<IGC_F32>(load8<IGC_F32>(reinterpret_cast<const char*>(from), n, p.D,
+                                        (reinterpret_cast<uintptr_t>(from) & 15u) == 0),
+                         f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += f[j];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tot[sub][lane * 8 + j] = acc[j];
+    __syncthreads();
+    if (sub == 0 && n0 < p.D) {
+#pragma unroll
+      for (int r = 1; r < 8; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += tot[r][lane * 8 + j];
+      finish8<kW>(p, v, static_cast<int>(n0), vec, acc);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct EmbedLayout {
+  size_t keys[2], pos[2], touched, partial, bytes;
+};
+EmbedLayout layout(int64_t M, int64_t V, int64_t D) {
+  EmbedLayout l = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up256(bytes);
+    return here;
+  };
+  if (M > kSmallM && V > 0 && D > 0) {
+    for (int i = 0; i < 2; ++i) {
+      l.keys[i] = take(static_cast<size_t>(M) * 4);
+      l.pos[i] = take(static_cast<size_t>(M) * 4);
+    }
+    l.touched = take(static_cast<size_t>((V + 31) / 32) * 4);
+    l.partial = take(static_cast<size_t>((M + kChunk - 1) / kChunk) * 2 * static_cast<size_t>(D) * 4);
+  }
+  l.bytes = at;
+  return l;
+}
+
+template <int kY, int kW>
+int run(const EmbedParams& p, cudaStream_t stream) {
+  const long long zero_blocks = p.accumulate ? 0 : (p.V + p.zero_rows - 1) / p.zero_rows;
+  if (p.M <= kSmallM) {
+    const long long blocks = static_cast<long long>(p.M) * p.slabs + zero_blocks;
+    if (blocks > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
+    if (blocks == 0) return IGC_OK;
+    return launch_pdl(embed_small_kernel<kY, kW>, dim3(static_cast<unsigned>(blocks)),
+                      dim3(kThreads), 0, stream, p);
+  }
+  const int chunks = (p.M + kChunk - 1) / kChunk;
+  const long long blocks = static_cast<long long>(chunks) * p.slabs + zero_blocks;
+  const long long join_cols = (static_cast<long long>(p.D) + 255) / 256;
+  if (blocks > 0x7fffffff || join_cols > 65535) return IGC_ERR_UNSUPPORTED;
+  const int smem = (kSortThreads / 32) * (1 << p.digit_bits) * 4;
+  if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (kSortThreads / 32) * kMaxDigit * 4) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return IGC_ERR_CUDA;
+  }
+  int rc = launch_pdl(embed_sort_kernel, dim3(kCtas), dim3(kSortThreads),
+                      static_cast<size_t>(smem), stream, p);
+  if (rc != IGC_OK) return rc;
+  rc = launch_pdl(embed_sums_kernel<kY, kW>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
+                  0, stream, p);
+  if (rc != IGC_OK) return rc;
+  return launch_pdl(embed_join_kernel<kW>,
+                    dim3(static_cast<unsigned>((chunks + 7) / 8), static_cast<unsigned>(join_cols)),
+                    dim3(256), 0, stream, p);
+}
+
+}  // namespace
+
+}  // namespace igc
+
+using namespace igc;
+
+extern "C" {
+
+size_t embedding_backward_workspace_size(int64_t M, int64_t V, int64_t D) {
+  return M < 0 || V < 0 || D < 0 ? 0 : layout(M, V, D).bytes;
+}
+
+int embedding_backward(int64_t M, int64_t V, int64_t D, const void* tokens, int token_bytes,
+                       const void* dY, int64_t lddy, int y_dtype, float scale, int accumulate,
+                       void* dW, int64_t lddw, int dw_dtype, void* workspace,
+                       size_t workspace_bytes, igc_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (M < 0 || V < 0 || D < 0 || (token_bytes != 4 && token_bytes != 8) || !is_type(y_dtype) ||
+      !is_type_or_f32(dw_dtype, y_dtype))
+    return IGC_ERR_INVALID_ARG;
+  if (V == 0 || D == 0 || (M == 0 && accumulate)) return IGC_OK;
+  if (!fits32(M) || !fits32(V) || !fits32(D)) return IGC_ERR_UNSUPPORTED;
+  if (dW == nullptr || lddw < D || (M > 0 && (tokens == nullptr || dY == nullptr || lddy < D)))
+    return IGC_ERR_INVALID_ARG;
+  if (is_any(dW, tokens, dY)) return IGC_ERR_INVALID_ARG;
+  if (!elements_aligned(Mat{dY, lddy, y_dtype}, Mat{dW, lddw, dw_dtype}) ||
+      reinterpret_cast<uintptr_t>(tokens) % token_bytes != 0)
+    return IGC_ERR_MISALIGNED;
+  DeviceInfo dev;
+  const int rc = current_device(&dev);
+  if (rc != IGC_OK) return rc;
+  const EmbedLayout l = layout(M, V, D);
+  if (l.bytes > 0 && (workspace == nullptr || workspace_bytes < l.bytes ||
+                      reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
+    return IGC_ERR_WORKSPACE;
+  EmbedParams p = {};
+  p.M = static_cast<int>(M), p.D = static_cast<int>(D), p.V = V;
+  p.vec = rows_vec(dY, lddy, y_dtype) && rows_vec(dW, lddw, dw_dtype);
+  p.token64 = token_bytes == 8;
+  p.accumulate = accumulate != 0;
+  p.slabs = static_cast<int>((D + kThreads * 8 - 1) / (kThreads * 8));
+  // about 64 KB of zeros to a block
+  const int64_t rows = 65536 / (D * static_cast<int64_t>(elem_size(dw_dtype)));
+  p.zero_rows = static_cast<int>(rows < 1 ? 1 : (rows > 64 ? 64 : rows));
+  p.tokens = tokens, p.dY = dY, p.dW = dW;
+  p.lddy = lddy, p.lddw = lddw;
+  p.scale = scale;
+  char* ws = static_cast<char*>(workspace);
+  for (int i = 0; i < 2; ++i) {
+    p.keys[i] = reinterpret_cast<uint32_t*>(ws + l.keys[i]);
+    p.pos[i] = reinterpret_cast<uint32_t*>(ws + l.pos[i]);
+  }
+  p.touched = accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + l.touched);
+  p.partial = reinterpret_cast<float*>(ws + l.partial);
+  int bits = 1;
+  while ((static_cast<int64_t>(1) << bits) <= V) ++bits;  // keys are 0 .. V
+  p.passes = (bits + 8) / 9;
+  p.digit_bits = (bits + p.passes - 1) / p.passes;
+  if (y_dtype == IGC_F32) return run<IGC_F32, IGC_F32>(p, stream);
+  if (y_dtype == IGC_F16)
+    return dw_dtype == IGC_F32 ? run<IGC_F16, IGC_F32>(p, stream)
+                               : run<IGC_F16, IGC_F16>(p, stream);
+  return dw_dtype == IGC_F32 ? run<IGC_BF16, IGC_F32>(p, stream)
+                             : run<IGC_BF16, IGC_BF16>(p, stream);
+}
+
+}  // extern "C"
