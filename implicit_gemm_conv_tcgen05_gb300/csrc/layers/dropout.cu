@@ -48,12 +48,12 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     if (u0 + threadIdx.x + i * kThreads >= p.units) continue;
-    float v[8];
+    float v[8], f[8] = {};
     unpack8<kX>(x[i], v);
-    if constexpr (kDrop) drop8(p.drop, offset, row[i], n[i], v);
-    if (p.R != nullptr) {
-      float f[8];
-      unpack8<kY>(r[i], f);
+    if (p.R != nullptr) unpack8<kY>(r[i], f);
+    if constexpr (kDrop) {
+      drop8(p.drop, offset, row[i], n[i], v, f);
+    } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += f[j];
     }

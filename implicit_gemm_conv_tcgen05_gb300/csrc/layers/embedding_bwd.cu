@@ -3,9 +3,9 @@
 // Bound by memory: dY is read once and dW written once (a training batch touches a small part of
 // a large table: most of the time goes to the zeros of the rest).
 //
-// Few positions: one launch.  A block per position (and 1024 columns) looks through all tokens;
-// the block of a token's first position adds the rows of all its positions, in order.  Further
-// blocks write the zeros of the rows that no token points to.
+// Few positions: one launch.  A block per position (and 512 columns) looks through all tokens;
+// the block of a token's first position adds the rows of all its positions, in four shares.
+// Further blocks write the zeros of the rows that no token points to.
 //
 // Many: the positions are sorted by token first (stable, so that a token's positions stay in
 // order), by a cluster of eight blocks with a radix sort.  Blocks then walk chunks of 32 sorted
@@ -18,15 +18,18 @@ namespace igc {
 namespace {
 
 constexpr int kThreads = 128;       // of a block over 1024 columns
+constexpr int kSmallUnits = 64, kSmallSubs = 4;  // few positions: 512 columns, four shares of rows
+constexpr int kSmallThreads = kSmallUnits * kSmallSubs;
 constexpr int kSmallM = 1024;       // positions up to which one launch does
 constexpr int kChunk = 32;          // sorted positions of a block
+constexpr int kAhead = 8;           // rows that a thread loads before it adds the first
 constexpr int kCtas = 8;            // of the sorting cluster
 constexpr int kSortThreads = 1024, kSortWarps = kCtas * (kSortThreads / 32);
 constexpr int kMaxDigit = 512;      // values of a digit of the radix sort
 
 struct EmbedParams {
   int M, D, vec, token64, accumulate;
-  int slabs;                 // blocks of 1024 columns to a row
+  int slabs;                 // blocks to a row
   int zero_rows;             // rows of a block that writes zeros
   long long V;
   const void* tokens;
@@ -64,19 +67,18 @@ __device__ __forceinline__ void finish8(const EmbedParams& p, long long v, int n
 }
 
 template <int kY>
-__device__ __forceinline__ void add_row8(const EmbedParams& p, long long i, int n, bool vec,
-                                         float (&acc)[8]) {
+__device__ __forceinline__ void add8(const Raw8<kY>& y, float (&acc)[8]) {
   float f[8];
-  unpack8<kY>(load8<kY>(row_at<kY>(p.dY, i, p.lddy), n, p.D, vec), f);
+  unpack8<kY>(y, f);
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] += f[j];
 }
 
-template <int kW>
+template <int kW, int kStep>
 __device__ __forceinline__ void zero_row(const EmbedParams& p, long long v, bool vec) {
   const float zero[8] = {};
   char* row = row_at<kW>(p.dW, v, p.lddw);
-  for (long long n = threadIdx.x * 8; n < p.D; n += kThreads * 8)
+  for (long long n = threadIdx.x * 8; n < p.D; n += kStep * 8)
     store8<kW>(row, static_cast<int>(n), p.D, vec, zero);
 }
 
@@ -84,47 +86,96 @@ __device__ __forceinline__ void zero_row(const EmbedParams& p, long long v, bool
 // few positions
 // ---------------------------------------------------------------------------
 template <int kY, int kW>
-__global__ void __launch_bounds__(kThreads) embed_small_kernel(const EmbedParams p) {
+__global__ void __launch_bounds__(kSmallThreads) embed_small_kernel(const EmbedParams p) {
   __shared__ uint32_t bits[kSmallM / 32];
+  __shared__ float4 tot[kSmallSubs - 1][2][kSmallUnits];
   grid_dependency_wait();
   grid_dependents_launch();
   const bool vec = p.vec != 0;
   const long long token_blocks = static_cast<long long>(p.M) * p.slabs;
+  constexpr int kPer = kSmallM / kSmallThreads;
   if (blockIdx.x >= token_blocks) {
     // the rows [v0, v1): bits says which a token points to
     const long long v0 = (blockIdx.x - token_blocks) * p.zero_rows;
     const long long v1 = min(p.V, v0 + p.zero_rows);
     if (threadIdx.x < 2) bits[threadIdx.x] = 0;
     __syncthreads();
-    for (int j = threadIdx.x; j < p.M; j += kThreads) {
-      const long long v = token_at(p, j);
-      if (v >= v0 && v < v1) atomicOr(&bits[(v - v0) / 32], 1u << ((v - v0) % 32));
+    long long v[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = k * kSmallThreads + static_cast<int>(threadIdx.x);
+      v[k] = j < p.M ? token_at(p, j) : -1;
     }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (v[k] >= v0 && v[k] < v1) atomicOr(&bits[(v[k] - v0) / 32], 1u << ((v[k] - v0) % 32));
     __syncthreads();
-    for (long long v = v0; v < v1; ++v)
-      if (!(bits[(v - v0) / 32] >> ((v - v0) % 32) & 1u)) zero_row<kW>(p, v, vec);
+    for (long long r = v0; r < v1; ++r)
+      if (!(bits[(r - v0) / 32] >> ((r - v0) % 32) & 1u)) zero_row<kW, kSmallThreads>(p, r, vec);
     return;
   }
   const int i = static_cast<int>(blockIdx.x / p.slabs);
+  // bit j: position j holds the same token as position i
+  const int words = (p.M + 31) / 32;
+  long long held[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int j = k * kSmallThreads + static_cast<int>(threadIdx.x);
+    held[k] = j < p.M ? token_at(p, j) : -1;
+  }
   const long long v = token_at(p, i);
   if (v < 0 || v >= p.V) return;
-  // bit j: position j holds the same token
-  const int words = (p.M + 31) / 32;
-  for (int j0 = 0; j0 < words * 32; j0 += kThreads) {
-    const int j = j0 + static_cast<int>(threadIdx.x);
-    const uint32_t same = __ballot_sync(0xffffffffu, j < p.M && token_at(p, min(j, p.M - 1)) == v);
-    if (threadIdx.x % 32 == 0 && j / 32 < words) bits[j / 32] = same;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t same = __ballot_sync(0xffffffffu, held[k] == v);
+    if (threadIdx.x % 32 == 0) bits[(k * kSmallThreads + static_cast<int>(threadIdx.x)) / 32] = same;
   }
   __syncthreads();
-  for (int k = 0; k < i / 32; ++k)
-    if (bits[k] != 0) return;
-  if (bits[i / 32] & ((1u << (i % 32)) - 1u)) return;
-  const int n = (static_cast<int>(blockIdx.x % p.slabs) * kThreads + static_cast<int>(threadIdx.x)) * 8;
-  if (n >= p.D) return;
+  uint32_t earlier = 0;
+  for (int k = 0; k < i / 32; ++k) earlier |= bits[k];
+  if (earlier != 0 || (bits[i / 32] & ((1u << (i % 32)) - 1u)) != 0) return;
+  const int unit = static_cast<int>(threadIdx.x) % kSmallUnits;
+  const int sub = static_cast<int>(threadIdx.x) / kSmallUnits;
+  const int n = (static_cast<int>(blockIdx.x % p.slabs) * kSmallUnits + unit) * 8;
+  // of the token's positions in order, each share has every kSmallSubs-th; it loads kAhead rows
+  // before it adds the first
   float acc[8] = {};
-  for (int k = i / 32; k < words; ++k) {
-    for (uint32_t left = bits[k]; left != 0; left &= left - 1)
-      add_row8<kY>(p, k * 32 + __ffs(static_cast<int>(left)) - 1, n, vec, acc);
+  int k = i / 32, count = 0;
+  uint32_t left = bits[k];
+  for (bool more = n < p.D; more;) {
+    Raw8<kY> y[kAhead];
+    int found = 0;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      int j = -1;
+      while (true) {
+        while (left == 0 && k + 1 < words) left = bits[++k];
+        if (left == 0) break;
+        j = k * 32 + __ffs(static_cast<int>(left)) - 1;
+        left &= left - 1;
+        if (count++ % kSmallSubs == sub) break;
+        j = -1;
+      }
+      if (j < 0) continue;
+      y[a] = load8<kY>(row_at<kY>(p.dY, j, p.lddy), n, p.D, vec);
+      found = a + 1;
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (a < found) add8<kY>(y[a], acc);
+    more = found == kAhead;
+  }
+  if (sub > 0) {
+    tot[sub - 1][0][unit] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    tot[sub - 1][1][unit] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  }
+  __syncthreads();
+  if (sub > 0 || n >= p.D) return;
+#pragma unroll
+  for (int r = 0; r < kSmallSubs - 1; ++r) {
+    const float4 a = tot[r][0][unit], b = tot[r][1][unit];
+    acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
+    acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
   }
   finish8<kW>(p, v, n, vec, acc);
 }
@@ -132,6 +183,12 @@ __global__ void __launch_bounds__(kThreads) embed_small_kernel(const EmbedParams
 // ---------------------------------------------------------------------------
 // many positions: the sort
 // ---------------------------------------------------------------------------
+// A pass of the radix sort: every warp counts the digits of its run of positions, the counts of
+// all warps become places, and every warp moves its run there.  A run is taken kBatch steps of
+// 32 positions at a time; one of a single batch (up to 65536 positions in all) keeps its keys
+// and their ranks in registers between the count and the move.
+constexpr int kBatch = 8;
+
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
     embed_sort_kernel(const EmbedParams p) {
   extern __shared__ uint32_t hist[];  // [32 warps][digits]: counts, then places
@@ -142,10 +199,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int digits = 1 << p.digit_bits;
   const uint32_t below = (1u << lane) - 1u;
-  // each warp of the cluster has a run of positions, and counts and places it by itself
   const int run = ((p.M + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const long long first = static_cast<long long>(rank * (kSortThreads / 32) + warp) * run;
-  const int steps = first < p.M ? static_cast<int>((min(static_cast<long long>(run), p.M - first) + 31) / 32) : 0;
+  const int steps =
+      first < p.M
+          ? static_cast<int>((min(static_cast<long long>(run), p.M - first) + 31) / 32)
+          : 0;
+  const int batches = (run / 32 + kBatch - 1) / kBatch;
   uint32_t* mine = hist + warp * digits;
   if (p.touched != nullptr)
     for (long long k = static_cast<long long>(rank) * kSortThreads + threadIdx.x;
@@ -157,29 +217,54 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
     const uint32_t* pos_in = p.pos[(pass + p.passes) & 1];
     uint32_t* keys_out = p.keys[(pass + p.passes + 1) & 1];
     uint32_t* pos_out = p.pos[(pass + p.passes + 1) & 1];
-    auto key_at = [&](long long i) -> uint32_t {
-      if (pass > 0) return __ldcg(keys_in + i);
-      const long long v = token_at(p, static_cast<int>(i));
-      return static_cast<uint32_t>(v >= 0 && v < p.V ? v : p.V);
+    uint32_t key[kBatch], pos[kBatch], at[kBatch];
+    auto load = [&](int batch) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int step = batch * kBatch + k;
+        const long long i = first + step * 32 + lane;
+        if (step >= steps || i >= p.M) continue;
+        if (pass > 0) {
+          key[k] = __ldcg(keys_in + i);
+          pos[k] = __ldcg(pos_in + i);
+        } else {
+          const long long v = token_at(p, static_cast<int>(i));
+          key[k] = static_cast<uint32_t>(v >= 0 && v < p.V ? v : p.V);
+          pos[k] = static_cast<uint32_t>(i);
+        }
+      }
     };
-    auto digit_of = [&](uint32_t key) {
-      return (key >> shift) & static_cast<uint32_t>(digits - 1);
+    auto digit_of = [&](uint32_t v) {
+      return (v >> shift) & static_cast<uint32_t>(digits - 1);
+    };
+    // at: the keys' places among those of their digit that mine counts from where it stands
+    auto rank_keys = [&](int batch) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int step = batch * kBatch + k;
+        if (step >= steps) break;
+        const bool valid = first + step * 32 + lane < p.M;
+        // (a lane past the last position has a digit that no other has)
+        const uint32_t d = valid ? digit_of(key[k]) : 0xffffffffu;
+        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        if (valid) at[k] = mine[d] + __popc(peers & below);
+        __syncwarp();
+        if (valid && (peers & below) == 0) mine[d] += __popc(peers);
+        __syncwarp();
+      }
     };
     for (int d = lane; d < digits; d += 32) mine[d] = 0;
     __syncwarp();
-    for (int k = 0; k < steps; ++k) {
-      const long long i = first + k * 32 + lane;
-      const bool valid = i < p.M;
-      const uint32_t d = valid ? digit_of(key_at(i)) : 0xffffffffu;
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      if (valid && (peers & below) == 0) mine[d] += __popc(peers);
-      __syncwarp();
+    for (int batch = 0; batch < batches; ++batch) {
+      load(batch);
+      rank_keys(batch);
     }
     __syncthreads();
     // the warps' counts become places within the block's share of a digit
     const int d = static_cast<int>(threadIdx.x);
     if (d < digits) {
       uint32_t sum = 0;
+#pragma unroll 8
       for (int w = 0; w < kSortThreads / 32; ++w) {
         const uint32_t c = hist[w * digits + d];
         hist[w * digits + d] = sum;
@@ -207,31 +292,37 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
     }
     if (lane == 31) scan[warp] = upto;
     __syncthreads();
-    uint32_t ahead = 0;
-    for (int w = 0; w < warp; ++w) ahead += scan[w];
+    uint32_t ahead = lane < warp ? scan[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
     if (d < digits) base[d] = ahead + upto - all + before;
     __syncthreads();
-    for (int k = 0; k < steps; ++k) {
-      const long long i = first + k * 32 + lane;
-      const bool valid = i < p.M;
-      uint32_t key = 0, dg = 0xffffffffu;
-      if (valid) {
-        key = key_at(i);
-        dg = digit_of(key);
+    for (int batch = 0; batch < batches; ++batch) {
+      const bool kept = batches == 1;
+      if (!kept) {
+        load(batch);
+        rank_keys(batch);  // (from the places on now)
       }
-      const uint32_t peers = __match_any_sync(0xffffffffu, dg);
-      if (valid) {
-        const uint32_t at = base[dg] + mine[dg] + __popc(peers & below);
-        keys_out[at] = key;
-        pos_out[at] = pass > 0 ? __ldcg(pos_in + i) : static_cast<uint32_t>(i);
-        if (pass == 0 && p.touched != nullptr && key < p.V)
-          atomicOr(p.touched + key / 32, 1u << (key % 32));
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int step = batch * kBatch + k;
+        if (step >= steps || first + step * 32 + lane >= p.M) continue;
+        const uint32_t dg = digit_of(key[k]);
+        const uint32_t to = base[dg] + at[k] + (kept ? mine[dg] : 0u);
+        keys_out[to] = key[k];
+        pos_out[to] = pos[k];
       }
-      __syncwarp();
-      if (valid && (peers & below) == 0) mine[dg] += __popc(peers);
-      __syncwarp();
     }
     cluster_sync();  // what the next pass, and a block's reads of the others' totals, rely on
+  }
+  // the rows of dW that a token points to, each set once (by every position, the atomics on the
+  // words of frequent tokens took 20 us of a training batch's 33)
+  if (p.touched == nullptr) return;
+  for (long long i = static_cast<long long>(rank) * kSortThreads + threadIdx.x; i < p.M;
+       i += kCtas * kSortThreads) {
+    const uint32_t v = __ldcg(p.keys[0] + i);
+    if (v < p.V && (i == 0 || __ldcg(p.keys[0] + i - 1) != v))
+      atomicOr(p.touched + v / 32, 1u << (v % 32));
   }
 }
 
@@ -250,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams 
     const long long v0 = (blockIdx.x - sum_blocks) * p.zero_rows;
     const long long v1 = min(p.V, v0 + p.zero_rows);
     for (long long v = v0; v < v1; ++v)
-      if (!(p.touched[v / 32] >> (v % 32) & 1u)) zero_row<kW>(p, v, vec);
+      if (!(p.touched[v / 32] >> (v % 32) & 1u)) zero_row<kW, kThreads>(p, v, vec);
     return;
   }
   const int c = static_cast<int>(blockIdx.x / p.slabs);
@@ -266,7 +357,6 @@ __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams 
   __syncthreads();
   const int n = (static_cast<int>(blockIdx.x % p.slabs) * kThreads + static_cast<int>(threadIdx.x)) * 8;
   if (n >= p.D) return;
-  constexpr int kAhead = 8;
   float acc[8] = {};
   bool from_start = keys[0] == keys[1];  // the token at hand began in an earlier chunk
   for (int k0 = 0; k0 < kChunk; k0 += kAhead) {
@@ -279,10 +369,7 @@ __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams 
     for (int k = 0; k < kAhead; ++k) {
       const uint32_t v = keys[k0 + k + 1];
       if (v == none) return;  // the rest holds no tokens of the table
-      float f[8];
-      unpack8<kY>(y[k], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += f[j];
+      add8<kY>(y[k], acc);
       const bool last = k0 + k == kChunk - 1, goes_on = keys[k0 + k + 2] == v;
       if (goes_on && !last) continue;
       if (from_start || goes_on) {
@@ -299,57 +386,80 @@ __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams 
   }
 }
 
-// Tokens that cross chunks: the sum of the chunk where one begins and of those it goes on in.  A
-// block looks at eight chunks and has 256 columns, its eight warps share a token's chunks.
+// Tokens that cross chunks: the sum of the chunk where one begins and of those it goes on in.
+// A block has 256 columns and looks at 16 chunks, a warp at each: a token that goes on in few
+// chunks is the warp's, one that goes on in many is then shared by all 16 warps.
+constexpr int kJoinWarps = 16;
+
 template <int kW>
-__global__ void __launch_bounds__(256) embed_join_kernel(const EmbedParams p) {
-  __shared__ float tot[8][256];
+__global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const EmbedParams p) {
+  __shared__ float tot[kJoinWarps][256];
+  __shared__ int long_end[kJoinWarps];  // last chunk of the token that begins in a warp's chunk
   grid_dependency_wait();
   grid_dependents_launch();
   const bool vec = p.vec != 0;
   const int chunks = (p.M + kChunk - 1) / kChunk;
-  const int sub = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const long long n0 = static_cast<long long>(blockIdx.y) * 256 + lane * 8;
-  for (int c = blockIdx.x * 8; c < min(chunks, static_cast<int>(blockIdx.x) * 8 + 8); ++c) {
-    const long long p0 = static_cast<long long>(c) * kChunk, next = p0 + kChunk;
-    if (next >= p.M) return;
-    const uint32_t v = p.keys[0][next - 1];
-    if (v >= p.V || p.keys[0][next] != v) continue;          // nothing goes on
-    if (p0 > 0 && p.keys[0][p0 - 1] == v) continue;          // began earlier
-    int end = c + 1;  // the chunk that the token ends in: by halves, the tokens ascend
-    int step = 1;
-    while (end + step < chunks && p.keys[0][static_cast<long long>(end + step) * kChunk] == v) {
-      end += step;
-      step *= 2;
-    }
-    for (; step > 0; step /= 2)
-      if (end + step < chunks && p.keys[0][static_cast<long long>(end + step) * kChunk] == v)
-        end += step;
-    float acc[8] = {};
-    if (n0 < p.D) {
-      const int n = static_cast<int>(n0);
-      // the sums of chunks c (its last token's), c + 1, ... end (their first token's)
-#pragma unroll 4
-      for (int k = c + sub; k <= end; k += 8) {
-        const float* from = p.partial + (static_cast<long long>(k) * 2 + (k == c ? 1 : 0)) * p.D;
-        float f[8];
-        unpack8<IGC_F32>(load8<IGC_F32>(reinterpret_cast<const char*>(from), n, p.D,
-                                        (reinterpret_cast<uintptr_t>(from) & 15u) == 0),
-                         f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += f[j];
+  const int n = static_cast<int>(n0);
+  // chunk k's part of the token that begins in chunk c: of its last token there, of its first
+  // in those after
+  auto part = [&](int k, int c) {
+    const float* from = p.partial + (static_cast<long long>(k) * 2 + (k == c ? 1 : 0)) * p.D;
+    return load8<IGC_F32>(reinterpret_cast<const char*>(from), n, p.D,
+                          (reinterpret_cast<uintptr_t>(from) & 15u) == 0);
+  };
+  const int mine = blockIdx.x * kJoinWarps + warp;
+  const long long p0 = static_cast<long long>(mine) * kChunk, next = p0 + kChunk;
+  int end = -1;
+  uint32_t v = 0;
+  if (next < p.M) {
+    v = p.keys[0][next - 1];
+    const uint32_t after = p.keys[0][next];
+    const uint32_t ahead = p0 > 0 ? p.keys[0][p0 - 1] : ~v;
+    if (v < p.V && after == v && ahead != v) {
+      // the chunk that it ends in: the tokens ascend, 32 chunks are looked at at once
+      end = mine + 1;
+      while (true) {
+        const long long k = static_cast<long long>(end) + 1 + lane;
+        const uint32_t more =
+            __ballot_sync(0xffffffffu, k < chunks && p.keys[0][k * kChunk] == v);
+        end += __popc(more);
+        if (more != 0xffffffffu) break;
       }
     }
+  }
+  const bool shared = end - mine >= kAhead;
+  if (lane == 0) long_end[warp] = end >= 0 && shared ? end : -1;
+  if (end >= 0 && !shared && n0 < p.D) {
+    Raw8<IGC_F32> f[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (mine + k <= end) f[k] = part(mine + k, mine);
+    float acc[8] = {};
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (mine + k <= end) add8<IGC_F32>(f[k], acc);
+    finish8<kW>(p, v, n, vec, acc);
+  }
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const int last = long_end[w], c = blockIdx.x * kJoinWarps + w;
+    if (last < 0) continue;
+    float acc[8] = {};
+    if (n0 < p.D) {
+#pragma unroll 4
+      for (int k = c + warp; k <= last; k += kJoinWarps) add8<IGC_F32>(part(k, c), acc);
+    }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tot[sub][lane * 8 + j] = acc[j];
+    for (int j = 0; j < 8; ++j) tot[warp][lane * 8 + j] = acc[j];
     __syncthreads();
-    if (sub == 0 && n0 < p.D) {
-#pragma unroll
-      for (int r = 1; r < 8; ++r)
+    if (warp == 0 && n0 < p.D) {
+      for (int r = 1; r < kJoinWarps; ++r)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += tot[r][lane * 8 + j];
-      finish8<kW>(p, v, static_cast<int>(n0), vec, acc);
+      finish8<kW>(p, p.keys[0][static_cast<long long>(c) * kChunk + kChunk - 1], n, vec, acc);
     }
   }
 }
@@ -390,7 +500,7 @@ int run(const EmbedParams& p, cudaStream_t stream) {
     if (blocks > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
     if (blocks == 0) return IGC_OK;
     return launch_pdl(embed_small_kernel<kY, kW>, dim3(static_cast<unsigned>(blocks)),
-                      dim3(kThreads), 0, stream, p);
+                      dim3(kSmallThreads), 0, stream, p);
   }
   const int chunks = (p.M + kChunk - 1) / kChunk;
   const long long blocks = static_cast<long long>(chunks) * p.slabs + zero_blocks;
@@ -409,8 +519,9 @@ int run(const EmbedParams& p, cudaStream_t stream) {
                   0, stream, p);
   if (rc != IGC_OK) return rc;
   return launch_pdl(embed_join_kernel<kW>,
-                    dim3(static_cast<unsigned>((chunks + 7) / 8), static_cast<unsigned>(join_cols)),
-                    dim3(256), 0, stream, p);
+                    dim3(static_cast<unsigned>((chunks + kJoinWarps - 1) / kJoinWarps),
+                         static_cast<unsigned>(join_cols)),
+                    dim3(kJoinWarps * 32), 0, stream, p);
 }
 
 }  // namespace
@@ -453,7 +564,8 @@ int embedding_backward(int64_t M, int64_t V, int64_t D, const void* tokens, int 
   p.vec = rows_vec(dY, lddy, y_dtype) && rows_vec(dW, lddw, dw_dtype);
   p.token64 = token_bytes == 8;
   p.accumulate = accumulate != 0;
-  p.slabs = static_cast<int>((D + kThreads * 8 - 1) / (kThreads * 8));
+  const int64_t slab = (M <= kSmallM ? kSmallUnits : kThreads) * 8;
+  p.slabs = static_cast<int>((D + slab - 1) / slab);
   // about 64 KB of zeros to a block
   const int64_t rows = 65536 / (D * static_cast<int64_t>(elem_size(dw_dtype)));
   p.zero_rows = static_cast<int>(rows < 1 ? 1 : (rows > 64 ? 64 : rows));

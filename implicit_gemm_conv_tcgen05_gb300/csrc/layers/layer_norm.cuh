@@ -26,7 +26,61 @@ struct NormParams {
   Drop drop;
 };
 
-// S of eight columns; X and R are each loaded if they are there.
+// S of eight columns from X and R, where each is there.
+template <int kT, int kS, bool kDrop>
+__device__ __forceinline__ void join8(const NormParams& p, uint64_t offset, long long row, int n,
+                                      const Raw8<kT>& x, const Raw8<kS>& r, float (&s)[8]) {
+  if (p.X == nullptr) {
+    unpack8<kS>(r, s);
+    return;
+  }
+  float f[8] = {};
+  unpack8<kT>(x, s);
+  if (p.R != nullptr) unpack8<kS>(r, f);
+  if constexpr (kDrop) {
+    drop8(p.drop, offset, row, n, s, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      unpair(add2(pair(s[2 * j], s[2 * j + 1]), pair(f[2 * j], f[2 * j + 1])), s[2 * j],
+             s[2 * j + 1]);
+  }
+}
+
+// s less the mean; returns the sum of the squares.
+__device__ __forceinline__ float center8(float (&s)[8], float mean, int n, int N) {
+  if (n + 8 > N) {
+    // (what lies past the row's end is to differ by nothing)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j >= N) s[j] = mean;
+  }
+  const uint64_t m = pair(-mean, -mean);
+  uint64_t q = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t d = add2(pair(s[2 * j], s[2 * j + 1]), m);
+    q = fma2(d, d, q);
+    unpair(d, s[2 * j], s[2 * j + 1]);
+  }
+  return sum2(q);
+}
+
+// Y of eight columns from the differences from the mean.
+template <int kT>
+__device__ __forceinline__ void affine8(const NormParams& p, float rstd, int n, float (&s)[8]) {
+  float w[8], b[8];
+  load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, w);
+  load_vec8<kT>(p.b, n, p.N, p.w_f32, 0.0f, b);
+  const uint64_t r = pair(rstd, rstd);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t d = mul2(pair(s[2 * j], s[2 * j + 1]), r);
+    unpair(fma2(d, pair(w[2 * j], w[2 * j + 1]), pair(b[2 * j], b[2 * j + 1])), s[2 * j],
+           s[2 * j + 1]);
+  }
+}
+
 template <int kT, int kS, bool kDrop>
 __device__ __forceinline__ void joined8(const NormParams& p, uint64_t offset, long long row, int n,
                                         bool vec, float (&s)[8]) {
@@ -34,112 +88,44 @@ __device__ __forceinline__ void joined8(const NormParams& p, uint64_t offset, lo
   Raw8<kS> r;
   if (p.X != nullptr) x = load8<kT>(row_at<kT>(p.X, row, p.ldx), n, p.N, vec);
   if (p.R != nullptr) r = load8<kS>(row_at<kS>(p.R, row, p.ldr), n, p.N, vec);
-  if (p.X != nullptr) {
-    unpack8<kT>(x, s);
-    if constexpr (kDrop) drop8(p.drop, offset, row, n, s);
-    if (p.R != nullptr) {
-      float f[8];
-      unpack8<kS>(r, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += f[j];
-    }
-  } else {
-    unpack8<kS>(r, s);
-  }
+  join8<kT, kS, kDrop>(p, offset, row, n, x, r, s);
 }
 
-// kLanes threads to a row, kUnits units of eight columns to a thread; rows of 32 threads share
-// a block of four warps.
-template <int kT, int kS, int kLanes, int kUnits, bool kDrop>
-__global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes)
-    layer_norm_kernel(const NormParams p) {
-  constexpr int kRows = kLanes < 128 ? 128 / kLanes : 1;
-  __shared__ float red[2][kLanes / 32];
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / kLanes;
-  if (kRows > 1 && row >= p.M) return;
-  const int t = threadIdx.x % kLanes;
-  const bool vec = p.vec != 0;
-  const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
-  float s[kUnits][8];
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int n = (i * kLanes + t) * 8;
-    if (n < p.N) {
-      joined8<kT, kS, kDrop>(p, offset, row, n, vec, s[i]);
-      sum += ((s[i][0] + s[i][1]) + (s[i][2] + s[i][3])) +
-             ((s[i][4] + s[i][5]) + (s[i][6] + s[i][7]));
-    }
-  }
-  const float mean = row_sum<kLanes>(sum, red[0]) / static_cast<float>(p.N);
-  sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int n = (i * kLanes + t) * 8;
-    if (n >= p.N) continue;
-    if (p.S != nullptr) store8<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec, s[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      s[i][j] -= mean;
-      if (n + j < p.N) sum += s[i][j] * s[i][j];
-    }
-  }
-  const float var = row_sum<kLanes>(sum, red[1]) / static_cast<float>(p.N);
-  const float rstd = 1.0f / sqrtf(var + p.eps);
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int n = (i * kLanes + t) * 8;
-    if (n >= p.N) continue;
-    float w[8], b[8];
-    load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, w);
-    load_vec8<kT>(p.b, n, p.N, p.w_f32, 0.0f, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * rstd * w[j] + b[j];
-    store8<kT>(row_at<kT>(p.Y, row, p.ldy), n, p.N, vec, s[i]);
-  }
-  if (t == 0) {
-    if (p.mean != nullptr) p.mean[row] = mean;
-    if (p.rstd != nullptr) p.rstd[row] = rstd;
-  }
+// 1 / sqrt(x): the hardware's approximation and one step of Newton's on it.
+__device__ __forceinline__ float rsqrt_step(float x) {
+  const float y = rsqrtf(x);
+  return y > 0.0f && y < INFINITY ? fmaf(0.5f * y, fmaf(-x * y, y, 1.0f), y) : y;
 }
 
-// Rows of any length: S is formed again for each of the three passes.  (S may be R: it is
-// stored in the last.)
-template <int kT, int kS, bool kDrop>
-__global__ void __launch_bounds__(1024) layer_norm_long_kernel(const NormParams p) {
-  __shared__ float red[2][32];
+// Rows of any length and alignment: S is formed again for each of the three passes.  (S may be
+// R: it is stored in the last.)
+template <int kT, int kS, int kThreads, bool kDrop>
+__global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(const NormParams p) {
+  __shared__ __align__(16) float red[2][kThreads / 32];
   grid_dependency_wait();
   grid_dependents_launch();
   const long long row = blockIdx.x;
   const bool vec = p.vec != 0;
   const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
   float s[8], sum = 0.0f;
-  for (long long n = threadIdx.x * 8; n < p.N; n += 8192) {
+  for (long long n = threadIdx.x * 8; n < p.N; n += kThreads * 8) {
     joined8<kT, kS, kDrop>(p, offset, row, static_cast<int>(n), vec, s);
     sum += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   }
-  const float mean = row_sum<1024>(sum, red[0]) / static_cast<float>(p.N);
+  const float mean = row_sum<kThreads>(sum, red[0]) / static_cast<float>(p.N);
   sum = 0.0f;
-  for (long long n = threadIdx.x * 8; n < p.N; n += 8192) {
+  for (long long n = threadIdx.x * 8; n < p.N; n += kThreads * 8) {
     joined8<kT, kS, kDrop>(p, offset, row, static_cast<int>(n), vec, s);
-    float q = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q += n + j < p.N ? (s[j] - mean) * (s[j] - mean) : 0.0f;
-    sum += q;
+    sum += center8(s, mean, static_cast<int>(n), p.N);
   }
-  const float var = row_sum<1024>(sum, red[1]) / static_cast<float>(p.N);
-  const float rstd = 1.0f / sqrtf(var + p.eps);
-  for (long long m = threadIdx.x * 8; m < p.N; m += 8192) {
+  const float var = row_sum<kThreads>(sum, red[1]) / static_cast<float>(p.N);
+  const float rstd = rsqrt_step(var + p.eps);
+  for (long long m = threadIdx.x * 8; m < p.N; m += kThreads * 8) {
     const int n = static_cast<int>(m);
     joined8<kT, kS, kDrop>(p, offset, row, n, vec, s);
     if (p.S != nullptr) store8<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec, s);
-    float w[8], b[8];
-    load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, w);
-    load_vec8<kT>(p.b, n, p.N, p.w_f32, 0.0f, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = (s[j] - mean) * rstd * w[j] + b[j];
+    (void)center8(s, mean, n, p.N);
+    affine8<kT>(p, rstd, n, s);
     store8<kT>(row_at<kT>(p.Y, row, p.ldy), n, p.N, vec, s);
   }
   if (threadIdx.x == 0) {
@@ -148,28 +134,153 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(const NormParams 
   }
 }
 
-template <int kT, int kS, int kLanes, int kUnits>
-int launch_norm(const NormParams& p, bool drop, cudaStream_t stream) {
-  constexpr int kRows = kLanes < 128 ? 128 / kLanes : 1;
-  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(p.M) + kRows - 1) / kRows);
-  return launch_pdl(drop ? layer_norm_kernel<kT, kS, kLanes, kUnits, true>
-                         : layer_norm_kernel<kT, kS, kLanes, kUnits, false>,
-                    dim3(blocks), dim3(kLanes * kRows), 0, stream, p);
+// Blocks of an SM: 768 threads of 80 registers (16384 x 4096 bf16 with dropout and residual: 86 us;
+// 640 threads 92, 512 threads 92).
+constexpr int norm_blocks(int lanes) { return lanes <= 128 ? 6 : (lanes <= 256 ? 3 : 1); }
+
+// Rows that start on 16-byte boundaries, one to a group of kLanes threads, four units to a
+// thread, all loaded before the first is used.
+template <int kT, int kS, int kLanes, bool kDrop>
+__global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes, norm_blocks(kLanes))
+    layer_norm_rows_kernel(const NormParams p) {
+  constexpr int kGroups = kLanes < 128 ? 128 / kLanes : 1, kUnits = 4;
+  constexpr int kSizeT = kT == IGC_F32 ? 4 : 2, kSizeS = kS == IGC_F32 ? 4 : 2;
+  __shared__ __align__(16) float red[kGroups][2][(kLanes / 32 + 3) / 4 * 4];
+  const int t = threadIdx.x % kLanes, group = threadIdx.x / kLanes, N8 = p.N / 8 * 8;
+  const long long row = static_cast<long long>(blockIdx.x) * kGroups + group;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (kGroups > 1 && row >= p.M) return;
+  const bool has_x = p.X != nullptr, has_r = p.R != nullptr, has_s = p.S != nullptr;
+  const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
+  const float inv = 1.0f / static_cast<float>(p.N);
+  const int last = N8 + t < p.N ? N8 + t : -1;
+  const char* x_row = row_at<kT>(p.X, row, p.ldx);
+  const char* r_row = row_at<kS>(p.R, row, p.ldr);
+  char* s_row = row_at<kS>(p.S, row, p.lds);
+  char* y_row = row_at<kT>(p.Y, row, p.ldy);
+  auto one_row = [&](auto whole) {
+    float s[kUnits][8], s_last = 0.0f;
+    Raw8<kT> x[kUnits];
+    Raw8<kS> r[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = (i * kLanes + t) * 8;
+      if (!decltype(whole)::value && n >= N8) continue;
+      if (has_x) x[i] = load8<kT>(x_row, n, n + 8, true);
+      if (has_r) r[i] = load8<kS>(r_row, n, n + 8, true);
+    }
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = (i * kLanes + t) * 8;
+      if (!decltype(whole)::value && n >= N8) continue;
+      float f[8] = {};
+      if (has_r) unpack8<kS>(r[i], f);
+      if constexpr (kDrop) {
+        unpack8<kT>(x[i], s[i]);
+        drop8(p.drop, offset, row, n, s[i], f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] = f[j];
+        if (has_x) {
+          unpack8<kT>(x[i], s[i]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[i][j] += f[j];
+        }
+      }
+      sum = add2(sum, add2(add2(pair(s[i][0], s[i][1]), pair(s[i][2], s[i][3])),
+                           add2(pair(s[i][4], s[i][5]), pair(s[i][6], s[i][7]))));
+    }
+    float total = sum2(sum);
+    if (last >= 0) {
+      const float x_last = has_x ? load1<kT>(x_row, last) : 0.0f;
+      const float r_last = has_r ? load1<kS>(r_row, last) : 0.0f;
+      s_last = kDrop ? drop1(p.drop, offset, row, last, x_last, r_last) : x_last + r_last;
+      total += s_last;
+    }
+    const float mean = row_sum<kLanes>(total, red[group][0], group) * inv;
+    const uint64_t m = pair(-mean, -mean);
+    uint64_t squares = 0;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = (i * kLanes + t) * 8;
+      if (!decltype(whole)::value && n >= N8) continue;
+      if (has_s) store_unit<kS>(s_row + n * kSizeS, s[i]);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const uint64_t d = add2(pair(s[i][j], s[i][j + 1]), m);
+        squares = fma2(d, d, squares);
+        unpair(d, s[i][j], s[i][j + 1]);
+      }
+    }
+    total = sum2(squares);
+    if (last >= 0) {
+      if (has_s) store1<kS>(s_row, last, s_last);
+      s_last -= mean;
+      total = fmaf(s_last, s_last, total);
+    }
+    const float var = row_sum<kLanes>(total, red[group][1], group) * inv;
+    const float rstd = rsqrt_step(var + p.eps);
+    const uint64_t r2 = pair(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = (i * kLanes + t) * 8;
+      if (!decltype(whole)::value && n >= N8) continue;
+      float wv[8], bv[8];
+      load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, wv);
+      load_vec8<kT>(p.b, n, p.N, p.w_f32, 0.0f, bv);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        unpair(fma2(mul2(pair(s[i][j], s[i][j + 1]), r2), pair(wv[j], wv[j + 1]),
+                    pair(bv[j], bv[j + 1])),
+               s[i][j], s[i][j + 1]);
+      store_unit<kT>(y_row + n * kSizeT, s[i]);
+    }
+    if (last >= 0) {
+      float wv = 1.0f, bv = 0.0f;
+      if (p.w != nullptr) wv = load_vec(p.w, last, p.w_f32, kT == IGC_BF16);
+      if (p.b != nullptr) bv = load_vec(p.b, last, p.w_f32, kT == IGC_BF16);
+      store1<kT>(y_row, last, fmaf(s_last * rstd, wv, bv));
+    }
+    if (t == 0) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+  };
+  if (__all_sync(0xffffffffu, ((kUnits - 1) * kLanes + t) * 8 < N8))
+    one_row(std::true_type{});
+  else
+    one_row(std::false_type{});
+}
+
+template <int kT, int kS, int kLanes>
+int launch_rows(const NormParams& p, bool drop, cudaStream_t stream) {
+  constexpr int kGroups = kLanes < 128 ? 128 / kLanes : 1;
+  const long long blocks = (static_cast<long long>(p.M) + kGroups - 1) / kGroups;
+  return launch_pdl(drop ? layer_norm_rows_kernel<kT, kS, kLanes, true>
+                         : layer_norm_rows_kernel<kT, kS, kLanes, false>,
+                    dim3(static_cast<unsigned>(blocks)), dim3(kLanes * kGroups), 0, stream, p);
 }
 
 template <int kT, int kS>
 int run_norm(const NormParams& p, bool drop, cudaStream_t stream) {
   const long long units = (static_cast<long long>(p.N) + 7) / 8;
-  if (units <= 32) return launch_norm<kT, kS, 32, 1>(p, drop, stream);
-  if (units <= 64) return launch_norm<kT, kS, 32, 2>(p, drop, stream);
-  if (units <= 128) return launch_norm<kT, kS, 32, 4>(p, drop, stream);
-  if (units <= 256) return launch_norm<kT, kS, 128, 2>(p, drop, stream);
-  if (units <= 512) return launch_norm<kT, kS, 256, 2>(p, drop, stream);
-  if (units <= 1024) return launch_norm<kT, kS, 512, 2>(p, drop, stream);
-  if (units <= 2048) return launch_norm<kT, kS, 512, 4>(p, drop, stream);
-  return launch_pdl(drop ? layer_norm_long_kernel<kT, kS, true>
-                         : layer_norm_long_kernel<kT, kS, false>,
-                    dim3(static_cast<unsigned>(p.M)), dim3(1024), 0, stream, p);
+  if (p.vec) {
+    if (units <= 128) return launch_rows<kT, kS, 32>(p, drop, stream);
+    if (units <= 256) return launch_rows<kT, kS, 64>(p, drop, stream);
+    if (units <= 512) return launch_rows<kT, kS, 128>(p, drop, stream);
+    if (units <= 1024) return launch_rows<kT, kS, 256>(p, drop, stream);
+    if (units <= 2048) return launch_rows<kT, kS, 512>(p, drop, stream);
+  }
+  const dim3 grid(static_cast<unsigned>(p.M));
+  if (units <= 512)
+    return launch_pdl(drop ? layer_norm_any_kernel<kT, kS, 128, true>
+                           : layer_norm_any_kernel<kT, kS, 128, false>,
+                      grid, dim3(128), 0, stream, p);
+  return launch_pdl(drop ? layer_norm_any_kernel<kT, kS, 1024, true>
+                         : layer_norm_any_kernel<kT, kS, 1024, false>,
+                    grid, dim3(1024), 0, stream, p);
 }
 
 // By type (layer_norm_f32.cu, layer_norm_f16.cu, layer_norm_bf16.cu).

@@ -11,7 +11,7 @@
 // blocks' in order (no atomics).
 #pragma once
 
-#include "layers_host.h"
+#include "row_stream_host.h"
 
 namespace igc {
 
@@ -33,24 +33,86 @@ struct NormBwdParams {
 // Blocks whose partial sums the workspace has room for.
 inline int64_t norm_bwd_max_blocks(int64_t N) { return N <= 1024 ? 1216 : 608; }
 
-// dS and dX of eight columns from g, h and the row's sums.
+// dS and dX of eight columns from g, h and the row's sums; ds_row and dx_row are where the
+// row's dS and dX start.
 template <int kT, int kS, bool kDrop>
 __device__ __forceinline__ void grads8(const NormBwdParams& p, uint64_t offset, long long row,
-                                       int n, bool vec, float rstd, float c1, float c2,
-                                       const Raw8<kS>& a, const float (&g)[8],
+                                       char* ds_row, char* dx_row, int n, bool vec, float rstd,
+                                       float c1, float c2, const Raw8<kS>& a, const float (&g)[8],
                                        const float (&h)[8]) {
-  float d[8], f[8];
+  float d[8], f[8] = {};
+  if (p.A != nullptr) unpack8<kS>(a, f);
+  const uint64_t r = pair(rstd, rstd), m1 = pair(-c1, -c1), m2 = pair(-c2, -c2);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) d[j] = rstd * (g[j] - c1 - h[j] * c2);
-  if (p.A != nullptr) {
-    unpack8<kS>(a, f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) d[j] += f[j];
+  for (int j = 0; j < 8; j += 2) {
+    const uint64_t x = fma2(pair(h[j], h[j + 1]), m2, add2(pair(g[j], g[j + 1]), m1));
+    unpair(fma2(x, r, pair(f[j], f[j + 1])), d[j], d[j + 1]);
   }
-  if (p.dS != nullptr) store8<kS>(row_at<kS>(p.dS, row, p.ldds), n, p.N, vec, d);
+  if (p.dS != nullptr) store8<kS>(ds_row, n, p.N, vec, d);
   if (p.dX != nullptr) {
     if constexpr (kDrop) drop8(p.drop, offset, row, n, d);
-    store8<kT>(row_at<kT>(p.dX, row, p.lddx), n, p.N, vec, d);
+    store8<kT>(dx_row, n, p.N, vec, d);
+  }
+}
+
+// One row of sums per block: its kRows groups of kLanes threads add theirs in order.
+template <int kLanes, int kUnits, int kRows>
+__device__ __forceinline__ void store_sums(const NormBwdParams& p, const float (&sw)[kUnits][8],
+                                           const float (&sb)[kUnits][8]) {
+  constexpr int kCols = kLanes * kUnits * 8;
+  __shared__ float tot[kRows > 1 ? kCols : 1];
+  const int t = threadIdx.x % kLanes;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const float(&acc)[kUnits][8] = v ? sb : sw;
+    for (int r = 0; kRows > 1 && r < kRows; ++r) {
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) / kLanes == r) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float& at = tot[(i * kLanes + t) * 8 + j];
+            at = r == 0 ? acc[i][j] : at + acc[i][j];
+          }
+      }
+    }
+    float* out = p.partial + (static_cast<long long>(v) * gridDim.x + blockIdx.x) * p.N;
+    if constexpr (kRows > 1) {
+      __syncthreads();
+      for (int n = threadIdx.x; n < p.N; n += blockDim.x) out[n] = tot[n];
+    } else {
+      const bool whole = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int n = (i * kLanes + t) * 8;
+        if (n < p.N) store8<IGC_F32>(reinterpret_cast<char*>(out), n, p.N, whole, acc[i]);
+      }
+    }
+  }
+}
+
+// g and h of eight columns from dY (g) and S (h), with their part of the row's sums and of the
+// column sums.
+template <bool kSums>
+__device__ __forceinline__ void terms8(float mean, float rstd, const float (&w)[8], float (&g)[8],
+                                       float (&h)[8], uint64_t& c1, uint64_t& c2, float (&sw)[8],
+                                       float (&sb)[8]) {
+  const uint64_t m = pair(-mean, -mean), r = pair(rstd, rstd);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint64_t hh = mul2(add2(pair(h[j], h[j + 1]), m), r);
+    const uint64_t y = pair(g[j], g[j + 1]);
+    if constexpr (kSums) {
+      unpair(fma2(y, hh, pair(sw[j], sw[j + 1])), sw[j], sw[j + 1]);
+      unpair(add2(y, pair(sb[j], sb[j + 1])), sb[j], sb[j + 1]);
+    }
+    const uint64_t gg = mul2(y, pair(w[j], w[j + 1]));
+    // (past the row's end dY and so g are 0)
+    c1 = add2(c1, gg);
+    c2 = fma2(gg, hh, c2);
+    unpair(gg, g[j], g[j + 1]);
+    unpair(hh, h[j], h[j + 1]);
   }
 }
 
@@ -60,8 +122,7 @@ template <int kT, int kS, int kLanes, int kUnits, bool kDrop, bool kSums>
 __global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes)
     layer_norm_bwd_kernel(const NormBwdParams p) {
   constexpr int kRows = kLanes < 128 ? 128 / kLanes : 1;
-  constexpr int kCols = kLanes * kUnits * 8;
-  __shared__ float red[2][2][kLanes / 32];
+  __shared__ __align__(16) float2 red[2][(kLanes / 32 + 1) / 2 * 2];
   grid_dependency_wait();
   grid_dependents_launch();
   const int t = threadIdx.x % kLanes;
@@ -75,7 +136,7 @@ __global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes)
     const float mean = p.mean[row], rstd = p.rstd[row];
     float g[kUnits][8], h[kUnits][8];
     Raw8<kS> a[kUnits];
-    float c1 = 0.0f, c2 = 0.0f;
+    uint64_t p1 = 0, p2 = 0;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int n = (i * kLanes + t) * 8;
@@ -87,123 +148,228 @@ __global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes)
       load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, w);
       unpack8<kT>(y, g[i]);
       unpack8<kS>(s, h[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[i][j] = (h[i][j] - mean) * rstd;
-        if constexpr (kSums) {
-          sw[i][j] += g[i][j] * h[i][j];
-          sb[i][j] += g[i][j];
-        }
-        g[i][j] *= w[j];
-        // (past the row's end dY and so g are 0)
-        c1 += g[i][j];
-        c2 += g[i][j] * h[i][j];
-      }
+      terms8<kSums>(mean, rstd, w, g[i], h[i], p1, p2, sw[kSums ? i : 0], sb[kSums ? i : 0]);
     }
-    // (the next row uses the other pair of arrays: no barrier after the reads)
-    c1 = warp_sum_all(c1);
-    c2 = warp_sum_all(c2);
-    if constexpr (kLanes > 32) {
-      if (threadIdx.x % 32 == 0) {
-        red[phase][0][threadIdx.x / 32] = c1;
-        red[phase][1][threadIdx.x / 32] = c2;
-      }
-      __syncthreads();
-      c1 = c2 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kLanes / 32; ++i) {
-        c1 += red[phase][0][i];
-        c2 += red[phase][1][i];
-      }
-    }
+    float c1 = sum2(p1), c2 = sum2(p2);
+    // (the next row uses the other array: no barrier after the reads)
+    row_sums<kLanes>(c1, c2, red[phase]);
     c1 *= inv;
     c2 *= inv;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int n = (i * kLanes + t) * 8;
       if (n < p.N)
-        grads8<kT, kS, kDrop>(p, offset, row, n, vec, rstd, c1, c2, a[i], g[i], h[i]);
+        grads8<kT, kS, kDrop>(p, offset, row, row_at<kS>(p.dS, row, p.ldds),
+                              row_at<kT>(p.dX, row, p.lddx), n, vec, rstd, c1, c2, a[i], g[i],
+                              h[i]);
     }
   }
-  if constexpr (kSums) {
-    // one row of sums per block: the block's rows of threads add theirs in order
-    __shared__ float tot[kRows > 1 ? kCols : 1];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      float(&acc)[kUnits][8] = v ? sb : sw;
-      for (int r = 0; kRows > 1 && r < kRows; ++r) {
-        __syncthreads();
-        if (static_cast<int>(threadIdx.x) / kLanes == r) {
-#pragma unroll
-          for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float& at = tot[(i * kLanes + t) * 8 + j];
-              at = r == 0 ? acc[i][j] : at + acc[i][j];
-            }
+  if constexpr (kSums) store_sums<kLanes, kUnits, kRows>(p, sw, sb);
+}
+
+constexpr int kNormBwdStreamMost = 512;
+
+// The same with rows streamed through shared memory (row_stream.cuh), two units to a thread.
+template <int kT, int kS, int kLanes, bool kDrop>
+__global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
+    layer_norm_bwd_stream_kernel(const NormBwdParams p, const RowStream st) {
+  constexpr int kGroups = kNormBwdStreamMost / kLanes, kUnits = 2;
+  constexpr int kSizeT = kT == IGC_F32 ? 4 : 2, kSizeS = kS == IGC_F32 ? 4 : 2;
+  extern __shared__ __align__(128) char ring[];
+  __shared__ uint64_t full[kGroups][kMaxSlots];
+  __shared__ __align__(16) float2 red[kGroups][2][(kLanes / 32 + 1) / 2 * 2];
+  __shared__ int abort_flag;
+  const RowWalk walk = row_walk<kLanes, kGroups>(st, ring, full, &abort_flag, p.M);
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int t = walk.t, N8 = p.N / 8 * 8;
+  keep_weights<kT>(ring, st.plane, p.w, N8, p.w_f32);
+  __syncthreads();
+  const bool has_a = p.A != nullptr, has_s = p.dS != nullptr, has_x = p.dX != nullptr;
+  auto fill = [&](int k) {
+    const long long row = walk.first + k * walk.step;
+    const int slot = k % st.slots;
+    const char* const from[kStreamMats] = {row_at<kT>(p.dY, row, p.lddy),
+                                           row_at<kS>(p.S, row, p.lds),
+                                           row_at<kS>(p.A, row, p.lda)};
+    fill_slot(st, walk.slots + slot * st.slot_bytes, walk.bars + slot, from);
+  };
+  // A group of one warp refills a slot when its row is done; a larger one after the barrier of
+  // the next row, a row later: it fills one slot less at first.
+  constexpr int kBehind = kLanes == 32 ? 0 : 1;
+  if (t == 0)
+    for (int k = 0; k < walk.count && k < st.slots - kBehind; ++k) fill(k);
+  const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
+  const float inv = 1.0f / static_cast<float>(p.N);
+  float sw[kUnits][8] = {}, sb[kUnits][8] = {}, sw_last = 0.0f, sb_last = 0.0f;
+  // the column past the whole units that this thread has, if any; the next row's statistics and
+  // its elements there arrive during a row
+  const int last = N8 + t < p.N ? N8 + t : -1;
+  const float w_last =
+      last >= 0 && p.w != nullptr
+          ? load_vec(p.w, last, kT == IGC_F32 || p.w_f32, kT == IGC_BF16)
+          : 1.0f;
+  float mean = 0.0f, rstd = 0.0f, y_last = 0.0f, s_last = 0.0f, a_last = 0.0f;
+  auto load_last = [&](long long row) {
+    y_last = load1<kT>(row_at<kT>(p.dY, row, p.lddy), last);
+    s_last = load1<kS>(row_at<kS>(p.S, row, p.lds), last);
+    if (has_a) a_last = load1<kS>(row_at<kS>(p.A, row, p.lda), last);
+  };
+  if (walk.count > 0) {
+    mean = p.mean[walk.first], rstd = p.rstd[walk.first];
+    if (last >= 0) load_last(walk.first);
+  }
+  char* ds_row = row_at<kS>(p.dS, walk.first, p.ldds);
+  char* dx_row = row_at<kT>(p.dX, walk.first, p.lddx);
+  const long long ds_step = walk.step * p.ldds * kSizeS, dx_step = walk.step * p.lddx * kSizeT;
+  int stopped = -1;  // the row whose wait gave up
+  int slot = 0;
+  uint32_t phase = 0;
+  // whole: every lane of the warp has all its units, so that nothing keeps the loads and the
+  // arithmetic of different units apart (a branch for each unit exposes every unit's latency)
+  auto walk_rows = [&](auto whole) {
+    for (int k = 0; k < walk.count; ++k) {
+      const long long row = walk.first + k * walk.step;
+      const char* at = walk.slots + slot * st.slot_bytes;
+      float mean_next = 0.0f, rstd_next = 0.0f;
+      if (k + 1 < walk.count)
+        mean_next = p.mean[row + walk.step], rstd_next = p.rstd[row + walk.step];
+      // (a wait that gave up is reported; the group goes on to its end, without further copies)
+      if (!mbar_wait(walk.bars + slot, phase, st.wait_limit, &abort_flag, st.status,
+                     kSiteNormBwdRow) && stopped < 0)
+        stopped = k;
+      float g[kUnits][8], h[kUnits][8];
+      uint64_t p1 = 0, p2 = 0;
+  #pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int n = (i * kLanes + t) * 8;
+        if (!decltype(whole)::value && n >= N8) continue;
+        float wv[8];
+        kept_weights(ring, st.plane, n, wv);
+        load_unit<kT>(at + st.at[0] + n * kSizeT, g[i]);
+        load_unit<kS>(at + st.at[1] + n * kSizeS, h[i]);
+        terms8<true>(mean, rstd, wv, g[i], h[i], p1, p2, sw[i], sb[i]);
+      }
+      float c1 = sum2(p1), c2 = sum2(p2), g_last = 0.0f, h_last = 0.0f, f_last = a_last;
+      if (last >= 0) {
+        h_last = (s_last - mean) * rstd;
+        sw_last = fmaf(y_last, h_last, sw_last);
+        sb_last += y_last;
+        g_last = y_last * w_last;
+        c1 += g_last;
+        c2 = fmaf(g_last, h_last, c2);
+        if (k + 1 < walk.count) load_last(row + walk.step);
+      }
+      row_sums<kLanes>(c1, c2, red[walk.group][k & 1], walk.group);
+      if (kBehind && t == 0 && stopped < 0 && k + st.slots - 1 < walk.count)
+        fill(k + st.slots - 1);
+      c1 *= inv;
+      c2 *= inv;
+      const uint64_t r2 = pair(rstd, rstd), m1 = pair(-c1, -c1), m2 = pair(-c2, -c2);
+  #pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int n = (i * kLanes + t) * 8;
+        if (!decltype(whole)::value && n >= N8) continue;
+        float d[8], f[8] = {};
+        if (has_a) load_unit<kS>(at + st.at[2] + n * kSizeS, f);
+  #pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const uint64_t x =
+              fma2(pair(h[i][j], h[i][j + 1]), m2, add2(pair(g[i][j], g[i][j + 1]), m1));
+          unpair(fma2(x, r2, pair(f[j], f[j + 1])), d[j], d[j + 1]);
+        }
+        if (has_s) store_unit<kS>(ds_row + n * kSizeS, d);
+        if (has_x) {
+          if constexpr (kDrop) drop8(p.drop, offset, row, n, d);
+          store_unit<kT>(dx_row + n * kSizeT, d);
         }
       }
-      float* out = p.partial + (static_cast<long long>(v) * gridDim.x + blockIdx.x) * p.N;
-      if constexpr (kRows > 1) {
-        __syncthreads();
-        for (int n = threadIdx.x; n < p.N; n += blockDim.x) out[n] = tot[n];
-      } else {
-        const bool whole = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-          const int n = (i * kLanes + t) * 8;
-          if (n < p.N)
-            store8<IGC_F32>(reinterpret_cast<char*>(out), n, p.N, whole, acc[i]);
-        }
+      if (last >= 0) {
+        const float d = fmaf(rstd, fmaf(-h_last, c2, g_last - c1), f_last);
+        if (has_s) store1<kS>(ds_row, last, d);
+        if (has_x)
+          store1<kT>(dx_row, last, kDrop ? drop1(p.drop, offset, row, last, d, 0.0f) : d);
       }
+      if constexpr (!kBehind) {
+        __syncwarp();
+        if (t == 0 && stopped < 0 && k + st.slots < walk.count) fill(k + st.slots);
+      }
+      mean = mean_next, rstd = rstd_next;
+      ds_row += ds_step;
+      dx_row += dx_step;
+      if (++slot == st.slots) slot = 0, phase ^= 1u;
     }
+  };
+  if (__all_sync(0xffffffffu, ((kUnits - 1) * kLanes + t) * 8 < N8))
+    walk_rows(std::true_type{});
+  else
+    walk_rows(std::false_type{});
+  if (t == 0 && stopped >= 0)
+    drain_slots(st, walk.bars, stopped, min(walk.count, stopped + st.slots));
+  if (p.partial == nullptr) return;
+  // one row of sums per block: the groups' go over their rings, and are added in order
+  float* tot = reinterpret_cast<float*>(ring);
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const float(&acc)[kUnits][8] = v ? sb : sw;
+    float* to = tot + (walk.group * 2 + v) * p.N;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int n = (i * kLanes + t) * 8;
+      if (n >= N8) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) to[n + j] = acc[i][j];
+    }
+    if (last >= 0) to[last] = v ? sb_last : sw_last;
+  }
+  __syncthreads();
+  for (int n = threadIdx.x; n < p.N; n += kGroups * kLanes) {
+    float dw = 0.0f, db = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kGroups; ++r) {
+      dw += tot[2 * r * p.N + n];
+      db += tot[(2 * r + 1) * p.N + n];
+    }
+    p.partial[static_cast<long long>(blockIdx.x) * p.N + n] = dw;
+    p.partial[(static_cast<long long>(gridDim.x) + blockIdx.x) * p.N + n] = db;
   }
 }
 
 // Rows of any length, without the column sums: the row is read twice.
 template <int kT, int kS, bool kDrop>
 __global__ void __launch_bounds__(512) layer_norm_bwd_long_kernel(const NormBwdParams p) {
-  __shared__ float red[2][16];
+  __shared__ __align__(16) float2 red[16];
   grid_dependency_wait();
   grid_dependents_launch();
   const long long row = blockIdx.x;
   const bool vec = p.vec != 0;
   const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
   const float mean = p.mean[row], rstd = p.rstd[row];
-  auto terms = [&](int n, float(&g)[8], float(&h)[8]) {
+  uint64_t p1 = 0, p2 = 0;
+  float g[8], h[8], none[8];
+  auto terms = [&](int n) {
     const Raw8<kT> y = load8<kT>(row_at<kT>(p.dY, row, p.lddy), n, p.N, vec);
     const Raw8<kS> s = load8<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec);
     float w[8];
     load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, w);
     unpack8<kT>(y, g);
     unpack8<kS>(s, h);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[j] = (h[j] - mean) * rstd;
-      g[j] *= w[j];
-    }
+    terms8<false>(mean, rstd, w, g, h, p1, p2, none, none);
   };
-  float g[8], h[8], c1 = 0.0f, c2 = 0.0f;
-  for (long long n = threadIdx.x * 8; n < p.N; n += 512 * 8) {
-    terms(static_cast<int>(n), g, h);
-    float q1 = 0.0f, q2 = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      q1 += g[j];
-      q2 += g[j] * h[j];
-    }
-    c1 += q1;
-    c2 += q2;
-  }
+  for (long long n = threadIdx.x * 8; n < p.N; n += 512 * 8) terms(static_cast<int>(n));
+  float c1 = sum2(p1), c2 = sum2(p2);
   const float inv = 1.0f / static_cast<float>(p.N);
-  c1 = row_sum<512>(c1, red[0]) * inv;
-  c2 = row_sum<512>(c2, red[1]) * inv;
+  row_sums<512>(c1, c2, red);
+  c1 *= inv;
+  c2 *= inv;
   for (long long m = threadIdx.x * 8; m < p.N; m += 512 * 8) {
     const int n = static_cast<int>(m);
-    terms(n, g, h);
+    terms(n);
     Raw8<kS> a = {};
     if (p.A != nullptr) a = load8<kS>(row_at<kS>(p.A, row, p.lda), n, p.N, vec);
-    grads8<kT, kS, kDrop>(p, offset, row, n, vec, rstd, c1, c2, a, g, h);
+    grads8<kT, kS, kDrop>(p, offset, row, row_at<kS>(p.dS, row, p.ldds),
+                          row_at<kT>(p.dX, row, p.lddx), n, vec, rstd, c1, c2, a, g, h);
   }
 }
 
@@ -272,11 +438,43 @@ int launch_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, in
   return launch_pdl(kern, dim3(static_cast<unsigned>(*blocks)), dim3(kBlock), 0, stream, p);
 }
 
+// Streams the rows if each group of threads has more than two of them; *done: whether it did.
+template <int kT, int kS, int kLanes>
+int stream_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
+                    bool* done, cudaStream_t stream) {
+  constexpr int kGroups = kNormBwdStreamMost / kLanes;
+  RowStream st;
+  const int sizes[kStreamMats] = {static_cast<int>(elem_size(kT)), static_cast<int>(elem_size(kS)),
+                                  p.A != nullptr ? static_cast<int>(elem_size(kS)) : 0};
+  *done = p.vec && p.M > 2ll * dev.sm_count * kGroups &&
+          dev.sm_count <= norm_bwd_max_blocks(p.N) &&
+          plan_stream(dev, p.N, sizes, kGroups, &st);
+  if (!*done) return IGC_OK;
+  *blocks = dev.sm_count;
+  return launch_stream(drop ? layer_norm_bwd_stream_kernel<kT, kS, kLanes, true>
+                            : layer_norm_bwd_stream_kernel<kT, kS, kLanes, false>,
+                       dev, kGroups * kLanes, kGroups,
+                       static_cast<size_t>(kGroups) * p.N * 8, stream, p, st);
+}
+
 // *blocks: rows of partial sums that it leaves.
 template <int kT, int kS>
 int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
                  cudaStream_t stream) {
   const long long units = (static_cast<long long>(p.N) + 7) / 8;
+  bool done = false;
+  int rc = IGC_OK;
+  if (units <= 64)
+    rc = stream_norm_bwd<kT, kS, 32>(dev, p, drop, blocks, &done, stream);
+  else if (units <= 128)
+    rc = stream_norm_bwd<kT, kS, 64>(dev, p, drop, blocks, &done, stream);
+  else if (units <= 256)
+    rc = stream_norm_bwd<kT, kS, 128>(dev, p, drop, blocks, &done, stream);
+  else if (units <= 512)
+    rc = stream_norm_bwd<kT, kS, 256>(dev, p, drop, blocks, &done, stream);
+  else if (units <= 1024)
+    rc = stream_norm_bwd<kT, kS, 512>(dev, p, drop, blocks, &done, stream);
+  if (done) return rc;
   if (units <= 32) return launch_norm_bwd<kT, kS, 32, 1>(dev, p, drop, blocks, stream);
   if (units <= 64) return launch_norm_bwd<kT, kS, 32, 2>(dev, p, drop, blocks, stream);
   if (units <= 128) return launch_norm_bwd<kT, kS, 128, 1>(dev, p, drop, blocks, stream);

@@ -74,16 +74,36 @@ __device__ __forceinline__ void unpack8(const Raw8<kT>& r, float (&v)[8]) {
   }
 }
 
+// Rounds eight values and stores them at p, a 16-byte boundary.
+template <int kT>
+__device__ __forceinline__ void store_unit(char* p, const float (&v)[8]) {
+  if constexpr (kT == IGC_F32) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    constexpr bool bf16 = kT == IGC_BF16;
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16),
+                                              pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16));
+  }
+}
+// Eight elements at p, a 16-byte boundary.
+template <int kT>
+__device__ __forceinline__ void load_unit(const char* p, float (&v)[8]) {
+  Raw8<kT> r;
+  r.q[0] = reinterpret_cast<const uint4*>(p)[0];
+  if constexpr (kT == IGC_F32) r.q[1] = reinterpret_cast<const uint4*>(p)[1];
+  unpack8<kT>(r, v);
+}
+
 // Rounds eight values and stores those before the row's end.
 template <int kT>
 __device__ __forceinline__ void store8(char* row, int n, int N, bool vec, const float (&v)[8]) {
+  if (vec && n + 8 <= N) {
+    store_unit<kT>(row + static_cast<long long>(n) * (kT == IGC_F32 ? 4 : 2), v);
+    return;
+  }
   if constexpr (kT == IGC_F32) {
     float* p = reinterpret_cast<float*>(row) + n;
-    if (vec && n + 8 <= N) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (n + i < N) p[i] = v[i];
@@ -92,14 +112,25 @@ __device__ __forceinline__ void store8(char* row, int n, int N, bool vec, const 
     uint16_t* p = reinterpret_cast<uint16_t*>(row) + n;
     const uint32_t w[4] = {pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16),
                            pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16)};
-    if (vec && n + 8 <= N) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (n + i < N) p[i] = static_cast<uint16_t>(i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
   }
+}
+
+template <int kT>
+__device__ __forceinline__ float load1(const char* row, int n) {
+  if constexpr (kT == IGC_F32)
+    return reinterpret_cast<const float*>(row)[n];
+  else
+    return load16(row, n, kT == IGC_BF16);
+}
+template <int kT>
+__device__ __forceinline__ void store1(char* row, int n, float v) {
+  if constexpr (kT == IGC_F32)
+    reinterpret_cast<float*>(row)[n] = v;
+  else
+    store16(row, n, v, kT == IGC_BF16);
 }
 
 // Elements [n, n + 8) of a vector of N that is fp32 (f32) or of type kT; `none` for no vector
@@ -120,47 +151,96 @@ __device__ __forceinline__ void load_vec8(const void* p, int n, int N, bool f32,
 }
 
 // ---------------------------------------------------------------------------
+// two fp32 values in one instruction
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(uint64_t p) {
+  float lo, hi;
+  unpair(p, lo, hi);
+  return lo + hi;
+}
+
+// ---------------------------------------------------------------------------
 // dropout
 // ---------------------------------------------------------------------------
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC 2011): ten rounds, each two 32 x 32 -> 64 bit
-// products, two three-way exclusive ors and a step of the key.
-__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1) {
+// products and two three-way exclusive ors with the round's keys.
+constexpr int kPhiloxRounds = 10;
+
+struct Drop {
+  uint32_t key[kPhiloxRounds][2] = {};  // the seed, stepped from round to round
+  uint64_t offset = 0;
+  const uint64_t* step = nullptr;
+  uint32_t threshold = 0;  // T << 16 (T < 65536; no dropout is another variant of a kernel)
+  float scale = 1.0f;      // 65536 / T (0 for T = 0)
+};
+
+__device__ __forceinline__ uint4 philox(const Drop& d, uint4 c) {
 #pragma unroll
-  for (int r = 0; r < 10; ++r) {
+  for (int r = 0; r < kPhiloxRounds; ++r) {
     const uint64_t a = static_cast<uint64_t>(c.x) * 0xD2511F53u;
     const uint64_t b = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
-    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k0, static_cast<uint32_t>(b),
-                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k1, static_cast<uint32_t>(a));
-    k0 += 0x9E3779B9u, k1 += 0xBB67AE85u;
+    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ d.key[r][0], static_cast<uint32_t>(b),
+                   static_cast<uint32_t>(a >> 32) ^ c.w ^ d.key[r][1], static_cast<uint32_t>(a));
   }
   return c;
 }
 
-struct Drop {
-  uint32_t k0 = 0, k1 = 0;     // the seed
-  uint64_t offset = 0;
-  const uint64_t* step = nullptr;
-  uint32_t threshold = 0;      // T << 16 (T < 65536; no dropout is another variant of a kernel)
-  float scale = 1.0f;          // 65536 / T (0 for T = 0)
-};
-
-// v: eight elements of row `row` from column n (a multiple of 8) on, dropped and scaled.  One
-// block of Philox for all eight, 16 bits each: 5 instructions an element beside the 10 that 32
-// bits each would take, and p to 2^-17 is finer than a rate is ever set.  What is dropped is
-// selected away, not multiplied by 0: an infinity there leaves nothing.
+// v: eight elements of row `row` from column n (a multiple of 8) on; each becomes v * scale + r
+// if it is kept, else r.  One block of Philox for all eight, 16 bits each: 5 instructions an
+// element beside the 10 that 32 bits each would take, and p to 2^-17 is finer than a rate is
+// ever set.  What is dropped is selected away, not multiplied by 0: an infinity there leaves
+// nothing.
 __device__ __forceinline__ void drop8(const Drop& d, uint64_t offset, long long row, int n,
-                                      float (&v)[8]) {
-  const uint4 q = philox4x32_10(
-      make_uint4(static_cast<uint32_t>(n) / 8u, static_cast<uint32_t>(row),
-                 static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)),
-      d.k0, d.k1);
+                                      float (&v)[8], const float (&r)[8]) {
+  const uint4 q = philox(d, make_uint4(static_cast<uint32_t>(n) / 8u, static_cast<uint32_t>(row),
+                                       static_cast<uint32_t>(offset),
+                                       static_cast<uint32_t>(offset >> 32)));
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // a half is under T just where the word that has it as its upper half is under T << 16
-    v[2 * i] = (w[i] << 16) < d.threshold ? v[2 * i] * d.scale : 0.0f;
-    v[2 * i + 1] = w[i] < d.threshold ? v[2 * i + 1] * d.scale : 0.0f;
+    v[2 * i] = (w[i] << 16) < d.threshold ? fmaf(v[2 * i], d.scale, r[2 * i]) : r[2 * i];
+    v[2 * i + 1] = w[i] < d.threshold ? fmaf(v[2 * i + 1], d.scale, r[2 * i + 1]) : r[2 * i + 1];
   }
+}
+__device__ __forceinline__ void drop8(const Drop& d, uint64_t offset, long long row, int n,
+                                      float (&v)[8]) {
+  const float none[8] = {};
+  drop8(d, offset, row, n, v, none);
+}
+
+// One element, of column n.
+__device__ __forceinline__ float drop1(const Drop& d, uint64_t offset, long long row, int n,
+                                       float v, float r) {
+  const uint4 q = philox(d, make_uint4(static_cast<uint32_t>(n) / 8u, static_cast<uint32_t>(row),
+                                       static_cast<uint32_t>(offset),
+                                       static_cast<uint32_t>(offset >> 32)));
+  const int i = n % 8 / 2;
+  const uint32_t w = i < 2 ? (i == 0 ? q.x : q.y) : (i == 2 ? q.z : q.w);
+  return (n % 2 ? w : w << 16) < d.threshold ? fmaf(v, d.scale, r) : r;
 }
 
 __device__ __forceinline__ uint64_t drop_offset(const Drop& d) {
@@ -176,21 +256,67 @@ __device__ __forceinline__ float warp_sum_all(float v) {
   return v;
 }
 
-// kThreads = 32: a warp; else the whole block of kThreads threads, through red (one array of
-// kThreads / 32 values for each sum that may be in flight between two barriers).
+// A barrier of the kThreads threads of group `group` (of a block that is all of them, or several
+// groups: each has a barrier of its own).
 template <int kThreads>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+__device__ __forceinline__ void group_sync(int group) {
+  if constexpr (kThreads == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kThreads) : "memory");
+}
+
+// kThreads = 32: a warp; else a group of kThreads threads, through its red (16-byte aligned; one
+// array of kThreads / 32 values for each sum that may be in flight between two barriers).
+template <int kThreads>
+__device__ __forceinline__ float row_sum(float v, float* red, int group = 0) {
   v = warp_sum_all(v);
   if constexpr (kThreads > 32) {
     constexpr int kWarps = kThreads / 32;
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    float s[4] = {};
+    if (threadIdx.x % 32 == 0) red[threadIdx.x % kThreads / 32] = v;
+    group_sync<kThreads>(group);
+    if constexpr (kWarps % 4 == 0) {
+      uint64_t s = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) s[i % 4] += red[i];
-    v = (s[0] + s[1]) + (s[2] + s[3]);
+      for (int i = 0; i < kWarps / 4; ++i) {
+        const float4 q = reinterpret_cast<const float4*>(red)[i];
+        s = add2(s, add2(pair(q.x, q.y), pair(q.z, q.w)));
+      }
+      v = sum2(s);
+    } else {
+      v = red[0];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) v += red[i];
+    }
   }
   return v;
+}
+
+// Two sums at once; red: kThreads / 32 pairs.  Half the lanes carry one sum on, half the other.
+template <int kThreads>
+__device__ __forceinline__ void row_sums(float& a, float& b, float2* red, int group = 0) {
+  const int lane = threadIdx.x % 32;
+  const bool upper = lane >= 16;
+  float v = upper ? b : a;
+  v += __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (kThreads == 32) {
+    const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+    a = upper ? other : v;
+    b = upper ? v : other;
+  } else {
+    constexpr int kWarps = kThreads / 32;
+    if (lane % 16 == 0) reinterpret_cast<float*>(red + threadIdx.x % kThreads / 32)[upper] = v;
+    group_sync<kThreads>(group);
+    uint64_t s = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps / 2; ++i) {
+      const float4 q = reinterpret_cast<const float4*>(red)[i];
+      s = add2(s, add2(pair(q.x, q.y), pair(q.z, q.w)));
+    }
+    unpair(s, a, b);
+  }
 }
 
 }  // namespace igc

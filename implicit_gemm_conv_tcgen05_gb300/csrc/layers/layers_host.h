@@ -19,8 +19,10 @@ inline bool make_drop(double p, uint64_t seed, uint64_t offset, const uint64_t* 
   if (!(p >= 0.0 && p <= 1.0)) return false;
   const uint32_t T = static_cast<uint32_t>(std::nearbyint((1.0 - p) * 65536.0));
   *active = T < 65536u;
-  d->k0 = static_cast<uint32_t>(seed);
-  d->k1 = static_cast<uint32_t>(seed >> 32);
+  for (uint32_t r = 0; r < kPhiloxRounds; ++r) {
+    d->key[r][0] = static_cast<uint32_t>(seed) + r * 0x9E3779B9u;
+    d->key[r][1] = static_cast<uint32_t>(seed >> 32) + r * 0xBB67AE85u;
+  }
   d->offset = offset;
   d->step = step;
   d->threshold = T << 16;

@@ -1,0 +1,116 @@
+// Rows streamed through shared memory.  One block to an SM; the threads that share a row (a
+// group of kLanes) walk down the rows group, group + groups, ... and keep a ring of slots, each
+// filled with one row of every input by bulk copies ahead of its use, so that loads stay in
+// flight while earlier rows are summed and written.  The columns' weights are kept in shared
+// memory as fp32.
+//
+// A copy needs 16-byte boundaries and sizes: it takes the whole units of eight columns of a row.
+// The columns past them (N mod 8) are one element each for the group's first threads, loaded a
+// row ahead.
+#pragma once
+
+#include "layers.cuh"
+
+namespace igc {
+
+// Threads of a block, one to an SM: whole groups of kLanes, at most kMost.
+constexpr int stream_threads(int lanes, int most) { return most / lanes * lanes; }
+constexpr int kMaxSlots = 4;
+constexpr int kStreamMats = 3;  // inputs of a row, at most
+
+// The ring of one launch, in bytes: a slot is one row of each input, 16-byte aligned.
+struct RowStream {
+  int slots = 0;
+  uint32_t slot_bytes = 0;
+  uint32_t at[kStreamMats] = {};     // where an input's row starts in its slot
+  uint32_t bytes[kStreamMats] = {};  // copied of it (0: the input is absent)
+  uint32_t plane = 0;                // bytes of each half of the kept weights, ahead of the ring
+  uint64_t wait_limit = 0;
+  unsigned long long* status = nullptr;
+};
+
+// Sites of waits that gave up (device status word).
+enum : uint32_t { kSiteNormRow = 0x4c01, kSiteNormBwdRow = 0x4c02, kSiteRowDrain = 0x4c03 };
+
+__device__ __forceinline__ void bulk_load(uint32_t dst_smem, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst_smem),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// One thread: the row's inputs (rows[i]: where input i's row starts) into a slot.
+__device__ __forceinline__ void fill_slot(const RowStream& s, char* slot, uint64_t* bar,
+                                          const char* const (&rows)[kStreamMats]) {
+  uint32_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kStreamMats; ++i) total += s.bytes[i];
+  mbar_arrive_expect_tx(bar, total);
+  const uint32_t to = smem_u32(slot);
+#pragma unroll
+  for (int i = 0; i < kStreamMats; ++i)
+    if (s.bytes[i] != 0) bulk_load(to + s.at[i], rows[i], s.bytes[i], bar);
+}
+
+// The whole block: the weights of the whole units (fp32, or of type kT; 1 for none) into shared
+// memory, the first four of each unit in one plane and the last four in another: a warp's
+// 16-byte loads then meet no bank twice.
+template <int kT>
+__device__ __forceinline__ void keep_weights(char* to, uint32_t plane, const void* p, int N8,
+                                             bool f32) {
+  for (int n = threadIdx.x; n < N8; n += blockDim.x) {
+    const float v = p == nullptr ? 1.0f : load_vec(p, n, kT == IGC_F32 || f32, kT == IGC_BF16);
+    reinterpret_cast<float*>(to + n % 8 / 4 * plane)[n / 8 * 4 + n % 4] = v;
+  }
+}
+__device__ __forceinline__ void kept_weights(const char* from, uint32_t plane, int n,
+                                             float (&w)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(from)[n / 8];
+  const float4 b = reinterpret_cast<const float4*>(from + plane)[n / 8];
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+// After a wait gave up, the group's leader: the copies in flight (of its rows next, next + 1, ...
+// last - 1) are waited for, again with a limit, so that none lands after the block has gone.
+__device__ __forceinline__ void drain_slots(const RowStream& s, uint64_t* bars, int next,
+                                            int last) {
+  volatile int none = 0;
+  for (int k = next; k < last; ++k)
+    (void)mbar_wait(bars + k % s.slots, static_cast<uint32_t>(k / s.slots) & 1u, s.wait_limit,
+                    &none, s.status, kSiteRowDrain);
+}
+
+// A group's walk: rows first, first + step, ... (count of them), its slots and barriers.
+struct RowWalk {
+  long long first, step;
+  int count;
+  int t, group;
+  char* slots;
+  uint64_t* bars;
+};
+
+// The start of a streaming kernel: barriers and walk (ring: the dynamic shared memory).
+template <int kLanes, int kGroups>
+__device__ __forceinline__ RowWalk row_walk(const RowStream& st, char* ring,
+                                            uint64_t (&full)[kGroups][kMaxSlots],
+                                            int* abort_flag, int M) {
+  RowWalk w;
+  w.t = threadIdx.x % kLanes;
+  w.group = threadIdx.x / kLanes;
+  w.slots = ring + 2 * st.plane + w.group * (st.slots * st.slot_bytes);
+  w.bars = full[w.group];
+  if (w.t == 0) {
+    for (int i = 0; i < st.slots; ++i) mbar_init(w.bars + i, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) *abort_flag = 0;
+  w.first = static_cast<long long>(blockIdx.x) * kGroups + w.group;
+  w.step = static_cast<long long>(gridDim.x) * kGroups;
+  w.count = w.first < M ? static_cast<int>((M - w.first + w.step - 1) / w.step) : 0;
+  return w;
+}
+
+}  // namespace igc

@@ -1,0 +1,52 @@
+// Host side of the rows streamed through shared memory: the ring's plan and its launch.
+#pragma once
+
+#include "layers_host.h"
+#include "row_stream.cuh"
+
+namespace igc {
+
+constexpr int kStreamStatic = 3072;  // bytes for the kernels' static shared memory
+
+// The ring for rows of N columns whose inputs have elements of sizes[i] bytes (0: absent), with
+// `groups` rings to a block: false where rows are too short or too long for one (at least two
+// slots).
+inline bool plan_stream(const DeviceInfo& dev, int64_t N, const int (&sizes)[kStreamMats],
+                        int groups, RowStream* s) {
+  if (N < 64) return false;
+  uint32_t at = 0;
+  for (int i = 0; i < kStreamMats; ++i) {
+    s->at[i] = at;
+    s->bytes[i] = static_cast<uint32_t>(N / 8 * 8 * sizes[i]);
+    at += s->bytes[i];
+  }
+  s->slot_bytes = (at + 127) / 128 * 128;
+  s->plane = static_cast<uint32_t>((N / 8 * 16 + 127) / 128 * 128);
+  const size_t room = dev.smem_optin - kStreamStatic;
+  if (2 * s->plane >= room) return false;
+  const size_t slots = (room - 2 * s->plane) / (static_cast<size_t>(groups) * s->slot_bytes);
+  if (slots < 2) return false;
+  s->slots = static_cast<int>(slots < kMaxSlots ? slots : kMaxSlots);
+  s->wait_limit = wait_limit_ns();
+  s->status = status_word();
+  return true;
+}
+
+// least: bytes of dynamic shared memory that the kernel uses whatever the ring takes.
+template <typename P>
+int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int threads, int groups,
+                  size_t least, cudaStream_t stream, const P& p, const RowStream& s) {
+  // (the attribute belongs to the function: set by every call, which costs less than to look
+  // whether it is)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(dev.smem_optin) - kStreamStatic) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return IGC_ERR_CUDA;
+  }
+  const size_t bytes = static_cast<size_t>(2) * s.plane +
+                       static_cast<size_t>(groups) * s.slots * s.slot_bytes;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(dev.sm_count)), dim3(static_cast<unsigned>(threads)),
+                    bytes < least ? least : bytes, stream, p, s);
+}
+
+}  // namespace igc
