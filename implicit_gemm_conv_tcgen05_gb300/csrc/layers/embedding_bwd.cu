@@ -8,8 +8,8 @@
 // Further blocks write the zeros of the rows that no token points to.
 //
 // Many: the positions are sorted by token first (stable, so that a token's positions stay in
-// order), by a cluster of eight blocks with a radix sort.  Blocks then walk chunks of 32 sorted
-// positions and write each token's sum; the sums of a token that crosses a chunk's border go to
+// order), by a cluster of eight blocks with a radix sort.  Blocks then walk chunks of 32 to 128
+// sorted positions and write each token's sum; the sums of a token that crosses a chunk's border go to
 // the workspace, and a last kernel adds them in order.  No atomics on sums.
 #include "layers_host.h"
 
@@ -21,8 +21,9 @@ constexpr int kThreads = 128;       // of a block over 1024 columns
 constexpr int kSmallUnits = 64, kSmallSubs = 4;  // few positions: 512 columns, four shares of rows
 constexpr int kSmallThreads = kSmallUnits * kSmallSubs;
 constexpr int kSmallM = 1024;       // positions up to which one launch does
-constexpr int kChunk = 32;          // sorted positions of a block
-constexpr int kAhead = 8;           // rows that a thread loads before it adds the first
+constexpr int kMinChunk = 32, kMaxChunk = 128;  // sorted positions of a block
+constexpr int kAhead = 8, kSmallAhead = 4;  // rows that a thread loads before it adds the first
+constexpr int kZeroRows = 64;       // of a block that writes zeros, at most
 constexpr int kCtas = 8;            // of the sorting cluster
 constexpr int kSortThreads = 1024, kSortWarps = kCtas * (kSortThreads / 32);
 constexpr int kMaxDigit = 512;      // values of a digit of the radix sort
@@ -30,16 +31,17 @@ constexpr int kMaxDigit = 512;      // values of a digit of the radix sort
 struct EmbedParams {
   int M, D, vec, token64, accumulate;
   int slabs;                 // blocks to a row
-  int zero_rows;             // rows of a block that writes zeros
+  int chunk;                 // sorted positions of a block
+  int zero_rows;             // rows of a block that writes zeros, and those blocks
+  unsigned zero_blocks;
   long long V;
   const void* tokens;
   const void* dY;
   void* dW;
   long long lddy, lddw;
   float scale;
-  uint32_t* keys[2];         // sorted tokens (V: none of the table's), and their positions
-  uint32_t* pos[2];
-  uint32_t* touched;         // a bit for each row of dW that a token points to
+  uint2* pairs[2];           // sorted: token (V: none of the table's) and position
+  uint8_t* touched;          // 1 for each row of dW that a token points to
   float* partial;            // [chunk][2][D]: sums of a chunk's first and last token
   int digit_bits, passes;
 };
@@ -47,6 +49,22 @@ struct EmbedParams {
 __device__ __forceinline__ long long token_at(const EmbedParams& p, int i) {
   return p.token64 ? static_cast<const long long*>(p.tokens)[i]
                    : static_cast<const int*>(p.tokens)[i];
+}
+
+// Tokens first + k * step (k < kN) that lie before M, -1 for the others: all loaded before the
+// first is looked at.
+template <int kN>
+__device__ __forceinline__ void tokens_at(const EmbedParams& p, long long first, int step,
+                                          long long (&v)[kN]) {
+  if (p.token64) {
+    const long long* t = static_cast<const long long*>(p.tokens);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) v[k] = first + k * step < p.M ? t[first + k * step] : -1;
+  } else {
+    const int* t = static_cast<const int*>(p.tokens);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) v[k] = first + k * step < p.M ? t[first + k * step] : -1;
+  }
 }
 
 // dW[v] (8 columns) = scale * acc, added to what is there when accumulating.
@@ -86,26 +104,21 @@ __device__ __forceinline__ void zero_row(const EmbedParams& p, long long v, bool
 // few positions
 // ---------------------------------------------------------------------------
 template <int kY, int kW>
-__global__ void __launch_bounds__(kSmallThreads) embed_small_kernel(const EmbedParams p) {
+__global__ void __launch_bounds__(kSmallThreads, 4) embed_small_kernel(const EmbedParams p) {
   __shared__ uint32_t bits[kSmallM / 32];
   __shared__ float4 tot[kSmallSubs - 1][2][kSmallUnits];
   grid_dependency_wait();
   grid_dependents_launch();
   const bool vec = p.vec != 0;
-  const long long token_blocks = static_cast<long long>(p.M) * p.slabs;
   constexpr int kPer = kSmallM / kSmallThreads;
-  if (blockIdx.x >= token_blocks) {
+  if (blockIdx.x < p.zero_blocks) {
     // the rows [v0, v1): bits says which a token points to
-    const long long v0 = (blockIdx.x - token_blocks) * p.zero_rows;
+    const long long v0 = static_cast<long long>(blockIdx.x) * p.zero_rows;
     const long long v1 = min(p.V, v0 + p.zero_rows);
     if (threadIdx.x < 2) bits[threadIdx.x] = 0;
     __syncthreads();
     long long v[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int j = k * kSmallThreads + static_cast<int>(threadIdx.x);
-      v[k] = j < p.M ? token_at(p, j) : -1;
-    }
+    tokens_at<kPer>(p, threadIdx.x, kSmallThreads, v);
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (v[k] >= v0 && v[k] < v1) atomicOr(&bits[(v[k] - v0) / 32], 1u << ((v[k] - v0) % 32));
@@ -114,15 +127,11 @@ __global__ void __launch_bounds__(kSmallThreads) embed_small_kernel(const EmbedP
       if (!(bits[(r - v0) / 32] >> ((r - v0) % 32) & 1u)) zero_row<kW, kSmallThreads>(p, r, vec);
     return;
   }
-  const int i = static_cast<int>(blockIdx.x / p.slabs);
+  const int i = static_cast<int>((blockIdx.x - p.zero_blocks) / p.slabs);
   // bit j: position j holds the same token as position i
   const int words = (p.M + 31) / 32;
   long long held[kPer];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int j = k * kSmallThreads + static_cast<int>(threadIdx.x);
-    held[k] = j < p.M ? token_at(p, j) : -1;
-  }
+  tokens_at<kPer>(p, threadIdx.x, kSmallThreads, held);
   const long long v = token_at(p, i);
   if (v < 0 || v >= p.V) return;
 #pragma unroll
@@ -136,17 +145,18 @@ __global__ void __launch_bounds__(kSmallThreads) embed_small_kernel(const EmbedP
   if (earlier != 0 || (bits[i / 32] & ((1u << (i % 32)) - 1u)) != 0) return;
   const int unit = static_cast<int>(threadIdx.x) % kSmallUnits;
   const int sub = static_cast<int>(threadIdx.x) / kSmallUnits;
-  const int n = (static_cast<int>(blockIdx.x % p.slabs) * kSmallUnits + unit) * 8;
-  // of the token's positions in order, each share has every kSmallSubs-th; it loads kAhead rows
+  const int n =
+      (static_cast<int>((blockIdx.x - p.zero_blocks) % p.slabs) * kSmallUnits + unit) * 8;
+  // of the token's positions in order, each share has every kSmallSubs-th; it loads kSmallAhead rows
   // before it adds the first
   float acc[8] = {};
   int k = i / 32, count = 0;
   uint32_t left = bits[k];
   for (bool more = n < p.D; more;) {
-    Raw8<kY> y[kAhead];
+    Raw8<kY> y[kSmallAhead];
     int found = 0;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
+    for (int a = 0; a < kSmallAhead; ++a) {
       int j = -1;
       while (true) {
         while (left == 0 && k + 1 < words) left = bits[++k];
@@ -161,9 +171,9 @@ __global__ void __launch_bounds__(kSmallThreads) embed_small_kernel(const EmbedP
       found = a + 1;
     }
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
+    for (int a = 0; a < kSmallAhead; ++a)
       if (a < found) add8<kY>(y[a], acc);
-    more = found == kAhead;
+    more = found == kSmallAhead;
   }
   if (sub > 0) {
     tot[sub - 1][0][unit] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -207,31 +217,32 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
           : 0;
   const int batches = (run / 32 + kBatch - 1) / kBatch;
   uint32_t* mine = hist + warp * digits;
-  if (p.touched != nullptr)
+  if (p.touched != nullptr)  // (its place in the workspace is a multiple of 256 bytes)
     for (long long k = static_cast<long long>(rank) * kSortThreads + threadIdx.x;
-         k < (p.V + 31) / 32; k += kCtas * kSortThreads)
-      p.touched[k] = 0;
+         k < (p.V + 15) / 16; k += kCtas * kSortThreads)
+      reinterpret_cast<uint4*>(p.touched)[k] = make_uint4(0, 0, 0, 0);
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.digit_bits;
-    const uint32_t* keys_in = p.keys[(pass + p.passes) & 1];
-    const uint32_t* pos_in = p.pos[(pass + p.passes) & 1];
-    uint32_t* keys_out = p.keys[(pass + p.passes + 1) & 1];
-    uint32_t* pos_out = p.pos[(pass + p.passes + 1) & 1];
+    const uint2* in = p.pairs[(pass + p.passes) & 1];
+    uint2* out = p.pairs[(pass + p.passes + 1) & 1];
     uint32_t key[kBatch], pos[kBatch], at[kBatch];
     auto load = [&](int batch) {
+      const long long from = first + batch * (kBatch * 32) + lane;
+      if (pass == 0) {
+        long long v[kBatch];
+        tokens_at<kBatch>(p, from, 32, v);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int step = batch * kBatch + k;
-        const long long i = first + step * 32 + lane;
-        if (step >= steps || i >= p.M) continue;
-        if (pass > 0) {
-          key[k] = __ldcg(keys_in + i);
-          pos[k] = __ldcg(pos_in + i);
-        } else {
-          const long long v = token_at(p, static_cast<int>(i));
-          key[k] = static_cast<uint32_t>(v >= 0 && v < p.V ? v : p.V);
-          pos[k] = static_cast<uint32_t>(i);
+        for (int k = 0; k < kBatch; ++k) {
+          key[k] = static_cast<uint32_t>(v[k] >= 0 && v[k] < p.V ? v[k] : p.V);
+          pos[k] = static_cast<uint32_t>(from + k * 32);
         }
+      } else {
+        uint2 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          v[k] = from + k * 32 < p.M ? __ldcg(in + from + k * 32) : make_uint2(0, 0);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) key[k] = v[k].x, pos[k] = v[k].y;
       }
     };
     auto digit_of = [&](uint32_t v) {
@@ -309,20 +320,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
         if (step >= steps || first + step * 32 + lane >= p.M) continue;
         const uint32_t dg = digit_of(key[k]);
         const uint32_t to = base[dg] + at[k] + (kept ? mine[dg] : 0u);
-        keys_out[to] = key[k];
-        pos_out[to] = pos[k];
+        out[to] = make_uint2(key[k], pos[k]);
+        // (a byte that several positions set is set to the same)
+        if (pass == 0 && p.touched != nullptr && key[k] < p.V) p.touched[key[k]] = 1;
       }
     }
     cluster_sync();  // what the next pass, and a block's reads of the others' totals, rely on
-  }
-  // the rows of dW that a token points to, each set once (by every position, the atomics on the
-  // words of frequent tokens took 20 us of a training batch's 33)
-  if (p.touched == nullptr) return;
-  for (long long i = static_cast<long long>(rank) * kSortThreads + threadIdx.x; i < p.M;
-       i += kCtas * kSortThreads) {
-    const uint32_t v = __ldcg(p.keys[0] + i);
-    if (v < p.V && (i == 0 || __ldcg(p.keys[0] + i - 1) != v))
-      atomicOr(p.touched + v / 32, 1u << (v % 32));
   }
 }
 
@@ -331,35 +334,39 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
 // ---------------------------------------------------------------------------
 template <int kY, int kW>
 __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams p) {
-  __shared__ uint32_t keys[kChunk + 2], pos[kChunk];
+  __shared__ uint32_t keys[kMaxChunk + 2], pos[kMaxChunk];
   grid_dependency_wait();
   grid_dependents_launch();
   const bool vec = p.vec != 0;
-  const int chunks = (p.M + kChunk - 1) / kChunk;
-  const long long sum_blocks = static_cast<long long>(chunks) * p.slabs;
+  const int chunks = (p.M + p.chunk - 1) / p.chunk;
+  const unsigned sum_blocks = static_cast<unsigned>(chunks) * p.slabs;
   if (blockIdx.x >= sum_blocks) {
-    const long long v0 = (blockIdx.x - sum_blocks) * p.zero_rows;
+    const long long v0 = static_cast<long long>(blockIdx.x - sum_blocks) * p.zero_rows;
     const long long v1 = min(p.V, v0 + p.zero_rows);
+    if (v0 + static_cast<int>(threadIdx.x) < v1 && threadIdx.x < kZeroRows)
+      keys[threadIdx.x] = p.touched[v0 + threadIdx.x];
+    __syncthreads();
     for (long long v = v0; v < v1; ++v)
-      if (!(p.touched[v / 32] >> (v % 32) & 1u)) zero_row<kW, kThreads>(p, v, vec);
+      if (keys[v - v0] == 0) zero_row<kW, kThreads>(p, v, vec);
     return;
   }
   const int c = static_cast<int>(blockIdx.x / p.slabs);
-  const long long p0 = static_cast<long long>(c) * kChunk;
+  const long long p0 = static_cast<long long>(c) * p.chunk;
   const uint32_t none = static_cast<uint32_t>(p.V);
   // keys[k + 1]: token of the chunk's position k; a token that is not in the table before the
   // first position, after the last, and for what is not to be summed
-  if (threadIdx.x < kChunk + 2) {
-    const long long at = p0 + static_cast<int>(threadIdx.x) - 1;
-    keys[threadIdx.x] = at >= 0 && at < p.M ? p.keys[0][at] : none;
-    if (threadIdx.x > 0 && threadIdx.x <= kChunk) pos[threadIdx.x - 1] = at < p.M ? p.pos[0][at] : 0u;
+  for (int k = threadIdx.x; k < p.chunk + 2; k += kThreads) {
+    const long long at = p0 + k - 1;
+    const uint2 v = at >= 0 && at < p.M ? p.pairs[0][at] : make_uint2(none, 0);
+    keys[k] = v.x;
+    if (k > 0 && k <= p.chunk) pos[k - 1] = v.y;
   }
   __syncthreads();
   const int n = (static_cast<int>(blockIdx.x % p.slabs) * kThreads + static_cast<int>(threadIdx.x)) * 8;
   if (n >= p.D) return;
   float acc[8] = {};
   bool from_start = keys[0] == keys[1];  // the token at hand began in an earlier chunk
-  for (int k0 = 0; k0 < kChunk; k0 += kAhead) {
+  for (int k0 = 0; k0 < p.chunk; k0 += kAhead) {
     Raw8<kY> y[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams 
       const uint32_t v = keys[k0 + k + 1];
       if (v == none) return;  // the rest holds no tokens of the table
       add8<kY>(y[k], acc);
-      const bool last = k0 + k == kChunk - 1, goes_on = keys[k0 + k + 2] == v;
+      const bool last = k0 + k == p.chunk - 1, goes_on = keys[k0 + k + 2] == v;
       if (goes_on && !last) continue;
       if (from_start || goes_on) {
         float* out = p.partial + (static_cast<long long>(c) * 2 + (from_start ? 0 : 1)) * p.D;
@@ -387,9 +394,9 @@ __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams 
 }
 
 // Tokens that cross chunks: the sum of the chunk where one begins and of those it goes on in.
-// A block has 256 columns and looks at 16 chunks, a warp at each: a token that goes on in few
-// chunks is the warp's, one that goes on in many is then shared by all 16 warps.
-constexpr int kJoinWarps = 16;
+// A block has 256 columns and looks at 8 chunks, a warp at each: a token that goes on in few
+// chunks is the warp's, one that goes on in many is then shared by all 8 warps.
+constexpr int kJoinWarps = 8, kJoinAhead = 4;
 
 template <int kW>
 __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const EmbedParams p) {
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
   grid_dependency_wait();
   grid_dependents_launch();
   const bool vec = p.vec != 0;
-  const int chunks = (p.M + kChunk - 1) / kChunk;
+  const int chunks = (p.M + p.chunk - 1) / p.chunk;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const long long n0 = static_cast<long long>(blockIdx.y) * 256 + lane * 8;
   const int n = static_cast<int>(n0);
@@ -410,35 +417,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
                           (reinterpret_cast<uintptr_t>(from) & 15u) == 0);
   };
   const int mine = blockIdx.x * kJoinWarps + warp;
-  const long long p0 = static_cast<long long>(mine) * kChunk, next = p0 + kChunk;
+  const long long p0 = static_cast<long long>(mine) * p.chunk, next = p0 + p.chunk;
   int end = -1;
   uint32_t v = 0;
   if (next < p.M) {
-    v = p.keys[0][next - 1];
-    const uint32_t after = p.keys[0][next];
-    const uint32_t ahead = p0 > 0 ? p.keys[0][p0 - 1] : ~v;
+    v = p.pairs[0][next - 1].x;
+    const uint32_t after = p.pairs[0][next].x;
+    const uint32_t ahead = p0 > 0 ? p.pairs[0][p0 - 1].x : ~v;
     if (v < p.V && after == v && ahead != v) {
       // the chunk that it ends in: the tokens ascend, 32 chunks are looked at at once
       end = mine + 1;
       while (true) {
         const long long k = static_cast<long long>(end) + 1 + lane;
         const uint32_t more =
-            __ballot_sync(0xffffffffu, k < chunks && p.keys[0][k * kChunk] == v);
+            __ballot_sync(0xffffffffu, k < chunks && p.pairs[0][k * p.chunk].x == v);
         end += __popc(more);
         if (more != 0xffffffffu) break;
       }
     }
   }
-  const bool shared = end - mine >= kAhead;
+  const bool shared = end - mine >= kJoinAhead;
   if (lane == 0) long_end[warp] = end >= 0 && shared ? end : -1;
   if (end >= 0 && !shared && n0 < p.D) {
-    Raw8<IGC_F32> f[kAhead];
+    Raw8<IGC_F32> f[kJoinAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
+    for (int k = 0; k < kJoinAhead; ++k)
       if (mine + k <= end) f[k] = part(mine + k, mine);
     float acc[8] = {};
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
+    for (int k = 0; k < kJoinAhead; ++k)
       if (mine + k <= end) add8<IGC_F32>(f[k], acc);
     finish8<kW>(p, v, n, vec, acc);
   }
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
       for (int r = 1; r < kJoinWarps; ++r)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] += tot[r][lane * 8 + j];
-      finish8<kW>(p, p.keys[0][static_cast<long long>(c) * kChunk + kChunk - 1], n, vec, acc);
+      finish8<kW>(p, p.pairs[0][static_cast<long long>(c) * p.chunk + p.chunk - 1].x, n, vec, acc);
     }
   }
 }
@@ -467,10 +474,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
+// Fewer borders for tokens to cross where there are many positions, more blocks where few.
+inline int64_t chunk_of(int64_t M) {
+  int64_t chunk = kMinChunk;
+  while (chunk < kMaxChunk && M > chunk * 256) chunk *= 2;
+  return chunk;
+}
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct EmbedLayout {
-  size_t keys[2], pos[2], touched, partial, bytes;
+  size_t pairs[2], touched, partial, bytes;
 };
 EmbedLayout layout(int64_t M, int64_t V, int64_t D) {
   EmbedLayout l = {};
@@ -481,20 +494,18 @@ EmbedLayout layout(int64_t M, int64_t V, int64_t D) {
     return here;
   };
   if (M > kSmallM && V > 0 && D > 0) {
-    for (int i = 0; i < 2; ++i) {
-      l.keys[i] = take(static_cast<size_t>(M) * 4);
-      l.pos[i] = take(static_cast<size_t>(M) * 4);
-    }
-    l.touched = take(static_cast<size_t>((V + 31) / 32) * 4);
-    l.partial = take(static_cast<size_t>((M + kChunk - 1) / kChunk) * 2 * static_cast<size_t>(D) * 4);
+    for (int i = 0; i < 2; ++i) l.pairs[i] = take(static_cast<size_t>(M) * sizeof(uint2));
+    l.touched = take(static_cast<size_t>(V));
+    l.partial = take(static_cast<size_t>((M + chunk_of(M) - 1) / chunk_of(M)) * 2 * static_cast<size_t>(D) * 4);
   }
   l.bytes = at;
   return l;
 }
 
 template <int kY, int kW>
-int run(const EmbedParams& p, cudaStream_t stream) {
+int run(EmbedParams p, cudaStream_t stream) {
   const long long zero_blocks = p.accumulate ? 0 : (p.V + p.zero_rows - 1) / p.zero_rows;
+  p.zero_blocks = static_cast<unsigned>(zero_blocks);
   if (p.M <= kSmallM) {
     const long long blocks = static_cast<long long>(p.M) * p.slabs + zero_blocks;
     if (blocks > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
@@ -502,7 +513,7 @@ int run(const EmbedParams& p, cudaStream_t stream) {
     return launch_pdl(embed_small_kernel<kY, kW>, dim3(static_cast<unsigned>(blocks)),
                       dim3(kSmallThreads), 0, stream, p);
   }
-  const int chunks = (p.M + kChunk - 1) / kChunk;
+  const int chunks = (p.M + p.chunk - 1) / p.chunk;
   const long long blocks = static_cast<long long>(chunks) * p.slabs + zero_blocks;
   const long long join_cols = (static_cast<long long>(p.D) + 255) / 256;
   if (blocks > 0x7fffffff || join_cols > 65535) return IGC_ERR_UNSUPPORTED;
@@ -566,18 +577,16 @@ int embedding_backward(int64_t M, int64_t V, int64_t D, const void* tokens, int 
   p.accumulate = accumulate != 0;
   const int64_t slab = (M <= kSmallM ? kSmallUnits : kThreads) * 8;
   p.slabs = static_cast<int>((D + slab - 1) / slab);
+  p.chunk = static_cast<int>(chunk_of(M));
   // about 64 KB of zeros to a block
   const int64_t rows = 65536 / (D * static_cast<int64_t>(elem_size(dw_dtype)));
-  p.zero_rows = static_cast<int>(rows < 1 ? 1 : (rows > 64 ? 64 : rows));
+  p.zero_rows = static_cast<int>(rows < 1 ? 1 : (rows > kZeroRows ? kZeroRows : rows));
   p.tokens = tokens, p.dY = dY, p.dW = dW;
   p.lddy = lddy, p.lddw = lddw;
   p.scale = scale;
   char* ws = static_cast<char*>(workspace);
-  for (int i = 0; i < 2; ++i) {
-    p.keys[i] = reinterpret_cast<uint32_t*>(ws + l.keys[i]);
-    p.pos[i] = reinterpret_cast<uint32_t*>(ws + l.pos[i]);
-  }
-  p.touched = accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + l.touched);
+  for (int i = 0; i < 2; ++i) p.pairs[i] = reinterpret_cast<uint2*>(ws + l.pairs[i]);
+  p.touched = accumulate ? nullptr : reinterpret_cast<uint8_t*>(ws + l.touched);
   p.partial = reinterpret_cast<float*>(ws + l.partial);
   int bits = 1;
   while ((static_cast<int64_t>(1) << bits) <= V) ++bits;  // keys are 0 .. V
