@@ -635,9 +635,15 @@ def _check_device(dev, name):
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _handle(stream, dev):
@@ -977,13 +983,22 @@ def _type_code(t, name):
     return code
 
 
+_or_f32 = {}
+
+
 def _type_or_f32(dtype):
-    f32 = _torch().float32
-    return (dtype,) if dtype is f32 else (dtype, f32)
+    """(dtype, fp32), of which dtype may be the one."""
+    types = _or_f32.get(dtype)
+    if types is None:
+        f32 = _torch().float32
+        types = _or_f32[dtype] = (dtype,) if dtype is f32 else (dtype, f32)
+    return types
 
 
 def _drop_args(p, seed, offset, step, dev):
     """(p, seed, offset, pointer of step) of a call with dropout."""
+    if p == 0.0 and seed is None and step is None and offset == 0:
+        return 0.0, 0, 0, None
     p = float(p)
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p is {p}: a probability is needed")
@@ -1004,7 +1019,7 @@ def _drop_args(p, seed, offset, step, dev):
 
 def _floats(v, name, n, dev):
     """Pointer of an optional fp32 vector of n elements."""
-    return _vector(v, name, (_torch().float32,), n, dev)[0]
+    return None if v is None else _vector(v, name, (_torch().float32,), n, dev)[0]
 
 
 def dropout_add(X, p, seed=None, offset=0, step=None, residual=None, Y=None, stream=None):

@@ -46,8 +46,7 @@ extern "C" {
 
 size_t layer_norm_backward_workspace_size(int64_t M, int64_t N) {
   if (M < 0 || N < 0) return 0;
-  const int64_t most = norm_bwd_max_blocks(N);
-  return static_cast<size_t>(2) * static_cast<size_t>(M < most ? M : most) *
+  return static_cast<size_t>(2) * static_cast<size_t>(M < kMaxPartials ? M : kMaxPartials) *
          static_cast<size_t>(N) * sizeof(float);
 }
 

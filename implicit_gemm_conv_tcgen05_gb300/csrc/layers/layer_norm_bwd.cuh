@@ -30,8 +30,7 @@ struct NormBwdParams {
   Drop drop;
 };
 
-// Blocks whose partial sums the workspace has room for.
-inline int64_t norm_bwd_max_blocks(int64_t N) { return N <= 1024 ? 1216 : 608; }
+constexpr int kMaxPartials = 512;  // rows of partial sums that the workspace has room for
 
 // dS and dX of eight columns from g, h and the row's sums; ds_row and dx_row are where the
 // row's dS and dX start.
@@ -52,43 +51,6 @@ __device__ __forceinline__ void grads8(const NormBwdParams& p, uint64_t offset, 
   if (p.dX != nullptr) {
     if constexpr (kDrop) drop8(p.drop, offset, row, n, d);
     store8<kT>(dx_row, n, p.N, vec, d);
-  }
-}
-
-// One row of sums per block: its kRows groups of kLanes threads add theirs in order.
-template <int kLanes, int kUnits, int kRows>
-__device__ __forceinline__ void store_sums(const NormBwdParams& p, const float (&sw)[kUnits][8],
-                                           const float (&sb)[kUnits][8]) {
-  constexpr int kCols = kLanes * kUnits * 8;
-  __shared__ float tot[kRows > 1 ? kCols : 1];
-  const int t = threadIdx.x % kLanes;
-#pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    const float(&acc)[kUnits][8] = v ? sb : sw;
-    for (int r = 0; kRows > 1 && r < kRows; ++r) {
-      __syncthreads();
-      if (static_cast<int>(threadIdx.x) / kLanes == r) {
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float& at = tot[(i * kLanes + t) * 8 + j];
-            at = r == 0 ? acc[i][j] : at + acc[i][j];
-          }
-      }
-    }
-    float* out = p.partial + (static_cast<long long>(v) * gridDim.x + blockIdx.x) * p.N;
-    if constexpr (kRows > 1) {
-      __syncthreads();
-      for (int n = threadIdx.x; n < p.N; n += blockDim.x) out[n] = tot[n];
-    } else {
-      const bool whole = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int n = (i * kLanes + t) * 8;
-        if (n < p.N) store8<IGC_F32>(reinterpret_cast<char*>(out), n, p.N, whole, acc[i]);
-      }
-    }
   }
 }
 
@@ -116,60 +78,9 @@ __device__ __forceinline__ void terms8(float mean, float rstd, const float (&w)[
   }
 }
 
-// kLanes threads to a row, kUnits units of eight columns to a thread.  kSums: with the column
-// sums.
-template <int kT, int kS, int kLanes, int kUnits, bool kDrop, bool kSums>
-__global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes)
-    layer_norm_bwd_kernel(const NormBwdParams p) {
-  constexpr int kRows = kLanes < 128 ? 128 / kLanes : 1;
-  __shared__ __align__(16) float2 red[2][(kLanes / 32 + 1) / 2 * 2];
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int t = threadIdx.x % kLanes;
-  const bool vec = p.vec != 0;
-  const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
-  const float inv = 1.0f / static_cast<float>(p.N);
-  float sw[kSums ? kUnits : 1][8] = {}, sb[kSums ? kUnits : 1][8] = {};
-  int phase = 0;
-  for (long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / kLanes;
-       row < p.M; row += static_cast<long long>(gridDim.x) * kRows, phase ^= 1) {
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float g[kUnits][8], h[kUnits][8];
-    Raw8<kS> a[kUnits];
-    uint64_t p1 = 0, p2 = 0;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int n = (i * kLanes + t) * 8;
-      if (n >= p.N) continue;
-      const Raw8<kT> y = load8<kT>(row_at<kT>(p.dY, row, p.lddy), n, p.N, vec);
-      const Raw8<kS> s = load8<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec);
-      if (p.A != nullptr) a[i] = load8<kS>(row_at<kS>(p.A, row, p.lda), n, p.N, vec);
-      float w[8];
-      load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, w);
-      unpack8<kT>(y, g[i]);
-      unpack8<kS>(s, h[i]);
-      terms8<kSums>(mean, rstd, w, g[i], h[i], p1, p2, sw[kSums ? i : 0], sb[kSums ? i : 0]);
-    }
-    float c1 = sum2(p1), c2 = sum2(p2);
-    // (the next row uses the other array: no barrier after the reads)
-    row_sums<kLanes>(c1, c2, red[phase]);
-    c1 *= inv;
-    c2 *= inv;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int n = (i * kLanes + t) * 8;
-      if (n < p.N)
-        grads8<kT, kS, kDrop>(p, offset, row, row_at<kS>(p.dS, row, p.ldds),
-                              row_at<kT>(p.dX, row, p.lddx), n, vec, rstd, c1, c2, a[i], g[i],
-                              h[i]);
-    }
-  }
-  if constexpr (kSums) store_sums<kLanes, kUnits, kRows>(p, sw, sb);
-}
+constexpr int kNormBwdStreamMost = 512;  // 128 registers each
 
-constexpr int kNormBwdStreamMost = 512;
-
-// The same with rows streamed through shared memory (row_stream.cuh), two units to a thread.
+// Rows streamed through shared memory (row_stream.cuh), two units to a thread.
 template <int kT, int kS, int kLanes, bool kDrop>
 __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
     layer_norm_bwd_stream_kernel(const NormBwdParams p, const RowStream st) {
@@ -336,9 +247,9 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   }
 }
 
-// Rows of any length, without the column sums: the row is read twice.
+// Rows of any length and alignment, without the column sums: the row is read twice.
 template <int kT, int kS, bool kDrop>
-__global__ void __launch_bounds__(512) layer_norm_bwd_long_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(512) layer_norm_bwd_any_kernel(const NormBwdParams p) {
   __shared__ __align__(16) float2 red[16];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -419,26 +330,7 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const NormBwdPa
   }
 }
 
-template <int kT, int kS, int kLanes, int kUnits>
-int launch_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
-                    cudaStream_t stream) {
-  constexpr int kRows = kLanes < 128 ? 128 / kLanes : 1;
-  constexpr int kBlock = kLanes * kRows;
-  const bool sums = p.partial != nullptr;
-  // about 1024 threads an SM
-  int64_t most = static_cast<int64_t>(dev.sm_count) * (kBlock >= 1024 ? 1 : 1024 / kBlock);
-  if (most > norm_bwd_max_blocks(p.N)) most = norm_bwd_max_blocks(p.N);
-  const int64_t all = (static_cast<int64_t>(p.M) + kRows - 1) / kRows;
-  *blocks = static_cast<int>(all < most ? all : most);
-  void (*kern)(NormBwdParams) =
-      drop ? (sums ? layer_norm_bwd_kernel<kT, kS, kLanes, kUnits, true, true>
-                   : layer_norm_bwd_kernel<kT, kS, kLanes, kUnits, true, false>)
-           : (sums ? layer_norm_bwd_kernel<kT, kS, kLanes, kUnits, false, true>
-                   : layer_norm_bwd_kernel<kT, kS, kLanes, kUnits, false, false>);
-  return launch_pdl(kern, dim3(static_cast<unsigned>(*blocks)), dim3(kBlock), 0, stream, p);
-}
-
-// Streams the rows if each group of threads has more than two of them; *done: whether it did.
+// *done: whether a block's shared memory holds two rows of every group.
 template <int kT, int kS, int kLanes>
 int stream_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
                     bool* done, cudaStream_t stream) {
@@ -446,14 +338,14 @@ int stream_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, in
   RowStream st;
   const int sizes[kStreamMats] = {static_cast<int>(elem_size(kT)), static_cast<int>(elem_size(kS)),
                                   p.A != nullptr ? static_cast<int>(elem_size(kS)) : 0};
-  *done = p.vec && p.M > 2ll * dev.sm_count * kGroups &&
-          dev.sm_count <= norm_bwd_max_blocks(p.N) &&
-          plan_stream(dev, p.N, sizes, kGroups, &st);
+  *done = plan_stream(dev, p.N, sizes, kGroups, &st);
   if (!*done) return IGC_OK;
-  *blocks = dev.sm_count;
+  const int64_t all = (static_cast<int64_t>(p.M) + kGroups - 1) / kGroups;
+  const int64_t most = dev.sm_count < kMaxPartials ? dev.sm_count : kMaxPartials;
+  *blocks = static_cast<int>(all < most ? all : most);
   return launch_stream(drop ? layer_norm_bwd_stream_kernel<kT, kS, kLanes, true>
                             : layer_norm_bwd_stream_kernel<kT, kS, kLanes, false>,
-                       dev, kGroups * kLanes, kGroups,
+                       dev, *blocks, kGroups * kLanes, kGroups,
                        static_cast<size_t>(kGroups) * p.N * 8, stream, p, st);
 }
 
@@ -464,7 +356,9 @@ int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* 
   const long long units = (static_cast<long long>(p.N) + 7) / 8;
   bool done = false;
   int rc = IGC_OK;
-  if (units <= 64)
+  if (!p.vec)
+    done = false;
+  else if (units <= 64)
     rc = stream_norm_bwd<kT, kS, 32>(dev, p, drop, blocks, &done, stream);
   else if (units <= 128)
     rc = stream_norm_bwd<kT, kS, 64>(dev, p, drop, blocks, &done, stream);
@@ -475,22 +369,16 @@ int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* 
   else if (units <= 1024)
     rc = stream_norm_bwd<kT, kS, 512>(dev, p, drop, blocks, &done, stream);
   if (done) return rc;
-  if (units <= 32) return launch_norm_bwd<kT, kS, 32, 1>(dev, p, drop, blocks, stream);
-  if (units <= 64) return launch_norm_bwd<kT, kS, 32, 2>(dev, p, drop, blocks, stream);
-  if (units <= 128) return launch_norm_bwd<kT, kS, 128, 1>(dev, p, drop, blocks, stream);
-  if (units <= 256) return launch_norm_bwd<kT, kS, 128, 2>(dev, p, drop, blocks, stream);
-  if (units <= 512) return launch_norm_bwd<kT, kS, 256, 2>(dev, p, drop, blocks, stream);
-  if (units <= 1024) return launch_norm_bwd<kT, kS, 512, 2>(dev, p, drop, blocks, stream);
   if (p.dS != nullptr || p.dX != nullptr) {
-    const int rc = launch_pdl(drop ? layer_norm_bwd_long_kernel<kT, kS, true>
-                                   : layer_norm_bwd_long_kernel<kT, kS, false>,
+    const int rc = launch_pdl(drop ? layer_norm_bwd_any_kernel<kT, kS, true>
+                                   : layer_norm_bwd_any_kernel<kT, kS, false>,
                               dim3(static_cast<unsigned>(p.M)), dim3(512), 0, stream, p);
     if (rc != IGC_OK) return rc;
   }
   if (p.partial == nullptr) return IGC_OK;
   const int64_t col_blocks = (static_cast<int64_t>(p.N) + 255) / 256;
   int64_t chunks = (dev.sm_count * 8 + col_blocks - 1) / col_blocks;
-  if (chunks > norm_bwd_max_blocks(p.N)) chunks = norm_bwd_max_blocks(p.N);
+  if (chunks > kMaxPartials) chunks = kMaxPartials;
   const int64_t rows = ((p.M + chunks - 1) / chunks + 7) / 8 * 8;
   chunks = (p.M + rows - 1) / rows;
   *blocks = static_cast<int>(chunks);

@@ -9,18 +9,16 @@ namespace igc {
 constexpr int kStreamStatic = 3072;  // bytes for the kernels' static shared memory
 
 // The ring for rows of N columns whose inputs have elements of sizes[i] bytes (0: absent), with
-// `groups` rings to a block: false where rows are too short or too long for one (at least two
-// slots).
+// `groups` rings to a block: false where rows are too long for one (at least two slots).
 inline bool plan_stream(const DeviceInfo& dev, int64_t N, const int (&sizes)[kStreamMats],
                         int groups, RowStream* s) {
-  if (N < 64) return false;
   uint32_t at = 0;
   for (int i = 0; i < kStreamMats; ++i) {
     s->at[i] = at;
     s->bytes[i] = static_cast<uint32_t>(N / 8 * 8 * sizes[i]);
     at += s->bytes[i];
   }
-  s->slot_bytes = (at + 127) / 128 * 128;
+  s->slot_bytes = at > 0 ? (at + 127) / 128 * 128 : 128;  // (no whole unit: nothing to copy)
   s->plane = static_cast<uint32_t>((N / 8 * 16 + 127) / 128 * 128);
   const size_t room = dev.smem_optin - kStreamStatic;
   if (2 * s->plane >= room) return false;
@@ -34,8 +32,8 @@ inline bool plan_stream(const DeviceInfo& dev, int64_t N, const int (&sizes)[kSt
 
 // least: bytes of dynamic shared memory that the kernel uses whatever the ring takes.
 template <typename P>
-int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int threads, int groups,
-                  size_t least, cudaStream_t stream, const P& p, const RowStream& s) {
+int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int blocks, int threads,
+                  int groups, size_t least, cudaStream_t stream, const P& p, const RowStream& s) {
   // (the attribute belongs to the function: set by every call, which costs less than to look
   // whether it is)
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -45,7 +43,7 @@ int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int threa
   }
   const size_t bytes = static_cast<size_t>(2) * s.plane +
                        static_cast<size_t>(groups) * s.slots * s.slot_bytes;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(dev.sm_count)), dim3(static_cast<unsigned>(threads)),
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(static_cast<unsigned>(threads)),
                     bytes < least ? least : bytes, stream, p, s);
 }
 
