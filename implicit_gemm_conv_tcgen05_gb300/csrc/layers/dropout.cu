@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
     unpack8<kX>(x[i], v);
     if (p.R != nullptr) unpack8<kY>(r[i], f);
     if constexpr (kDrop) {
-      drop8(p.drop, offset, row[i], n[i], v, f);
+      drop8(p.drop, drop_bits(p.drop, offset, row[i], n[i]), v, f);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += f[j];

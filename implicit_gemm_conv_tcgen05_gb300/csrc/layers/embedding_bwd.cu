@@ -8,7 +8,7 @@
 // Further blocks write the zeros of the rows that no token points to.
 //
 // Many: the positions are sorted by token first (stable, so that a token's positions stay in
-// order), by a cluster of eight blocks with a radix sort.  Blocks then walk chunks of 32 to 128
+// order), with a radix sort.  Blocks then walk chunks of 32 to 128
 // sorted positions and write each token's sum; the sums of a token that crosses a chunk's border go to
 // the workspace, and a last kernel adds them in order.  No atomics on sums.
 #include "layers_host.h"
@@ -21,17 +21,18 @@ constexpr int kThreads = 128;       // of a block over 1024 columns
 constexpr int kSmallUnits = 64, kSmallSubs = 4;  // few positions: 512 columns, four shares of rows
 constexpr int kSmallThreads = kSmallUnits * kSmallSubs;
 constexpr int kSmallM = 1024;       // positions up to which one launch does
-constexpr int kMinChunk = 32, kMaxChunk = 128;  // sorted positions of a block
+constexpr int kMinChunk = 32, kMaxChunk = 128;  // sorted positions of a chunk
+constexpr int kMaxSpan = 2048;                  // and of a block's chunks
 constexpr int kAhead = 8, kSmallAhead = 4;  // rows that a thread loads before it adds the first
 constexpr int kZeroRows = 64;       // of a block that writes zeros, at most
-constexpr int kCtas = 8;            // of the sorting cluster
-constexpr int kSortThreads = 1024, kSortWarps = kCtas * (kSortThreads / 32);
+constexpr int kSortThreads = 1024, kSortBlocks = 64;
 constexpr int kMaxDigit = 512;      // values of a digit of the radix sort
+constexpr int kBatch = 4;           // steps of 32 positions that a warp of the sort has at once
 
 struct EmbedParams {
   int M, D, vec, token64, accumulate;
   int slabs;                 // blocks to a row
-  int chunk;                 // sorted positions of a block
+  int chunk;                 // sorted positions that one thread adds
   int zero_rows;             // rows of a block that writes zeros, and those blocks
   unsigned zero_blocks;
   long long V;
@@ -42,8 +43,11 @@ struct EmbedParams {
   float scale;
   uint2* pairs[2];           // sorted: token (V: none of the table's) and position
   uint8_t* touched;          // 1 for each row of dW that a token points to
+  uint32_t* counts;          // [block of the sort][digit]
   float* partial;            // [chunk][2][D]: sums of a chunk's first and last token
   int digit_bits, passes;
+  int sort_steps;            // steps of 32 positions of a warp of the sort
+  int lanes_log2;            // threads that share a chunk's row in a block of the sums
 };
 
 __device__ __forceinline__ long long token_at(const EmbedParams& p, int i) {
@@ -51,19 +55,19 @@ __device__ __forceinline__ long long token_at(const EmbedParams& p, int i) {
                    : static_cast<const int*>(p.tokens)[i];
 }
 
-// Tokens first + k * step (k < kN) that lie before M, -1 for the others: all loaded before the
-// first is looked at.
+// Tokens of the positions first + k * step (k < kN) before end, -1 for the others: all loaded
+// before the first is looked at.
 template <int kN>
 __device__ __forceinline__ void tokens_at(const EmbedParams& p, long long first, int step,
-                                          long long (&v)[kN]) {
+                                          long long end, long long (&v)[kN]) {
   if (p.token64) {
     const long long* t = static_cast<const long long*>(p.tokens);
 #pragma unroll
-    for (int k = 0; k < kN; ++k) v[k] = first + k * step < p.M ? t[first + k * step] : -1;
+    for (int k = 0; k < kN; ++k) v[k] = first + k * step < end ? t[first + k * step] : -1;
   } else {
     const int* t = static_cast<const int*>(p.tokens);
 #pragma unroll
-    for (int k = 0; k < kN; ++k) v[k] = first + k * step < p.M ? t[first + k * step] : -1;
+    for (int k = 0; k < kN; ++k) v[k] = first + k * step < end ? t[first + k * step] : -1;
   }
 }
 
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(kSmallThreads, 4) embed_small_kernel(const Emb
     if (threadIdx.x < 2) bits[threadIdx.x] = 0;
     __syncthreads();
     long long v[kPer];
-    tokens_at<kPer>(p, threadIdx.x, kSmallThreads, v);
+    tokens_at<kPer>(p, threadIdx.x, kSmallThreads, p.M, v);
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (v[k] >= v0 && v[k] < v1) atomicOr(&bits[(v[k] - v0) / 32], 1u << ((v[k] - v0) % 32));
@@ -131,7 +135,7 @@ __global__ void __launch_bounds__(kSmallThreads, 4) embed_small_kernel(const Emb
   // bit j: position j holds the same token as position i
   const int words = (p.M + 31) / 32;
   long long held[kPer];
-  tokens_at<kPer>(p, threadIdx.x, kSmallThreads, held);
+  tokens_at<kPer>(p, threadIdx.x, kSmallThreads, p.M, held);
   const long long v = token_at(p, i);
   if (v < 0 || v >= p.V) return;
 #pragma unroll
@@ -193,153 +197,206 @@ __global__ void __launch_bounds__(kSmallThreads, 4) embed_small_kernel(const Emb
 // ---------------------------------------------------------------------------
 // many positions: the sort
 // ---------------------------------------------------------------------------
-// A pass of the radix sort: every warp counts the digits of its run of positions, the counts of
-// all warps become places, and every warp moves its run there.  A run is taken kBatch steps of
-// 32 positions at a time; one of a single batch (up to 65536 positions in all) keeps its keys
-// and their ranks in registers between the count and the move.
-constexpr int kBatch = 8;
+// One pass of the radix sort is two kernels of at most kSortBlocks blocks, each with a run of
+// positions (kSortThreads of them up to 65536 positions in all, a multiple of that beyond),
+// whose warps have runs of their own in it.  Every warp counts its digits; the first kernel
+// writes each block's counts, the second adds those of the smaller digits and of the blocks
+// before, and moves its run there.  (One cluster of eight blocks for all passes, with barriers
+// in place of launches, took 25 us for 32768 positions; this takes SORTUS.)
+struct SortRun {
+  uint32_t key[kBatch], pos[kBatch], at[kBatch];
+};
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kSortThreads)
-    embed_sort_kernel(const EmbedParams p) {
-  extern __shared__ uint32_t hist[];  // [32 warps][digits]: counts, then places
-  __shared__ uint32_t total[kMaxDigit], base[kMaxDigit], scan[32];
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int digits = 1 << p.digit_bits;
-  const uint32_t below = (1u << lane) - 1u;
-  const int run = ((p.M + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-  const long long first = static_cast<long long>(rank * (kSortThreads / 32) + warp) * run;
-  const int steps =
-      first < p.M
-          ? static_cast<int>((min(static_cast<long long>(run), p.M - first) + 31) / 32)
-          : 0;
-  const int batches = (run / 32 + kBatch - 1) / kBatch;
-  uint32_t* mine = hist + warp * digits;
-  if (p.touched != nullptr)  // (its place in the workspace is a multiple of 256 bytes)
-    for (long long k = static_cast<long long>(rank) * kSortThreads + threadIdx.x;
-         k < (p.V + 15) / 16; k += kCtas * kSortThreads)
-      reinterpret_cast<uint4*>(p.touched)[k] = make_uint4(0, 0, 0, 0);
-  for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = pass * p.digit_bits;
-    const uint2* in = p.pairs[(pass + p.passes) & 1];
-    uint2* out = p.pairs[(pass + p.passes + 1) & 1];
-    uint32_t key[kBatch], pos[kBatch], at[kBatch];
-    auto load = [&](int batch) {
-      const long long from = first + batch * (kBatch * 32) + lane;
-      if (pass == 0) {
-        long long v[kBatch];
-        tokens_at<kBatch>(p, from, 32, v);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          key[k] = static_cast<uint32_t>(v[k] >= 0 && v[k] < p.V ? v[k] : p.V);
-          pos[k] = static_cast<uint32_t>(from + k * 32);
-        }
-      } else {
-        uint2 v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          v[k] = from + k * 32 < p.M ? __ldcg(in + from + k * 32) : make_uint2(0, 0);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) key[k] = v[k].x, pos[k] = v[k].y;
-      }
-    };
-    auto digit_of = [&](uint32_t v) {
-      return (v >> shift) & static_cast<uint32_t>(digits - 1);
-    };
-    // at: the keys' places among those of their digit that mine counts from where it stands
-    auto rank_keys = [&](int batch) {
+struct Sorter {
+  const EmbedParams& p;
+  const int pass, warp, lane, digits, steps;
+  const long long first;
+  uint32_t* mine;  // the warp's counts of digits
+
+  __device__ __forceinline__ Sorter(const EmbedParams& q, int number, uint32_t* hist)
+      : p(q), pass(number), warp(threadIdx.x / 32), lane(threadIdx.x % 32),
+        digits(1 << q.digit_bits), steps(q.sort_steps),
+        first((static_cast<long long>(blockIdx.x) * (kSortThreads / 32) + threadIdx.x / 32) *
+              (q.sort_steps * 32)),
+        mine(hist + threadIdx.x / 32 * (1 << q.digit_bits)) {}
+
+  __device__ __forceinline__ uint32_t digit_of(uint32_t key) const {
+    return (key >> (pass * p.digit_bits)) & static_cast<uint32_t>(digits - 1);
+  }
+  // kBatch steps of 32 positions
+  __device__ __forceinline__ void load(SortRun& r, int batch) const {
+    const long long from = first + batch * (kBatch * 32) + lane;
+    const long long end = min(static_cast<long long>(p.M), first + steps * 32);
+    if (pass == 0) {
+      long long v[kBatch];
+      tokens_at<kBatch>(p, from, 32, end, v);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int step = batch * kBatch + k;
-        if (step >= steps) break;
-        const bool valid = first + step * 32 + lane < p.M;
-        // (a lane past the last position has a digit that no other has)
-        const uint32_t d = valid ? digit_of(key[k]) : 0xffffffffu;
-        const uint32_t peers = __match_any_sync(0xffffffffu, d);
-        if (valid) at[k] = mine[d] + __popc(peers & below);
-        __syncwarp();
-        if (valid && (peers & below) == 0) mine[d] += __popc(peers);
-        __syncwarp();
+        r.key[k] = static_cast<uint32_t>(v[k] >= 0 && v[k] < p.V ? v[k] : p.V);
+        r.pos[k] = static_cast<uint32_t>(from + k * 32);
       }
-    };
+    } else {
+      const uint2* in = p.pairs[(pass + p.passes) & 1];
+      uint2 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        v[k] = from + k * 32 < end ? in[from + k * 32] : make_uint2(0, 0);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) r.key[k] = v[k].x, r.pos[k] = v[k].y;
+    }
+  }
+  __device__ __forceinline__ bool holds(int batch, int k) const {
+    return batch * kBatch + k < steps && first + (batch * kBatch + k) * 32 + lane < p.M;
+  }
+  // at: the keys' places among those of their digit, counted in mine
+  __device__ __forceinline__ void rank(SortRun& r, int batch) const {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (batch * kBatch + k >= steps) break;
+      const bool valid = holds(batch, k);
+      // (a lane past the last position has a digit that no other has)
+      const uint32_t d = valid ? digit_of(r.key[k]) : 0xffffffffu;
+      const uint32_t peers = __match_any_sync(0xffffffffu, d);
+      const uint32_t ahead = __popc(peers & ((1u << lane) - 1u));
+      if (valid) r.at[k] = mine[d] + ahead;
+      __syncwarp();
+      if (valid && ahead == 0) mine[d] += __popc(peers);
+      __syncwarp();
+    }
+  }
+  // The rows of dW that a token points to: set by the positions whose neighbour holds another
+  // token.  (In the second pass, where most of a token's positions are neighbours: set by every
+  // position, the bytes of frequent tokens took 3 us of a training batch.  Warps that set the
+  // same byte set it to the same.)
+  __device__ __forceinline__ void mark(const SortRun& r, int batch) const {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const uint32_t other = __shfl_up_sync(0xffffffffu, r.key[k], 1);
+      if (holds(batch, k) && r.key[k] < p.V && (lane == 0 || other != r.key[k]))
+        p.touched[r.key[k]] = 1;
+    }
+  }
+  __device__ __forceinline__ void clear() const {
     for (int d = lane; d < digits; d += 32) mine[d] = 0;
     __syncwarp();
-    for (int batch = 0; batch < batches; ++batch) {
-      load(batch);
-      rank_keys(batch);
+  }
+  __device__ __forceinline__ int batches() const { return (steps + kBatch - 1) / kBatch; }
+};
+
+__global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const EmbedParams p, int pass) {
+  extern __shared__ uint32_t hist[];  // [32 warps][digits]
+  const Sorter s(p, pass, hist);
+  s.clear();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (pass == 0 && p.touched != nullptr)  // (its place in the workspace is a multiple of 256)
+    for (long long k = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x;
+         k < (p.V + 15) / 16; k += static_cast<long long>(gridDim.x) * kSortThreads)
+      reinterpret_cast<uint4*>(p.touched)[k] = make_uint4(0, 0, 0, 0);
+  SortRun r;
+  for (int batch = 0; batch < s.batches(); ++batch) {
+    s.load(r, batch);
+    s.rank(r, batch);
+    if (pass == 1 && p.touched != nullptr) s.mark(r, batch);
+  }
+  __syncthreads();
+  const int d = static_cast<int>(threadIdx.x);
+  if (d < s.digits) {
+    uint32_t sum = 0;
+#pragma unroll 16
+    for (int w = 0; w < kSortThreads / 32; ++w) sum += hist[w * s.digits + d];
+    p.counts[blockIdx.x * s.digits + d] = sum;
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_move_kernel(const EmbedParams p, int pass) {
+  extern __shared__ uint32_t hist[];  // [32 warps][digits]: counts, then places
+  __shared__ uint32_t part[2][kMaxDigit], scan[32];
+  const Sorter s(p, pass, hist);
+  s.clear();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  SortRun r;
+  s.load(r, 0);
+  // two threads to a digit, half of the blocks each: all blocks' counts, and those before this
+  const int d = static_cast<int>(threadIdx.x) % kMaxDigit, half = threadIdx.x / kMaxDigit;
+  const int rank = static_cast<int>(blockIdx.x), blocks = static_cast<int>(gridDim.x);
+  uint32_t all = 0, before = 0;
+  if (d < s.digits) {
+#pragma unroll 16
+    for (int c = half; c < blocks; c += 2) {
+      const uint32_t v = p.counts[c * s.digits + d];
+      all += v;
+      if (c < rank) before += v;
     }
-    __syncthreads();
-    // the warps' counts become places within the block's share of a digit
-    const int d = static_cast<int>(threadIdx.x);
-    if (d < digits) {
-      uint32_t sum = 0;
-#pragma unroll 8
-      for (int w = 0; w < kSortThreads / 32; ++w) {
-        const uint32_t c = hist[w * digits + d];
-        hist[w * digits + d] = sum;
-        sum += c;
-      }
-      total[d] = sum;
+  }
+  if (half == 1) {
+    part[0][d] = all;
+    part[1][d] = before;
+  }
+  const bool kept = s.batches() == 1;
+  s.rank(r, 0);
+  if (!kept) {
+    for (int batch = 1; batch < s.batches(); ++batch) {
+      s.load(r, batch);
+      s.rank(r, batch);
     }
-    cluster_sync();
-    // smaller digits of all blocks, then the same digit of the blocks before this one
-    uint32_t all = 0, before = 0;
-    if (d < digits) {
+  }
+  __syncthreads();
+  if (half == 0) all += part[0][d], before += part[1][d];
+  // the smaller digits' counts
+  uint32_t upto = half == 0 ? all : 0;
 #pragma unroll
-      for (int c = 0; c < kCtas; ++c) {
-        const uint32_t v =
-            ld_shared_cluster_u32(mapa_shared(smem_u32(total + d), static_cast<uint32_t>(c)));
-        all += v;
-        if (c < rank) before += v;
-      }
-    }
-    uint32_t upto = all;
+  for (int o = 1; o < 32; o *= 2) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (s.lane >= o) upto += v;
+  }
+  if (s.lane == 31) scan[s.warp] = upto;
+  __syncthreads();
+  uint32_t ahead = s.lane < s.warp ? scan[s.lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
+  for (int o = 16; o > 0; o /= 2) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+  // the warps' counts become places
+  if (half == 0 && d < s.digits) {
+    uint32_t place = ahead + upto - all + before;
+#pragma unroll 16
+    for (int w = 0; w < kSortThreads / 32; ++w) {
+      const uint32_t c = hist[w * s.digits + d];
+      hist[w * s.digits + d] = place;
+      place += c;
     }
-    if (lane == 31) scan[warp] = upto;
-    __syncthreads();
-    uint32_t ahead = lane < warp ? scan[lane] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
-    if (d < digits) base[d] = ahead + upto - all + before;
-    __syncthreads();
-    for (int batch = 0; batch < batches; ++batch) {
-      const bool kept = batches == 1;
-      if (!kept) {
-        load(batch);
-        rank_keys(batch);  // (from the places on now)
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int step = batch * kBatch + k;
-        if (step >= steps || first + step * 32 + lane >= p.M) continue;
-        const uint32_t dg = digit_of(key[k]);
-        const uint32_t to = base[dg] + at[k] + (kept ? mine[dg] : 0u);
-        out[to] = make_uint2(key[k], pos[k]);
-        // (a byte that several positions set is set to the same)
-        if (pass == 0 && p.touched != nullptr && key[k] < p.V) p.touched[key[k]] = 1;
-      }
+  }
+  __syncthreads();
+  uint2* out = p.pairs[(pass + p.passes + 1) & 1];
+  for (int batch = 0; batch < s.batches(); ++batch) {
+    if (!kept) {
+      s.load(r, batch);
+      s.rank(r, batch);  // (from the places on now)
     }
-    cluster_sync();  // what the next pass, and a block's reads of the others' totals, rely on
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (!s.holds(batch, k)) continue;
+      const uint32_t to = r.at[k] + (kept ? s.mine[s.digit_of(r.key[k])] : 0u);
+      out[to] = make_uint2(r.key[k], r.pos[k]);
+    }
+    if (p.passes == 1 && p.touched != nullptr) s.mark(r, batch);
   }
 }
 
 // ---------------------------------------------------------------------------
 // many positions: the sums
 // ---------------------------------------------------------------------------
+// A block has kThreads units of eight columns: of one chunk's rows or, where rows are narrow, of
+// several chunks'.
 template <int kY, int kW>
 __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams p) {
-  __shared__ uint32_t keys[kMaxChunk + 2], pos[kMaxChunk];
+  __shared__ uint32_t keys[kMaxSpan + 2], pos[kMaxSpan];
   grid_dependency_wait();
   grid_dependents_launch();
   const bool vec = p.vec != 0;
   const int chunks = (p.M + p.chunk - 1) / p.chunk;
-  const unsigned sum_blocks = static_cast<unsigned>(chunks) * p.slabs;
+  const int subs = kThreads >> p.lanes_log2;  // chunks of a block
+  const unsigned sum_blocks = static_cast<unsigned>((chunks + subs - 1) / subs) * p.slabs;
   if (blockIdx.x >= sum_blocks) {
     const long long v0 = static_cast<long long>(blockIdx.x - sum_blocks) * p.zero_rows;
     const long long v1 = min(p.V, v0 + p.zero_rows);
@@ -350,37 +407,42 @@ __global__ void __launch_bounds__(kThreads) embed_sums_kernel(const EmbedParams 
       if (keys[v - v0] == 0) zero_row<kW, kThreads>(p, v, vec);
     return;
   }
-  const int c = static_cast<int>(blockIdx.x / p.slabs);
-  const long long p0 = static_cast<long long>(c) * p.chunk;
+  const int sub = static_cast<int>(threadIdx.x) >> p.lanes_log2;
+  const int lane = static_cast<int>(threadIdx.x) & ((1 << p.lanes_log2) - 1);
+  const int c0 = static_cast<int>(blockIdx.x / p.slabs) * subs;
+  const long long p0 = static_cast<long long>(c0) * p.chunk;
   const uint32_t none = static_cast<uint32_t>(p.V);
-  // keys[k + 1]: token of the chunk's position k; a token that is not in the table before the
+  // keys[k + 1]: token of the block's position k; a token that is not in the table before the
   // first position, after the last, and for what is not to be summed
-  for (int k = threadIdx.x; k < p.chunk + 2; k += kThreads) {
+  for (int k = threadIdx.x; k < subs * p.chunk + 2; k += kThreads) {
     const long long at = p0 + k - 1;
     const uint2 v = at >= 0 && at < p.M ? p.pairs[0][at] : make_uint2(none, 0);
     keys[k] = v.x;
-    if (k > 0 && k <= p.chunk) pos[k - 1] = v.y;
+    if (k > 0 && k <= subs * p.chunk) pos[k - 1] = v.y;
   }
   __syncthreads();
-  const int n = (static_cast<int>(blockIdx.x % p.slabs) * kThreads + static_cast<int>(threadIdx.x)) * 8;
+  const int n = (static_cast<int>(blockIdx.x % p.slabs) * kThreads + lane) * 8;
   if (n >= p.D) return;
+  const uint32_t* key = keys + sub * p.chunk;
+  const uint32_t* at = pos + sub * p.chunk;
   float acc[8] = {};
-  bool from_start = keys[0] == keys[1];  // the token at hand began in an earlier chunk
+  bool from_start = key[0] == key[1];  // the token at hand began in an earlier chunk
   for (int k0 = 0; k0 < p.chunk; k0 += kAhead) {
     Raw8<kY> y[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (keys[k0 + k + 1] != none)
-        y[k] = load8<kY>(row_at<kY>(p.dY, pos[k0 + k], p.lddy), n, p.D, vec);
+      if (key[k0 + k + 1] != none)
+        y[k] = load8<kY>(row_at<kY>(p.dY, at[k0 + k], p.lddy), n, p.D, vec);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const uint32_t v = keys[k0 + k + 1];
+      const uint32_t v = key[k0 + k + 1];
       if (v == none) return;  // the rest holds no tokens of the table
       add8<kY>(y[k], acc);
-      const bool last = k0 + k == p.chunk - 1, goes_on = keys[k0 + k + 2] == v;
+      const bool last = k0 + k == p.chunk - 1, goes_on = key[k0 + k + 2] == v;
       if (goes_on && !last) continue;
       if (from_start || goes_on) {
-        float* out = p.partial + (static_cast<long long>(c) * 2 + (from_start ? 0 : 1)) * p.D;
+        float* out =
+            p.partial + (static_cast<long long>(c0 + sub) * 2 + (from_start ? 0 : 1)) * p.D;
         store8<IGC_F32>(reinterpret_cast<char*>(out), n, p.D,
                         (reinterpret_cast<uintptr_t>(out) & 15u) == 0, acc);
       } else {
@@ -474,16 +536,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-// Fewer borders for tokens to cross where there are many positions, more blocks where few.
-inline int64_t chunk_of(int64_t M) {
+// Fewer borders for tokens to cross where there is work for every SM without them.
+inline int64_t chunk_of(int64_t M, int64_t D) {
+  const int64_t units = (D + 7) / 8;
   int64_t chunk = kMinChunk;
-  while (chunk < kMaxChunk && M > chunk * 256) chunk *= 2;
+  while (chunk < kMaxChunk && M > 128 * 1024 / units * chunk) chunk *= 2;
   return chunk;
+}
+inline int64_t chunks_of(int64_t M, int64_t D) {
+  const int64_t chunk = chunk_of(M, D);
+  return (M + chunk - 1) / chunk;
+}
+// Steps of 32 positions of a warp of the sort.
+inline int64_t sort_steps(int64_t M) {
+  const int64_t most = static_cast<int64_t>(kSortThreads) * kSortBlocks;
+  return (M + most - 1) / most;
 }
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct EmbedLayout {
-  size_t pairs[2], touched, partial, bytes;
+  size_t pairs[2], touched, counts, partial, bytes;
 };
 EmbedLayout layout(int64_t M, int64_t V, int64_t D) {
   EmbedLayout l = {};
@@ -496,7 +568,8 @@ EmbedLayout layout(int64_t M, int64_t V, int64_t D) {
   if (M > kSmallM && V > 0 && D > 0) {
     for (int i = 0; i < 2; ++i) l.pairs[i] = take(static_cast<size_t>(M) * sizeof(uint2));
     l.touched = take(static_cast<size_t>(V));
-    l.partial = take(static_cast<size_t>((M + chunk_of(M) - 1) / chunk_of(M)) * 2 * static_cast<size_t>(D) * 4);
+    l.counts = take(static_cast<size_t>(kSortBlocks) * kMaxDigit * 4);
+    l.partial = take(static_cast<size_t>(chunks_of(M, D)) * 2 * static_cast<size_t>(D) * 4);
   }
   l.bytes = at;
   return l;
@@ -513,19 +586,29 @@ int run(EmbedParams p, cudaStream_t stream) {
     return launch_pdl(embed_small_kernel<kY, kW>, dim3(static_cast<unsigned>(blocks)),
                       dim3(kSmallThreads), 0, stream, p);
   }
-  const int chunks = (p.M + p.chunk - 1) / p.chunk;
-  const long long blocks = static_cast<long long>(chunks) * p.slabs + zero_blocks;
+  const int chunks = (p.M + p.chunk - 1) / p.chunk, subs = kThreads >> p.lanes_log2;
+  const long long blocks =
+      static_cast<long long>((chunks + subs - 1) / subs) * p.slabs + zero_blocks;
   const long long join_cols = (static_cast<long long>(p.D) + 255) / 256;
   if (blocks > 0x7fffffff || join_cols > 65535) return IGC_ERR_UNSUPPORTED;
   const int smem = (kSortThreads / 32) * (1 << p.digit_bits) * 4;
-  if (cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (kSortThreads / 32) * kMaxDigit * 4) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return IGC_ERR_CUDA;
+  for (auto kernel : {embed_count_kernel, embed_move_kernel}) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (kSortThreads / 32) * kMaxDigit * 4) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return IGC_ERR_CUDA;
+    }
   }
-  int rc = launch_pdl(embed_sort_kernel, dim3(kCtas), dim3(kSortThreads),
-                      static_cast<size_t>(smem), stream, p);
-  if (rc != IGC_OK) return rc;
+  const int run = kSortThreads * p.sort_steps;
+  const dim3 sort_grid(static_cast<unsigned>((p.M + static_cast<long long>(run) - 1) / run));
+  int rc = IGC_OK;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    for (auto kernel : {embed_count_kernel, embed_move_kernel}) {
+      rc = launch_pdl(kernel, sort_grid, dim3(kSortThreads), static_cast<size_t>(smem), stream, p,
+                      pass);
+      if (rc != IGC_OK) return rc;
+    }
+  }
   rc = launch_pdl(embed_sums_kernel<kY, kW>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
                   0, stream, p);
   if (rc != IGC_OK) return rc;
@@ -577,7 +660,11 @@ int embedding_backward(int64_t M, int64_t V, int64_t D, const void* tokens, int 
   p.accumulate = accumulate != 0;
   const int64_t slab = (M <= kSmallM ? kSmallUnits : kThreads) * 8;
   p.slabs = static_cast<int>((D + slab - 1) / slab);
-  p.chunk = static_cast<int>(chunk_of(M));
+  p.chunk = static_cast<int>(chunk_of(M, D));
+  // chunks of narrow rows share a block
+  p.lanes_log2 = 3;
+  while ((1 << p.lanes_log2) < kThreads && (8 << p.lanes_log2) < D) ++p.lanes_log2;
+  p.sort_steps = static_cast<int>(sort_steps(M));
   // about 64 KB of zeros to a block
   const int64_t rows = 65536 / (D * static_cast<int64_t>(elem_size(dw_dtype)));
   p.zero_rows = static_cast<int>(rows < 1 ? 1 : (rows > kZeroRows ? kZeroRows : rows));
@@ -587,6 +674,7 @@ int embedding_backward(int64_t M, int64_t V, int64_t D, const void* tokens, int 
   char* ws = static_cast<char*>(workspace);
   for (int i = 0; i < 2; ++i) p.pairs[i] = reinterpret_cast<uint2*>(ws + l.pairs[i]);
   p.touched = accumulate ? nullptr : reinterpret_cast<uint8_t*>(ws + l.touched);
+  p.counts = reinterpret_cast<uint32_t*>(ws + l.counts);
   p.partial = reinterpret_cast<float*>(ws + l.partial);
   int bits = 1;
   while ((static_cast<int64_t>(1) << bits) <= V) ++bits;  // keys are 0 .. V

@@ -38,7 +38,7 @@ __device__ __forceinline__ void join8(const NormParams& p, uint64_t offset, long
   unpack8<kT>(x, s);
   if (p.R != nullptr) unpack8<kS>(r, f);
   if constexpr (kDrop) {
-    drop8(p.drop, offset, row, n, s, f);
+    drop8(p.drop, drop_bits(p.drop, offset, row, n), s, f);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -134,27 +134,35 @@ __global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(const NormPara
   }
 }
 
-// Blocks of an SM: 768 threads of 80 registers (16384 x 4096 bf16 with dropout and residual: 86 us;
-// 640 threads 92, 512 threads 92).
-constexpr int norm_blocks(int lanes) { return lanes <= 128 ? 6 : (lanes <= 256 ? 3 : 1); }
+// Rows that start on 16-byte boundaries, one to a group of kLanes threads, kUnits units to a
+// thread, all loaded before the first is used.  A block to a row from 64 threads on: rows that
+// share a block wait for one another (32768 x 1536 bf16 with dropout and residual: 65 us, two
+// rows to a block 86).  Four units where rows are long, on 768 threads of 80 registers an SM
+// (16384 x 4096: 87 us; on 640 threads of more registers 94; two units to twice the threads 96),
+// three where that leaves fewer threads without, on 1024 (8192 x 6000: 72 us, on 768 80).
+template <int kLanes, int kUnits>
+struct NormRows {
+  static constexpr int kBlock = kLanes < 64 ? 128 : kLanes, kGroups = kBlock / kLanes,
+                       kPerSm = kBlock > 256 ? 2 : (kUnits == 2 || kUnits == 3 ? 1024 : 768) / kBlock;
+};
 
-// Rows that start on 16-byte boundaries, one to a group of kLanes threads, four units to a
-// thread, all loaded before the first is used.
-template <int kT, int kS, int kLanes, bool kDrop>
-__global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes, norm_blocks(kLanes))
+template <int kT, int kS, int kLanes, int kUnits, bool kDrop>
+__global__ void __launch_bounds__(NormRows<kLanes, kUnits>::kBlock, NormRows<kLanes, kUnits>::kPerSm)
     layer_norm_rows_kernel(const NormParams p) {
-  constexpr int kGroups = kLanes < 128 ? 128 / kLanes : 1, kUnits = 4;
+  constexpr int kGroups = NormRows<kLanes, kUnits>::kGroups;
   constexpr int kSizeT = kT == IGC_F32 ? 4 : 2, kSizeS = kS == IGC_F32 ? 4 : 2;
-  __shared__ __align__(16) float red[kGroups][2][(kLanes / 32 + 3) / 4 * 4];
+  __shared__ __align__(16) float red[kGroups][2][(kLanes + 127) / 128 * 4];
   const int t = threadIdx.x % kLanes, group = threadIdx.x / kLanes, N8 = p.N / 8 * 8;
   const long long row = static_cast<long long>(blockIdx.x) * kGroups + group;
   grid_dependency_wait();
   grid_dependents_launch();
-  if (kGroups > 1 && row >= p.M) return;
+  // (rows of less than a warp: the warp stays together for its shuffles)
+  if (kLanes >= 32 && kGroups > 1 && row >= p.M) return;
+  const bool there = kLanes >= 32 || row < p.M;
   const bool has_x = p.X != nullptr, has_r = p.R != nullptr, has_s = p.S != nullptr;
   const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
   const float inv = 1.0f / static_cast<float>(p.N);
-  const int last = N8 + t < p.N ? N8 + t : -1;
+  const int last = there && N8 + t < p.N ? N8 + t : -1;
   const char* x_row = row_at<kT>(p.X, row, p.ldx);
   const char* r_row = row_at<kS>(p.R, row, p.ldr);
   char* s_row = row_at<kS>(p.S, row, p.lds);
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes, norm_blocks(kLane
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int n = (i * kLanes + t) * 8;
-      if (!decltype(whole)::value && n >= N8) continue;
+      if (!decltype(whole)::value && (n >= N8 || !there)) continue;
       if (has_x) x[i] = load8<kT>(x_row, n, n + 8, true);
       if (has_r) r[i] = load8<kS>(r_row, n, n + 8, true);
     }
@@ -174,12 +182,12 @@ __global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes, norm_blocks(kLane
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int n = (i * kLanes + t) * 8;
-      if (!decltype(whole)::value && n >= N8) continue;
+      if (!decltype(whole)::value && (n >= N8 || !there)) continue;
       float f[8] = {};
       if (has_r) unpack8<kS>(r[i], f);
       if constexpr (kDrop) {
         unpack8<kT>(x[i], s[i]);
-        drop8(p.drop, offset, row, n, s[i], f);
+        drop8(p.drop, drop_bits(p.drop, offset, row, n), s[i], f);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[i][j] = f[j];
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes, norm_blocks(kLane
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int n = (i * kLanes + t) * 8;
-      if (!decltype(whole)::value && n >= N8) continue;
+      if (!decltype(whole)::value && (n >= N8 || !there)) continue;
       if (has_s) store_unit<kS>(s_row + n * kSizeS, s[i]);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes, norm_blocks(kLane
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int n = (i * kLanes + t) * 8;
-      if (!decltype(whole)::value && n >= N8) continue;
+      if (!decltype(whole)::value && (n >= N8 || !there)) continue;
       float wv[8], bv[8];
       load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, wv);
       load_vec8<kT>(p.b, n, p.N, p.w_f32, 0.0f, bv);
@@ -243,35 +251,46 @@ __global__ void __launch_bounds__(kLanes < 128 ? 128 : kLanes, norm_blocks(kLane
       if (p.b != nullptr) bv = load_vec(p.b, last, p.w_f32, kT == IGC_BF16);
       store1<kT>(y_row, last, fmaf(s_last * rstd, wv, bv));
     }
-    if (t == 0) {
+    if (t == 0 && there) {
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
   };
-  if (__all_sync(0xffffffffu, ((kUnits - 1) * kLanes + t) * 8 < N8))
+  if (__all_sync(0xffffffffu, there && ((kUnits - 1) * kLanes + t) * 8 < N8))
     one_row(std::true_type{});
   else
     one_row(std::false_type{});
 }
 
-template <int kT, int kS, int kLanes>
+template <int kT, int kS, int kLanes, int kUnits>
 int launch_rows(const NormParams& p, bool drop, cudaStream_t stream) {
-  constexpr int kGroups = kLanes < 128 ? 128 / kLanes : 1;
-  const long long blocks = (static_cast<long long>(p.M) + kGroups - 1) / kGroups;
-  return launch_pdl(drop ? layer_norm_rows_kernel<kT, kS, kLanes, true>
-                         : layer_norm_rows_kernel<kT, kS, kLanes, false>,
-                    dim3(static_cast<unsigned>(blocks)), dim3(kLanes * kGroups), 0, stream, p);
+  using Rows = NormRows<kLanes, kUnits>;
+  const long long blocks = (static_cast<long long>(p.M) + Rows::kGroups - 1) / Rows::kGroups;
+  return launch_pdl(drop ? layer_norm_rows_kernel<kT, kS, kLanes, kUnits, true>
+                         : layer_norm_rows_kernel<kT, kS, kLanes, kUnits, false>,
+                    dim3(static_cast<unsigned>(blocks)), dim3(Rows::kBlock), 0, stream, p);
+}
+
+// Three or four units to a thread, whichever leaves fewer of them without.
+template <int kT, int kS, int kLanes>
+int launch_long_rows(const NormParams& p, bool drop, cudaStream_t stream) {
+  return p.N <= kLanes * 24 ? launch_rows<kT, kS, kLanes, 3>(p, drop, stream)
+                            : launch_rows<kT, kS, kLanes, 4>(p, drop, stream);
 }
 
 template <int kT, int kS>
 int run_norm(const NormParams& p, bool drop, cudaStream_t stream) {
   const long long units = (static_cast<long long>(p.N) + 7) / 8;
   if (p.vec) {
-    if (units <= 128) return launch_rows<kT, kS, 32>(p, drop, stream);
-    if (units <= 256) return launch_rows<kT, kS, 64>(p, drop, stream);
-    if (units <= 512) return launch_rows<kT, kS, 128>(p, drop, stream);
-    if (units <= 1024) return launch_rows<kT, kS, 256>(p, drop, stream);
-    if (units <= 2048) return launch_rows<kT, kS, 512>(p, drop, stream);
+    if (units <= 8) return launch_rows<kT, kS, 8, 1>(p, drop, stream);
+    if (units <= 16) return launch_rows<kT, kS, 16, 1>(p, drop, stream);
+    if (units <= 32) return launch_rows<kT, kS, 32, 1>(p, drop, stream);
+    if (units <= 64) return launch_rows<kT, kS, 32, 2>(p, drop, stream);
+    if (units <= 128) return launch_long_rows<kT, kS, 32>(p, drop, stream);
+    if (units <= 256) return launch_long_rows<kT, kS, 64>(p, drop, stream);
+    if (units <= 512) return launch_long_rows<kT, kS, 128>(p, drop, stream);
+    if (units <= 1024) return launch_long_rows<kT, kS, 256>(p, drop, stream);
+    if (units <= 2048) return launch_long_rows<kT, kS, 512>(p, drop, stream);
   }
   const dim3 grid(static_cast<unsigned>(p.M));
   if (units <= 512)

@@ -49,7 +49,7 @@ __device__ __forceinline__ void grads8(const NormBwdParams& p, uint64_t offset, 
   }
   if (p.dS != nullptr) store8<kS>(ds_row, n, p.N, vec, d);
   if (p.dX != nullptr) {
-    if constexpr (kDrop) drop8(p.drop, offset, row, n, d);
+    if constexpr (kDrop) drop8(p.drop, drop_bits(p.drop, offset, row, n), d);
     store8<kT>(dx_row, n, p.N, vec, d);
   }
 }
@@ -94,8 +94,6 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   grid_dependency_wait();
   grid_dependents_launch();
   const int t = walk.t, N8 = p.N / 8 * 8;
-  keep_weights<kT>(ring, st.plane, p.w, N8, p.w_f32);
-  __syncthreads();
   const bool has_a = p.A != nullptr, has_s = p.dS != nullptr, has_x = p.dX != nullptr;
   auto fill = [&](int k) {
     const long long row = walk.first + k * walk.step;
@@ -110,6 +108,8 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   constexpr int kBehind = kLanes == 32 ? 0 : 1;
   if (t == 0)
     for (int k = 0; k < walk.count && k < st.slots - kBehind; ++k) fill(k);
+  keep_weights<kT>(ring, st.plane, p.w, N8, p.w_f32);
+  __syncthreads();
   const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
   const float inv = 1.0f / static_cast<float>(p.N);
   float sw[kUnits][8] = {}, sb[kUnits][8] = {}, sw_last = 0.0f, sb_last = 0.0f;
@@ -171,7 +171,20 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
         c2 = fmaf(g_last, h_last, c2);
         if (k + 1 < walk.count) load_last(row + walk.step);
       }
-      row_sums<kLanes>(c1, c2, red[walk.group][k & 1], walk.group);
+      // the bits of the dropout are made here, among the shuffles of the sums
+      uint4 bits[kDrop ? kUnits : 1];
+      if constexpr (kDrop) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+          bits[i] = drop_bits(p.drop, offset, row, (i * kLanes + t) * 8);
+      }
+      if constexpr (kLanes == 32) {
+        lane_sums<32>(c1, c2);
+      } else {
+        leave_sums<kLanes>(c1, c2, red[walk.group][k & 1]);
+        group_sync<kLanes>(walk.group);
+        take_sums<kLanes>(c1, c2, red[walk.group][k & 1]);
+      }
       if (kBehind && t == 0 && stopped < 0 && k + st.slots - 1 < walk.count)
         fill(k + st.slots - 1);
       c1 *= inv;
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
         }
         if (has_s) store_unit<kS>(ds_row + n * kSizeS, d);
         if (has_x) {
-          if constexpr (kDrop) drop8(p.drop, offset, row, n, d);
+          if constexpr (kDrop) drop8(p.drop, bits[i], d);
           store_unit<kT>(dx_row + n * kSizeT, d);
         }
       }
@@ -271,7 +284,9 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_any_kernel(const NormBwdPa
   for (long long n = threadIdx.x * 8; n < p.N; n += 512 * 8) terms(static_cast<int>(n));
   float c1 = sum2(p1), c2 = sum2(p2);
   const float inv = 1.0f / static_cast<float>(p.N);
-  row_sums<512>(c1, c2, red);
+  leave_sums<512>(c1, c2, red);
+  __syncthreads();
+  take_sums<512>(c1, c2, red);
   c1 *= inv;
   c2 *= inv;
   for (long long m = threadIdx.x * 8; m < p.N; m += 512 * 8) {
@@ -330,6 +345,85 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const NormBwdPa
   }
 }
 
+// Narrow rows: kLanes threads to a row, a unit to a thread, several rows at a time so that their
+// loads and sums overlap (as many as 128 registers hold).  Rows of any alignment.
+constexpr int kNarrowThreads = 512;
+
+template <int kT, int kS, int kLanes, bool kDrop>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
+    layer_norm_bwd_narrow_kernel(const NormBwdParams p) {
+  constexpr int kGroups = kNarrowThreads / kLanes, kNarrowRows = kS == IGC_F32 ? 2 : 4;
+  __shared__ float tot[2][kGroups][kLanes * 8];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int t = threadIdx.x % kLanes, group = threadIdx.x / kLanes, n = t * 8;
+  const bool vec = p.vec != 0;
+  const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
+  const float inv = 1.0f / static_cast<float>(p.N);
+  float w[8], sw[8] = {}, sb[8] = {};
+  load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, w);
+  const long long step = static_cast<long long>(gridDim.x) * kGroups;
+  // (all groups of a warp go as often as the one with most rows)
+  for (long long base = static_cast<long long>(blockIdx.x) * kGroups +
+                        group / (32 / kLanes) * (32 / kLanes);
+       base < p.M; base += step * kNarrowRows) {
+    Raw8<kT> y[kNarrowRows];
+    Raw8<kS> s[kNarrowRows], a[kNarrowRows];
+    float mean[kNarrowRows], rstd[kNarrowRows];
+#pragma unroll
+    for (int r = 0; r < kNarrowRows; ++r) {
+      const long long row = base + r * step + group % (32 / kLanes);
+      y[r] = {}, s[r] = {}, a[r] = {};
+      mean[r] = rstd[r] = 0.0f;
+      if (row >= p.M || n >= p.N) continue;
+      y[r] = load8<kT>(row_at<kT>(p.dY, row, p.lddy), n, p.N, vec);
+      s[r] = load8<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec);
+      if (p.A != nullptr) a[r] = load8<kS>(row_at<kS>(p.A, row, p.lda), n, p.N, vec);
+      mean[r] = p.mean[row], rstd[r] = p.rstd[row];
+    }
+#pragma unroll
+    for (int r = 0; r < kNarrowRows; ++r) {
+      const long long row = base + r * step + group % (32 / kLanes);
+      float g[8], h[8];
+      uint64_t p1 = 0, p2 = 0;
+      unpack8<kT>(y[r], g);
+      unpack8<kS>(s[r], h);
+      terms8<true>(mean[r], rstd[r], w, g, h, p1, p2, sw, sb);
+      float c1 = sum2(p1), c2 = sum2(p2);
+      lane_sums<kLanes>(c1, c2);
+      if (row < p.M && n < p.N)
+        grads8<kT, kS, kDrop>(p, offset, row, row_at<kS>(p.dS, row, p.ldds),
+                              row_at<kT>(p.dX, row, p.lddx), n, vec, rstd[r], c1 * inv, c2 * inv,
+                              a[r], g, h);
+    }
+  }
+  if (p.partial == nullptr) return;
+  // one row of sums per block: the groups' are added in order
+#pragma unroll
+  for (int j = 0; j < 8; ++j) tot[0][group][n + j] = sw[j], tot[1][group][n + j] = sb[j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * kLanes * 8; c += kNarrowThreads) {
+    const int v = c / (kLanes * 8), col = c % (kLanes * 8);
+    if (col >= p.N) continue;
+    float sum = 0.0f;
+#pragma unroll 16
+    for (int r = 0; r < kGroups; ++r) sum += tot[v][r][col];
+    p.partial[(static_cast<long long>(v) * gridDim.x + blockIdx.x) * p.N + col] = sum;
+  }
+}
+
+template <int kT, int kS, int kLanes>
+int launch_narrow(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
+                  cudaStream_t stream) {
+  const int64_t rows = kNarrowThreads / kLanes;
+  const int64_t all = (static_cast<int64_t>(p.M) + rows - 1) / rows;
+  const int64_t most = dev.sm_count < kMaxPartials ? dev.sm_count : kMaxPartials;
+  *blocks = static_cast<int>(all < most ? all : most);
+  return launch_pdl(drop ? layer_norm_bwd_narrow_kernel<kT, kS, kLanes, true>
+                         : layer_norm_bwd_narrow_kernel<kT, kS, kLanes, false>,
+                    dim3(static_cast<unsigned>(*blocks)), dim3(kNarrowThreads), 0, stream, p);
+}
+
 // *done: whether a block's shared memory holds two rows of every group.
 template <int kT, int kS, int kLanes>
 int stream_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
@@ -354,6 +448,9 @@ template <int kT, int kS>
 int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
                  cudaStream_t stream) {
   const long long units = (static_cast<long long>(p.N) + 7) / 8;
+  if (units <= 8) return launch_narrow<kT, kS, 8>(dev, p, drop, blocks, stream);
+  if (units <= 16) return launch_narrow<kT, kS, 16>(dev, p, drop, blocks, stream);
+  if (units <= 32) return launch_narrow<kT, kS, 32>(dev, p, drop, blocks, stream);
   bool done = false;
   int rc = IGC_OK;
   if (!p.vec)

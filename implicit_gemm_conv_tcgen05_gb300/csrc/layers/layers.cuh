@@ -208,16 +208,19 @@ __device__ __forceinline__ uint4 philox(const Drop& d, uint4 c) {
   return c;
 }
 
-// v: eight elements of row `row` from column n (a multiple of 8) on; each becomes v * scale + r
-// if it is kept, else r.  One block of Philox for all eight, 16 bits each: 5 instructions an
-// element beside the 10 that 32 bits each would take, and p to 2^-17 is finer than a rate is
-// ever set.  What is dropped is selected away, not multiplied by 0: an infinity there leaves
-// nothing.
-__device__ __forceinline__ void drop8(const Drop& d, uint64_t offset, long long row, int n,
-                                      float (&v)[8], const float (&r)[8]) {
-  const uint4 q = philox(d, make_uint4(static_cast<uint32_t>(n) / 8u, static_cast<uint32_t>(row),
-                                       static_cast<uint32_t>(offset),
-                                       static_cast<uint32_t>(offset >> 32)));
+// The random bits of eight elements of row `row` from column n (a multiple of 8) on.  One block
+// of Philox for all eight, 16 bits each: 5 instructions an element beside the 10 that 32 bits
+// each would take, and p to 2^-17 is finer than a rate is ever set.
+__device__ __forceinline__ uint4 drop_bits(const Drop& d, uint64_t offset, long long row, int n) {
+  return philox(d, make_uint4(static_cast<uint32_t>(n) / 8u, static_cast<uint32_t>(row),
+                              static_cast<uint32_t>(offset),
+                              static_cast<uint32_t>(offset >> 32)));
+}
+
+// v: eight elements; each becomes v * scale + r if its bits keep it, else r.  What is dropped is
+// selected away, not multiplied by 0: an infinity there leaves nothing.
+__device__ __forceinline__ void drop8(const Drop& d, uint4 q, float (&v)[8],
+                                      const float (&r)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -226,18 +229,15 @@ __device__ __forceinline__ void drop8(const Drop& d, uint64_t offset, long long 
     v[2 * i + 1] = w[i] < d.threshold ? fmaf(v[2 * i + 1], d.scale, r[2 * i + 1]) : r[2 * i + 1];
   }
 }
-__device__ __forceinline__ void drop8(const Drop& d, uint64_t offset, long long row, int n,
-                                      float (&v)[8]) {
+__device__ __forceinline__ void drop8(const Drop& d, uint4 q, float (&v)[8]) {
   const float none[8] = {};
-  drop8(d, offset, row, n, v, none);
+  drop8(d, q, v, none);
 }
 
 // One element, of column n.
 __device__ __forceinline__ float drop1(const Drop& d, uint64_t offset, long long row, int n,
                                        float v, float r) {
-  const uint4 q = philox(d, make_uint4(static_cast<uint32_t>(n) / 8u, static_cast<uint32_t>(row),
-                                       static_cast<uint32_t>(offset),
-                                       static_cast<uint32_t>(offset >> 32)));
+  const uint4 q = drop_bits(d, offset, row, n);
   const int i = n % 8 / 2;
   const uint32_t w = i < 2 ? (i == 0 ? q.x : q.y) : (i == 2 ? q.z : q.w);
   return (n % 2 ? w : w << 16) < d.threshold ? fmaf(v, d.scale, r) : r;
@@ -266,11 +266,14 @@ __device__ __forceinline__ void group_sync(int group) {
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kThreads) : "memory");
 }
 
-// kThreads = 32: a warp; else a group of kThreads threads, through its red (16-byte aligned; one
+// kThreads <= 32: a warp or an aligned part of one; else a group of kThreads threads, through its
+// red (16-byte aligned; one
 // array of kThreads / 32 values for each sum that may be in flight between two barriers).
 template <int kThreads>
 __device__ __forceinline__ float row_sum(float v, float* red, int group = 0) {
-  v = warp_sum_all(v);
+#pragma unroll
+  for (int o = (kThreads < 32 ? kThreads : 32) / 2; o > 0; o /= 2)
+    v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (kThreads > 32) {
     constexpr int kWarps = kThreads / 32;
     if (threadIdx.x % 32 == 0) red[threadIdx.x % kThreads / 32] = v;
@@ -292,31 +295,45 @@ __device__ __forceinline__ float row_sum(float v, float* red, int group = 0) {
   return v;
 }
 
-// Two sums at once; red: kThreads / 32 pairs.  Half the lanes carry one sum on, half the other.
+// Two sums at once over kThreads <= 32 lanes: half the lanes carry one sum on, half the other,
+// which is the upper half's (of all kThreads).
 template <int kThreads>
-__device__ __forceinline__ void row_sums(float& a, float& b, float2* red, int group = 0) {
+__device__ __forceinline__ float pair_sum(float a, float b, bool upper) {
+  float v = upper ? b : a;
+  v += __shfl_xor_sync(0xffffffffu, upper ? a : b, kThreads / 2);
+#pragma unroll
+  for (int o = kThreads / 4; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Both sums in every one of kThreads <= 32 lanes.
+template <int kThreads>
+__device__ __forceinline__ void lane_sums(float& a, float& b) {
+  const bool upper = threadIdx.x % kThreads >= kThreads / 2;
+  const float v = pair_sum<kThreads>(a, b, upper);
+  const float other = __shfl_xor_sync(0xffffffffu, v, kThreads / 2);
+  a = upper ? other : v;
+  b = upper ? v : other;
+}
+
+// Both sums over kThreads >= 64 threads.  First each warp leaves its own in red (kThreads / 32
+// pairs, 16-byte aligned); after a barrier every thread adds the warps'.
+template <int kThreads>
+__device__ __forceinline__ void leave_sums(float a, float b, float2* red) {
   const int lane = threadIdx.x % 32;
   const bool upper = lane >= 16;
-  float v = upper ? b : a;
-  v += __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+  const float v = pair_sum<32>(a, b, upper);
+  if (lane % 16 == 0) reinterpret_cast<float*>(red + threadIdx.x % kThreads / 32)[upper] = v;
+}
+template <int kThreads>
+__device__ __forceinline__ void take_sums(float& a, float& b, const float2* red) {
+  uint64_t s = 0;
 #pragma unroll
-  for (int o = 8; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (kThreads == 32) {
-    const float other = __shfl_xor_sync(0xffffffffu, v, 16);
-    a = upper ? other : v;
-    b = upper ? v : other;
-  } else {
-    constexpr int kWarps = kThreads / 32;
-    if (lane % 16 == 0) reinterpret_cast<float*>(red + threadIdx.x % kThreads / 32)[upper] = v;
-    group_sync<kThreads>(group);
-    uint64_t s = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps / 2; ++i) {
-      const float4 q = reinterpret_cast<const float4*>(red)[i];
-      s = add2(s, add2(pair(q.x, q.y), pair(q.z, q.w)));
-    }
-    unpair(s, a, b);
+  for (int i = 0; i < kThreads / 64; ++i) {
+    const float4 q = reinterpret_cast<const float4*>(red)[i];
+    s = add2(s, add2(pair(q.x, q.y), pair(q.z, q.w)));
   }
+  unpair(s, a, b);
 }
 
 }  // namespace igc

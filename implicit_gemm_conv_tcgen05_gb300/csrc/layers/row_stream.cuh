@@ -30,7 +30,7 @@ struct RowStream {
 };
 
 // Sites of waits that gave up (device status word).
-enum : uint32_t { kSiteNormRow = 0x4c01, kSiteNormBwdRow = 0x4c02, kSiteRowDrain = 0x4c03 };
+enum : uint32_t { kSiteNormBwdRow = 0x4c01, kSiteRowDrain = 0x4c02 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst_smem, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
@@ -60,9 +60,12 @@ __device__ __forceinline__ void fill_slot(const RowStream& s, char* slot, uint64
 template <int kT>
 __device__ __forceinline__ void keep_weights(char* to, uint32_t plane, const void* p, int N8,
                                              bool f32) {
-  for (int n = threadIdx.x; n < N8; n += blockDim.x) {
-    const float v = p == nullptr ? 1.0f : load_vec(p, n, kT == IGC_F32 || f32, kT == IGC_BF16);
-    reinterpret_cast<float*>(to + n % 8 / 4 * plane)[n / 8 * 4 + n % 4] = v;
+#pragma unroll 4
+  for (int n = static_cast<int>(threadIdx.x) * 8; n < N8; n += static_cast<int>(blockDim.x) * 8) {
+    float v[8];
+    load_vec8<kT>(p, n, N8, f32, 1.0f, v);
+    reinterpret_cast<float4*>(to)[n / 8] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(to + plane)[n / 8] = make_float4(v[4], v[5], v[6], v[7]);
   }
 }
 __device__ __forceinline__ void kept_weights(const char* from, uint32_t plane, int n,

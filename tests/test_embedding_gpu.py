@@ -123,6 +123,20 @@ def test_backward_widths(D):
         backward(M, 50, D, F32, F32, "one")
 
 
+@pytest.mark.parametrize("M", [65536, 65537, 131073, 262144, 262145, 1200000])
+def test_many_positions(M):
+    """The sort's blocks hold one, several and many runs of positions."""
+    backward(M, 90000, 9, F32, F32, "frequent")
+    backward(M, 1000, 4, BF16, F32, "any", itype=torch.int32)
+
+
+@pytest.mark.parametrize("D", [8, 16, 40, 64, 100, 128, 500, 520])
+def test_narrow_rows_share_blocks(D):
+    for M in (1100, 5000, 70000):
+        backward(M, 900, D, BF16, F32)
+        backward(M, 17, D, F16, F16, "few")
+
+
 def test_a_token_at_every_position():
     """One token's 70000 rows: sums of sums over all chunks."""
     backward(70000, 3, 512, BF16, F32, "one")
