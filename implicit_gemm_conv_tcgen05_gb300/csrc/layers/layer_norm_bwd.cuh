@@ -11,6 +11,8 @@
 // blocks' in order (no atomics).
 #pragma once
 
+#include <mutex>
+
 #include "row_stream_host.h"
 
 namespace igc {
@@ -80,8 +82,10 @@ __device__ __forceinline__ void terms8(float mean, float rstd, const float (&w)[
 
 constexpr int kNormBwdStreamMost = 512;  // 128 registers each
 
-// Rows streamed through shared memory (row_stream.cuh), two units to a thread.
-template <int kT, int kS, int kLanes, bool kDrop>
+// Rows streamed through shared memory (row_stream.cuh), two units to a thread.  Rows of more
+// columns than a block has are shared by the kCluster blocks of a cluster, which exchange their
+// sums through distributed shared memory.
+template <int kT, int kS, int kLanes, int kCluster, bool kDrop>
 __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
     layer_norm_bwd_stream_kernel(const NormBwdParams p, const RowStream st) {
   constexpr int kGroups = kNormBwdStreamMost / kLanes, kUnits = 2;
@@ -89,33 +93,48 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   extern __shared__ __align__(128) char ring[];
   __shared__ uint64_t full[kGroups][kMaxSlots];
   __shared__ __align__(16) float2 red[kGroups][2][(kLanes / 32 + 1) / 2 * 2];
+  // the cluster's sums, by block, and the barriers that count their arrival: two of each, for
+  // alternate rows
+  __shared__ __align__(16) uint64_t met[kGroups][2][kCluster], met_bar[kGroups][2];
   __shared__ int abort_flag;
-  const RowWalk walk = row_walk<kLanes, kGroups>(st, ring, full, &abort_flag, p.M);
+  const RowWalk walk = row_walk<kLanes, kGroups, kCluster>(st, ring, full, &abort_flag, p.M);
+  if constexpr (kCluster > 1) {
+    if (walk.t == 0) {
+      mbar_init(&met_bar[walk.group][0], 1);
+      mbar_init(&met_bar[walk.group][1], 1);
+      fence_mbar_init();
+    }
+    cluster_sync();
+  }
   grid_dependency_wait();
   grid_dependents_launch();
-  const int t = walk.t, N8 = p.N / 8 * 8;
+  // this block's columns [col0, col0 + cols), whole units
+  const int t = walk.t, N8 = p.N / 8 * 8, share = (N8 / 8 + kCluster - 1) / kCluster * 8;
+  const int rank = kCluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int col0 = rank * share, cols = min(share, N8 - col0);
   const bool has_a = p.A != nullptr, has_s = p.dS != nullptr, has_x = p.dX != nullptr;
   auto fill = [&](int k) {
     const long long row = walk.first + k * walk.step;
     const int slot = k % st.slots;
-    const char* const from[kStreamMats] = {row_at<kT>(p.dY, row, p.lddy),
-                                           row_at<kS>(p.S, row, p.lds),
-                                           row_at<kS>(p.A, row, p.lda)};
-    fill_slot(st, walk.slots + slot * st.slot_bytes, walk.bars + slot, from);
+    const char* const from[kStreamMats] = {row_at<kT>(p.dY, row, p.lddy) + col0 * kSizeT,
+                                           row_at<kS>(p.S, row, p.lds) + col0 * kSizeS,
+                                           row_at<kS>(p.A, row, p.lda) + col0 * kSizeS};
+    fill_slot(st, walk.slots + slot * st.slot_bytes, walk.bars + slot, from,
+              static_cast<uint32_t>(cols));
   };
   // A group of one warp refills a slot when its row is done; a larger one after the barrier of
   // the next row, a row later: it fills one slot less at first.
   constexpr int kBehind = kLanes == 32 ? 0 : 1;
   if (t == 0)
     for (int k = 0; k < walk.count && k < st.slots - kBehind; ++k) fill(k);
-  keep_weights<kT>(ring, st.plane, p.w, N8, p.w_f32);
+  keep_weights<kT>(ring, st.plane, p.w, col0, cols, p.w_f32);
   __syncthreads();
   const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
   const float inv = 1.0f / static_cast<float>(p.N);
   float sw[kUnits][8] = {}, sb[kUnits][8] = {}, sw_last = 0.0f, sb_last = 0.0f;
   // the column past the whole units that this thread has, if any; the next row's statistics and
   // its elements there arrive during a row
-  const int last = N8 + t < p.N ? N8 + t : -1;
+  const int last = rank == kCluster - 1 && N8 + t < p.N ? N8 + t : -1;
   const float w_last =
       last >= 0 && p.w != nullptr
           ? load_vec(p.w, last, kT == IGC_F32 || p.w_f32, kT == IGC_BF16)
@@ -130,14 +149,15 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
     mean = p.mean[walk.first], rstd = p.rstd[walk.first];
     if (last >= 0) load_last(walk.first);
   }
-  char* ds_row = row_at<kS>(p.dS, walk.first, p.ldds);
-  char* dx_row = row_at<kT>(p.dX, walk.first, p.lddx);
+  char* ds_row = row_at<kS>(p.dS, walk.first, p.ldds) + col0 * kSizeS;
+  char* dx_row = row_at<kT>(p.dX, walk.first, p.lddx) + col0 * kSizeT;
   const long long ds_step = walk.step * p.ldds * kSizeS, dx_step = walk.step * p.lddx * kSizeT;
   int stopped = -1;  // the row whose wait gave up
   int slot = 0;
   uint32_t phase = 0;
-  // whole: every lane of the warp has all its units, so that nothing keeps the loads and the
-  // arithmetic of different units apart (a branch for each unit exposes every unit's latency)
+  // whole: every lane of the warp has all its units, so that no branch keeps the loads and the
+  // arithmetic of different units apart (16384 x 4096 bf16 with dropout: 111 us, with a branch
+  // for each unit 122)
   auto walk_rows = [&](auto whole) {
     for (int k = 0; k < walk.count; ++k) {
       const long long row = walk.first + k * walk.step;
@@ -154,7 +174,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const int n = (i * kLanes + t) * 8;
-        if (!decltype(whole)::value && n >= N8) continue;
+        if (!decltype(whole)::value && n >= cols) continue;
         float wv[8];
         kept_weights(ring, st.plane, n, wv);
         load_unit<kT>(at + st.at[0] + n * kSizeT, g[i]);
@@ -176,7 +196,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       if constexpr (kDrop) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
-          bits[i] = drop_bits(p.drop, offset, row, (i * kLanes + t) * 8);
+          bits[i] = drop_bits(p.drop, offset, row, col0 + (i * kLanes + t) * 8);
       }
       if constexpr (kLanes == 32) {
         lane_sums<32>(c1, c2);
@@ -184,6 +204,26 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
         leave_sums<kLanes>(c1, c2, red[walk.group][k & 1]);
         group_sync<kLanes>(walk.group);
         take_sums<kLanes>(c1, c2, red[walk.group][k & 1]);
+      }
+      if constexpr (kCluster > 1) {
+        // (the bytes of the row after the next go to this row's barrier: they are sent by a block
+        // that has met the next row's, which this block sends after all of it has met this row's)
+        uint64_t* bar = &met_bar[walk.group][k & 1];
+        uint64_t* sums = met[walk.group][k & 1];
+        if (t == 0) {
+          mbar_arrive_expect_tx(bar, 8 * kCluster);
+#pragma unroll
+          for (int r = 0; r < kCluster; ++r)
+            store_async_u64(mapa_shared(smem_u32(sums + rank), r), pair(c1, c2),
+                            mapa_shared(smem_u32(bar), r));
+        }
+        if (!mbar_wait<true>(bar, static_cast<uint32_t>(k / 2) & 1u, st.wait_limit, &abort_flag,
+                             st.status, kSiteNormBwdMeet) && stopped < 0)
+          stopped = k;
+        uint64_t both = sums[0];
+#pragma unroll
+        for (int r = 1; r < kCluster; ++r) both = add2(both, sums[r]);
+        unpair(both, c1, c2);
       }
       if (kBehind && t == 0 && stopped < 0 && k + st.slots - 1 < walk.count)
         fill(k + st.slots - 1);
@@ -193,7 +233,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const int n = (i * kLanes + t) * 8;
-        if (!decltype(whole)::value && n >= N8) continue;
+        if (!decltype(whole)::value && n >= cols) continue;
         float d[8], f[8] = {};
         if (has_a) load_unit<kS>(at + st.at[2] + n * kSizeS, f);
   #pragma unroll
@@ -210,9 +250,9 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       }
       if (last >= 0) {
         const float d = fmaf(rstd, fmaf(-h_last, c2, g_last - c1), f_last);
-        if (has_s) store1<kS>(ds_row, last, d);
+        if (has_s) store1<kS>(ds_row, last - col0, d);
         if (has_x)
-          store1<kT>(dx_row, last, kDrop ? drop1(p.drop, offset, row, last, d, 0.0f) : d);
+          store1<kT>(dx_row, last - col0, kDrop ? drop1(p.drop, offset, row, last, d, 0.0f) : d);
       }
       if constexpr (!kBehind) {
         __syncwarp();
@@ -224,39 +264,43 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       if (++slot == st.slots) slot = 0, phase ^= 1u;
     }
   };
-  if (__all_sync(0xffffffffu, ((kUnits - 1) * kLanes + t) * 8 < N8))
+  if (__all_sync(0xffffffffu, ((kUnits - 1) * kLanes + t) * 8 < cols))
     walk_rows(std::true_type{});
   else
     walk_rows(std::false_type{});
   if (t == 0 && stopped >= 0)
     drain_slots(st, walk.bars, stopped, min(walk.count, stopped + st.slots));
+  if constexpr (kCluster > 1) cluster_sync();  // no block may exit before what is sent to it is there
   if (p.partial == nullptr) return;
-  // one row of sums per block: the groups' go over their rings, and are added in order
+  // one row of sums per block or cluster: the groups' go over their rings, and are added in order
   float* tot = reinterpret_cast<float*>(ring);
+  const int width = (rank == kCluster - 1 ? p.N : col0 + cols) - col0;
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
     const float(&acc)[kUnits][8] = v ? sb : sw;
-    float* to = tot + (walk.group * 2 + v) * p.N;
+    float* to = tot + (walk.group * 2 + v) * width;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int n = (i * kLanes + t) * 8;
-      if (n >= N8) continue;
+      if (n >= cols) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) to[n + j] = acc[i][j];
     }
-    if (last >= 0) to[last] = v ? sb_last : sw_last;
+    if (last >= 0) to[last - col0] = v ? sb_last : sw_last;
   }
   __syncthreads();
-  for (int n = threadIdx.x; n < p.N; n += kGroups * kLanes) {
+  const int rows = static_cast<int>(gridDim.x) / kCluster;
+  float* out = p.partial + static_cast<long long>(blockIdx.x / kCluster) * p.N + col0;
+  for (int n = threadIdx.x; n < width; n += kGroups * kLanes) {
     float dw = 0.0f, db = 0.0f;
 #pragma unroll
     for (int r = 0; r < kGroups; ++r) {
-      dw += tot[2 * r * p.N + n];
-      db += tot[(2 * r + 1) * p.N + n];
+      dw += tot[2 * r * width + n];
+      db += tot[(2 * r + 1) * width + n];
     }
-    p.partial[static_cast<long long>(blockIdx.x) * p.N + n] = dw;
-    p.partial[(static_cast<long long>(gridDim.x) + blockIdx.x) * p.N + n] = db;
+    out[n] = dw;
+    out[static_cast<long long>(rows) * p.N + n] = db;
   }
 }
 
@@ -425,22 +469,32 @@ int launch_narrow(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int*
 }
 
 // *done: whether a block's shared memory holds two rows of every group.
-template <int kT, int kS, int kLanes>
+template <int kT, int kS, int kLanes, int kCluster>
 int stream_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
                     bool* done, cudaStream_t stream) {
   constexpr int kGroups = kNormBwdStreamMost / kLanes;
+  auto kernel = drop ? layer_norm_bwd_stream_kernel<kT, kS, kLanes, kCluster, true>
+                     : layer_norm_bwd_stream_kernel<kT, kS, kLanes, kCluster, false>;
+  int64_t most = dev.sm_count;
+  if constexpr (kCluster > 1) {
+    static std::once_flag once[64];
+    static int clusters[64];
+    std::call_once(once[dev.device], [&] {
+      clusters[dev.device] = stream_clusters(kernel, dev, kCluster, kGroups * kLanes);
+    });
+    most = clusters[dev.device];
+  }
   RowStream st;
+  const int64_t cols = (p.N / 8 + kCluster - 1) / kCluster * 8;
   const int sizes[kStreamMats] = {static_cast<int>(elem_size(kT)), static_cast<int>(elem_size(kS)),
                                   p.A != nullptr ? static_cast<int>(elem_size(kS)) : 0};
-  *done = plan_stream(dev, p.N, sizes, kGroups, &st);
+  *done = most > 0 && plan_stream(dev, cols, sizes, kGroups, &st);
   if (!*done) return IGC_OK;
+  if (most > kMaxPartials) most = kMaxPartials;
   const int64_t all = (static_cast<int64_t>(p.M) + kGroups - 1) / kGroups;
-  const int64_t most = dev.sm_count < kMaxPartials ? dev.sm_count : kMaxPartials;
   *blocks = static_cast<int>(all < most ? all : most);
-  return launch_stream(drop ? layer_norm_bwd_stream_kernel<kT, kS, kLanes, true>
-                            : layer_norm_bwd_stream_kernel<kT, kS, kLanes, false>,
-                       dev, *blocks, kGroups * kLanes, kGroups,
-                       static_cast<size_t>(kGroups) * p.N * 8, stream, p, st);
+  return launch_stream(kernel, dev, *blocks * kCluster, kCluster, kGroups * kLanes, kGroups,
+                       static_cast<size_t>(kGroups) * (cols + 8) * 8, stream, p, st);
 }
 
 // *blocks: rows of partial sums that it leaves.
@@ -456,15 +510,23 @@ int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* 
   if (!p.vec)
     done = false;
   else if (units <= 64)
-    rc = stream_norm_bwd<kT, kS, 32>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 32, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 128)
-    rc = stream_norm_bwd<kT, kS, 64>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 64, 1>(dev, p, drop, blocks, &done, stream);
+  else if (units <= 192)  // (32768 x 1536 bf16: five rows at once, 88 us; four of 128 threads 108)
+    rc = stream_norm_bwd<kT, kS, 96, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 256)
-    rc = stream_norm_bwd<kT, kS, 128>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 128, 1>(dev, p, drop, blocks, &done, stream);
+  else if (units <= 320)  // (16384 x 2500: three at once, 93 us; two of 256 threads 125)
+    rc = stream_norm_bwd<kT, kS, 160, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 512)
-    rc = stream_norm_bwd<kT, kS, 256>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 256, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 1024)
-    rc = stream_norm_bwd<kT, kS, 512>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 512, 1>(dev, p, drop, blocks, &done, stream);
+  else if (units <= 2048)
+    rc = stream_norm_bwd<kT, kS, 256, 4>(dev, p, drop, blocks, &done, stream);
+  else if (units <= 4096)
+    rc = stream_norm_bwd<kT, kS, 256, 8>(dev, p, drop, blocks, &done, stream);
   if (done) return rc;
   if (p.dS != nullptr || p.dX != nullptr) {
     const int rc = launch_pdl(drop ? layer_norm_bwd_any_kernel<kT, kS, true>

@@ -327,9 +327,10 @@ __device__ __forceinline__ void leave_sums(float a, float b, float2* red) {
 }
 template <int kThreads>
 __device__ __forceinline__ void take_sums(float& a, float& b, const float2* red) {
-  uint64_t s = 0;
+  constexpr int kWarps = kThreads / 32;
+  uint64_t s = kWarps % 2 ? pair(red[kWarps - 1].x, red[kWarps - 1].y) : 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) {
+  for (int i = 0; i < kWarps / 2; ++i) {
     const float4 q = reinterpret_cast<const float4*>(red)[i];
     s = add2(s, add2(pair(q.x, q.y), pair(q.z, q.w)));
   }

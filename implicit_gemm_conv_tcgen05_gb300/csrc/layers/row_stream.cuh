@@ -23,14 +23,14 @@ struct RowStream {
   int slots = 0;
   uint32_t slot_bytes = 0;
   uint32_t at[kStreamMats] = {};     // where an input's row starts in its slot
-  uint32_t bytes[kStreamMats] = {};  // copied of it (0: the input is absent)
+  uint32_t size[kStreamMats] = {};   // bytes of its elements (0: the input is absent)
   uint32_t plane = 0;                // bytes of each half of the kept weights, ahead of the ring
   uint64_t wait_limit = 0;
   unsigned long long* status = nullptr;
 };
 
 // Sites of waits that gave up (device status word).
-enum : uint32_t { kSiteNormBwdRow = 0x4c01, kSiteRowDrain = 0x4c02 };
+enum : uint32_t { kSiteNormBwdRow = 0x4c01, kSiteNormBwdMeet = 0x4c02, kSiteRowDrain = 0x4c03 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst_smem, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
@@ -41,29 +41,40 @@ __device__ __forceinline__ void bulk_load(uint32_t dst_smem, const void* src, ui
       : "memory");
 }
 
-// One thread: the row's inputs (rows[i]: where input i's row starts) into a slot.
+// One thread: `cols` columns (whole units) of a row's inputs into a slot; from[i] is where those
+// of input i start.
 __device__ __forceinline__ void fill_slot(const RowStream& s, char* slot, uint64_t* bar,
-                                          const char* const (&rows)[kStreamMats]) {
+                                          const char* const (&from)[kStreamMats], uint32_t cols) {
   uint32_t total = 0;
 #pragma unroll
-  for (int i = 0; i < kStreamMats; ++i) total += s.bytes[i];
+  for (int i = 0; i < kStreamMats; ++i) total += s.size[i] * cols;
   mbar_arrive_expect_tx(bar, total);
   const uint32_t to = smem_u32(slot);
+  if (cols == 0) return;
 #pragma unroll
   for (int i = 0; i < kStreamMats; ++i)
-    if (s.bytes[i] != 0) bulk_load(to + s.at[i], rows[i], s.bytes[i], bar);
+    if (s.size[i] != 0) bulk_load(to + s.at[i], from[i], s.size[i] * cols, bar);
 }
 
-// The whole block: the weights of the whole units (fp32, or of type kT; 1 for none) into shared
-// memory, the first four of each unit in one plane and the last four in another: a warp's
+// Eight bytes into the shared memory of a block of the cluster, counted by a barrier there
+// (addresses in the cluster's shared window).
+__device__ __forceinline__ void store_async_u64(uint32_t to, uint64_t v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
+                   to),
+               "l"(v), "r"(bar)
+               : "memory");
+}
+
+// The whole block: the weights of its columns (whole units; fp32, or of type kT; 1 for none) into
+// shared memory, the first four of each unit in one plane and the last four in another: a warp's
 // 16-byte loads then meet no bank twice.
 template <int kT>
-__device__ __forceinline__ void keep_weights(char* to, uint32_t plane, const void* p, int N8,
-                                             bool f32) {
+__device__ __forceinline__ void keep_weights(char* to, uint32_t plane, const void* p, int col0,
+                                             int cols, bool f32) {
 #pragma unroll 4
-  for (int n = static_cast<int>(threadIdx.x) * 8; n < N8; n += static_cast<int>(blockDim.x) * 8) {
+  for (int n = static_cast<int>(threadIdx.x) * 8; n < cols; n += static_cast<int>(blockDim.x) * 8) {
     float v[8];
-    load_vec8<kT>(p, n, N8, f32, 1.0f, v);
+    load_vec8<kT>(p, col0 + n, col0 + cols, f32, 1.0f, v);
     reinterpret_cast<float4*>(to)[n / 8] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(to + plane)[n / 8] = make_float4(v[4], v[5], v[6], v[7]);
   }
@@ -96,7 +107,8 @@ struct RowWalk {
 };
 
 // The start of a streaming kernel: barriers and walk (ring: the dynamic shared memory).
-template <int kLanes, int kGroups>
+// (kCluster blocks that share rows walk down the same ones.)
+template <int kLanes, int kGroups, int kCluster>
 __device__ __forceinline__ RowWalk row_walk(const RowStream& st, char* ring,
                                             uint64_t (&full)[kGroups][kMaxSlots],
                                             int* abort_flag, int M) {
@@ -110,8 +122,8 @@ __device__ __forceinline__ RowWalk row_walk(const RowStream& st, char* ring,
     fence_mbar_init();
   }
   if (threadIdx.x == 0) *abort_flag = 0;
-  w.first = static_cast<long long>(blockIdx.x) * kGroups + w.group;
-  w.step = static_cast<long long>(gridDim.x) * kGroups;
+  w.first = static_cast<long long>(blockIdx.x / kCluster) * kGroups + w.group;
+  w.step = static_cast<long long>(gridDim.x / kCluster) * kGroups;
   w.count = w.first < M ? static_cast<int>((M - w.first + w.step - 1) / w.step) : 0;
   return w;
 }

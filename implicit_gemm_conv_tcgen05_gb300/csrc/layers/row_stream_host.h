@@ -8,15 +8,16 @@ namespace igc {
 
 constexpr int kStreamStatic = 3072;  // bytes for the kernels' static shared memory
 
-// The ring for rows of N columns whose inputs have elements of sizes[i] bytes (0: absent), with
-// `groups` rings to a block: false where rows are too long for one (at least two slots).
+// The ring for rows of which a block has at most N columns (whole units), of inputs whose elements
+// have sizes[i] bytes (0: absent), with `groups` rings to a block: false where rows are too long
+// for one (at least two slots).
 inline bool plan_stream(const DeviceInfo& dev, int64_t N, const int (&sizes)[kStreamMats],
                         int groups, RowStream* s) {
   uint32_t at = 0;
   for (int i = 0; i < kStreamMats; ++i) {
     s->at[i] = at;
-    s->bytes[i] = static_cast<uint32_t>(N / 8 * 8 * sizes[i]);
-    at += s->bytes[i];
+    s->size[i] = static_cast<uint32_t>(sizes[i]);
+    at += static_cast<uint32_t>(N / 8 * 8 * sizes[i]);
   }
   s->slot_bytes = at > 0 ? (at + 127) / 128 * 128 : 128;  // (no whole unit: nothing to copy)
   s->plane = static_cast<uint32_t>((N / 8 * 16 + 127) / 128 * 128);
@@ -32,8 +33,8 @@ inline bool plan_stream(const DeviceInfo& dev, int64_t N, const int (&sizes)[kSt
 
 // least: bytes of dynamic shared memory that the kernel uses whatever the ring takes.
 template <typename P>
-int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int blocks, int threads,
-                  int groups, size_t least, cudaStream_t stream, const P& p, const RowStream& s) {
+int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int blocks, int cluster,
+                  int threads, int groups, size_t least, cudaStream_t stream, const P& p, const RowStream& s) {
   // (the attribute belongs to the function: set by every call, which costs less than to look
   // whether it is)
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -43,8 +44,50 @@ int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int block
   }
   const size_t bytes = static_cast<size_t>(2) * s.plane +
                        static_cast<size_t>(groups) * s.slots * s.slot_bytes;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(static_cast<unsigned>(threads)),
-                    bytes < least ? least : bytes, stream, p, s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = bytes < least ? least : bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p, s) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return IGC_ERR_CUDA;
+  }
+  return IGC_OK;
+}
+
+// Clusters of `cluster` streaming blocks (one to an SM) that the device runs at once, of any
+// streaming kernel; 0 if that cannot be found out.
+template <typename P>
+int stream_clusters(void (*kernel)(P, RowStream), const DeviceInfo& dev, int cluster,
+                    int threads) {
+  const int smem = static_cast<int>(dev.smem_optin) - kStreamStatic;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / cluster * cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  return n;
 }
 
 }  // namespace igc
