@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
         if (k + 1 < walk.count) load_last(row + walk.step);
       }
       // the bits of the dropout are made here, among the shuffles of the sums
-      uint4 bits[kDrop ? kUnits : 1];
+      [[maybe_unused]] uint4 bits[kDrop ? kUnits : 1];
       if constexpr (kDrop) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
