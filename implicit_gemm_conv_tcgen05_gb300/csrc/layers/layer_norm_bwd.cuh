@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
         stopped = k;
       float g[kUnits][8], h[kUnits][8];
       uint64_t p1 = 0, p2 = 0;
-  #pragma unroll
+#pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const int n = (i * kLanes + t) * 8;
         if (!decltype(whole)::value && n >= cols) continue;
@@ -230,13 +230,13 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       c1 *= inv;
       c2 *= inv;
       const uint64_t r2 = pair(rstd, rstd), m1 = pair(-c1, -c1), m2 = pair(-c2, -c2);
-  #pragma unroll
+#pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const int n = (i * kLanes + t) * 8;
         if (!decltype(whole)::value && n >= cols) continue;
         float d[8], f[8] = {};
         if (has_a) load_unit<kS>(at + st.at[2] + n * kSizeS, f);
-  #pragma unroll
+#pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const uint64_t x =
               fma2(pair(h[i][j], h[i][j + 1]), m2, add2(pair(g[i][j], g[i][j + 1]), m1));

@@ -10,13 +10,18 @@
  *  - Matrices are row-major with a row stride (ld*) in elements, at least their number
  *    of columns, and may start at any multiple of their element's size.  Rows that start
  *    on 16-byte boundaries (of every matrix of the call) are read and written 16 bytes at
- *    a time; others element by element, at a fraction of the speed.
- *  - Sizes: anything that fits 32 bits.  An empty output is a no-op.
+ *    a time; others element by element, at a fraction of the speed.  Anything else is
+ *    IGC_ERR_MISALIGNED.
+ *  - Sizes: anything that fits 32 bits; what would need more than 2^31 - 1 blocks is
+ *    IGC_ERR_UNSUPPORTED.  An empty output is a no-op.
  *  - Aliasing: outputs must not overlap inputs or each other, but for the pairs that an
  *    entry names; those are the same pointer, type and row stride.  An output pointer that
  *    equals another pointer of the call is refused; other overlaps are not detected.
  *  - Results do not vary from run to run: every sum has a fixed order.
  *  - Nothing past a row's last column is written.
+ *  - Workspaces: 256-byte aligned device memory of at least the size that the
+ *    *_workspace_size function gives, not shared with a concurrent call; nothing in one
+ *    need survive between calls.
  *
  * Dropout.  Where an entry takes (p, seed, offset, step), drop(X) below is
  *
@@ -80,7 +85,10 @@ int dropout_add(int64_t M, int64_t N, const void *X, int64_t ldx, int x_dtype,
  *  mean, rstd  device fp32 vectors of M elements; either may be NULL: not stored.
  *
  *  dtype: any; s_dtype: dtype or IGC_F32 (a residual stream kept in fp32).  N >= 1.  The
- *  statistics and Y are those of the fp32 S, before it is rounded where it is stored.
+ *  statistics and Y are those of the fp32 S, before it is rounded where it is stored.  The
+ *  variance is a sum of squared differences from the mean in fp32: a row whose values differ by
+ *  more than 2^63 has an infinite one (rstd 0, Y = b), one whose sum overflows a mean that is not
+ *  finite (Y NaN).
  */
 int layer_norm(int64_t M, int64_t N, int dtype, const void *X, int64_t ldx,
                const void *R, int64_t ldr, int s_dtype, double p, uint64_t seed,
