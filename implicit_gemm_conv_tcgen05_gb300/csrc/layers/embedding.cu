@@ -1,7 +1,7 @@
 // embedding_lookup: Y[i] = scale W[token[i]].
 //
 // Bound by memory: the rows that are asked for are read once (a second time mostly from L2), Y
-// is written once.
+// is written once (32768 rows of 131072 x 4096 bf16: 64 us, 366 MB at 5.7 TB/s).
 #include "layers_host.h"
 
 namespace igc {

@@ -8,9 +8,10 @@
 // Further blocks write the zeros of the rows that no token points to.
 //
 // Many: the positions are sorted by token first (stable, so that a token's positions stay in
-// order), with a radix sort.  Blocks then walk chunks of 32 to 128
-// sorted positions and write each token's sum; the sums of a token that crosses a chunk's border go to
-// the workspace, and a last kernel adds them in order.  No atomics on sums.
+// order), with a radix sort.  Blocks then walk chunks of 32 to 128 sorted positions and write each
+// token's sum; the sums of a token that crosses a chunk's border go to the workspace, and a last
+// kernel adds them in order.  No atomics on sums.  32768 positions of 131072 x 4096 bf16: 208 us,
+// 1.34 GB at 6.5 TB/s, 21 us of it the sort.
 #include "layers_host.h"
 
 namespace igc {

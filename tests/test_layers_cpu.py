@@ -150,9 +150,9 @@ def test_workspace_sizes():
     size = igc.embedding_backward_workspace_size
     assert size(-1, 8, 8) == 0 and size(8, -1, 8) == 0 and size(8, 8, -1) == 0
     assert size(1, 100000, 4096) == 0 and size(5000, 0, 8) == 0 and size(5000, 8, 0) == 0
-    # tokens and positions twice, a byte for each row of the table, two rows of fp32 sums for 32
-    # positions
-    most = 4 * 4 * 8192 + 100000 + 2 * 256 * 64 * 4 + 8 * 256
+    # tokens and positions twice, a byte for each row of the table, the counts of 512 digits in 64
+    # blocks, two rows of fp32 sums for 32 positions
+    most = 4 * 4 * 8192 + 100000 + 64 * 512 * 4 + 2 * 256 * 64 * 4 + 8 * 256
     assert 4 * 4 * 8192 < size(8192, 100000, 64) <= most
 
 
