@@ -98,6 +98,7 @@ int layer_norm_backward(int64_t M, int64_t N, int dtype, const void* dY, int64_t
     a.lddy = lddy, a.lds = lds, a.lda = lda, a.ldds = ldds, a.lddx = lddx;
     a.mean = mean, a.rstd = rstd, a.w = w;
     a.partial = sums ? static_cast<float*>(workspace) : nullptr;
+    a.dw = dw, a.db = db, a.dw_f32 = dw_dtype == IGC_F32;
     active = active && dX != nullptr;
     if (dtype == IGC_F32)
       rc = layer_norm_bwd_f32(dev, a, active, &blocks, stream);
@@ -107,7 +108,7 @@ int layer_norm_backward(int64_t M, int64_t N, int dtype, const void* dY, int64_t
       rc = layer_norm_bwd_bf16(dev, a, s_dtype, active, &blocks, stream);
     if (rc != IGC_OK) return rc;
   }
-  if (!sums) return IGC_OK;
+  if (!sums || (M > 0 && blocks == 0)) return IGC_OK;
   return launch_pdl(norm_sums_kernel, dim3(static_cast<unsigned>((N + 31) / 32), 2), dim3(1024),
                     0, stream, static_cast<const float*>(workspace), blocks,
                     static_cast<int>(N), dw, db, dw_dtype == IGC_F32 ? 1 : 0,

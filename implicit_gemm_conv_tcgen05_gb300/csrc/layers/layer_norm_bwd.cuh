@@ -29,8 +29,15 @@ struct NormBwdParams {
   const float* rstd;
   const void* w;
   float* partial;  // [2][blocks][N]: dw, db (null: no column sums)
+  void* dw;        // written by the cluster that all blocks are, if they are one (join)
+  void* db;
+  int join, dw_f32;
   Drop drop;
 };
+
+// A batch of few rows is taken by at most this many blocks, one cluster: it adds the blocks' sums
+// through distributed shared memory and writes dw and db itself, one launch less.
+constexpr int kJoinBlocks = 8;
 
 constexpr int kMaxPartials = 512;  // rows of partial sums that the workspace has room for
 
@@ -54,6 +61,41 @@ __device__ __forceinline__ void grads8(const NormBwdParams& p, uint64_t offset, 
     if constexpr (kDrop) drop8(p.drop, drop_bits(p.drop, offset, row, n), d);
     store8<kT>(dx_row, n, p.N, vec, d);
   }
+}
+
+// The sums of one column by `blocks` blocks of a cluster, in order, where each has them at `sums`
+// (in its own shared memory).
+__device__ __forceinline__ float cluster_sum(const float* sums, int blocks) {
+  float total = 0.0f;
+#pragma unroll
+  for (int r = 0; r < kJoinBlocks; ++r)
+    if (r < blocks)
+      total += __uint_as_float(
+          ld_shared_cluster_u32(mapa_shared(smem_u32(sums), static_cast<uint32_t>(r))));
+  return total;
+}
+
+// The whole cluster: dw and db from the blocks' sums dw_sums[n] and db_sums[n], columns dealt
+// over the blocks.
+template <int kT>
+__device__ __noinline__ void join_sums(const NormBwdParams& p, const float* dw_sums,
+                                          const float* db_sums) {
+  const int blocks = static_cast<int>(gridDim.x);
+  cluster_sync();
+  for (int n = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x); n < p.N;
+       n += blocks * static_cast<int>(blockDim.x)) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      void* out = v ? p.db : p.dw;
+      if (out == nullptr) continue;
+      const float sum = cluster_sum((v ? db_sums : dw_sums) + n, blocks);
+      if (kT == IGC_F32 || p.dw_f32)
+        static_cast<float*>(out)[n] = sum;
+      else
+        store16(out, n, sum, kT == IGC_BF16);
+    }
+  }
+  cluster_sync();  // no block may exit while another reads its sums
 }
 
 // g and h of eight columns from dY (g) and S (h), with their part of the row's sums and of the
@@ -299,9 +341,14 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       dw += tot[2 * r * width + n];
       db += tot[(2 * r + 1) * width + n];
     }
-    out[n] = dw;
-    out[static_cast<long long>(rows) * p.N + n] = db;
+    if (p.join) {
+      tot[n] = dw, tot[width + n] = db;
+    } else {
+      out[n] = dw;
+      out[static_cast<long long>(rows) * p.N + n] = db;
+    }
   }
+  if (kCluster == 1 && p.join) join_sums<kT>(p, tot, tot + width);
 }
 
 // Rows of any length and alignment, without the column sums: the row is read twice.
@@ -392,11 +439,13 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const NormBwdPa
 // Narrow rows: kLanes threads to a row, a unit to a thread, several rows at a time so that their
 // loads and sums overlap (as many as 128 registers hold).  Rows of any alignment.
 constexpr int kNarrowThreads = 512;
+template <int kS>
+constexpr int kNarrowRowsOf = kS == IGC_F32 ? 2 : 4;
 
 template <int kT, int kS, int kLanes, bool kDrop>
 __global__ void __launch_bounds__(kNarrowThreads, 1)
     layer_norm_bwd_narrow_kernel(const NormBwdParams p) {
-  constexpr int kGroups = kNarrowThreads / kLanes, kNarrowRows = kS == IGC_F32 ? 2 : 4;
+  constexpr int kGroups = kNarrowThreads / kLanes, kNarrowRows = kNarrowRowsOf<kS>;
   __shared__ float tot[2][kGroups][kLanes * 8];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -452,26 +501,47 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     float sum = 0.0f;
 #pragma unroll 16
     for (int r = 0; r < kGroups; ++r) sum += tot[v][r][col];
-    p.partial[(static_cast<long long>(v) * gridDim.x + blockIdx.x) * p.N + col] = sum;
+    if (p.join)
+      tot[v][0][col] = sum;
+    else
+      p.partial[(static_cast<long long>(v) * gridDim.x + blockIdx.x) * p.N + col] = sum;
   }
+  if (p.join) join_sums<kT>(p, tot[0][0], tot[1][0]);
+}
+
+// Blocks of a launch whose blocks have `rows` rows side by side: as many as there is work for, at
+// most `most`.  *join (if not null): whether they are one cluster that adds its blocks' sums, as
+// where none then takes more than `once` rows, which take as long as one (64 x 1000 bf16: 15.0 us
+// a call, 6.6 on the device, as two launches 17.4 and 6.6; with four times the rows 15.0 and 10.0).
+inline int norm_bwd_blocks(const NormBwdParams& p, int64_t rows, int64_t once, int64_t most,
+                           bool* join) {
+  if (join != nullptr && p.partial != nullptr && p.M <= kJoinBlocks * once) {
+    *join = true;
+    most = kJoinBlocks;
+  }
+  const int64_t all = (static_cast<int64_t>(p.M) + rows - 1) / rows;
+  if (most > kMaxPartials) most = kMaxPartials;
+  return static_cast<int>(all < most ? all : most);
 }
 
 template <int kT, int kS, int kLanes>
-int launch_narrow(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
+int launch_narrow(const DeviceInfo& dev, NormBwdParams p, bool drop, int* blocks,
                   cudaStream_t stream) {
-  const int64_t rows = kNarrowThreads / kLanes;
-  const int64_t all = (static_cast<int64_t>(p.M) + rows - 1) / rows;
-  const int64_t most = dev.sm_count < kMaxPartials ? dev.sm_count : kMaxPartials;
-  *blocks = static_cast<int>(all < most ? all : most);
-  return launch_pdl(drop ? layer_norm_bwd_narrow_kernel<kT, kS, kLanes, true>
-                         : layer_norm_bwd_narrow_kernel<kT, kS, kLanes, false>,
-                    dim3(static_cast<unsigned>(*blocks)), dim3(kNarrowThreads), 0, stream, p);
+  constexpr int kRows = kNarrowThreads / kLanes;
+  bool join = false;
+  *blocks = norm_bwd_blocks(p, kRows, kRows * kNarrowRowsOf<kS>, dev.sm_count, &join);
+  p.join = join;
+  const int rc = launch_clusters(drop ? layer_norm_bwd_narrow_kernel<kT, kS, kLanes, true>
+                                      : layer_norm_bwd_narrow_kernel<kT, kS, kLanes, false>,
+                                 *blocks, join ? *blocks : 1, kNarrowThreads, 0, stream, p);
+  if (join) *blocks = 0;
+  return rc;
 }
 
 // *done: whether a block's shared memory holds two rows of every group.
 template <int kT, int kS, int kLanes, int kCluster>
-int stream_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
-                    bool* done, cudaStream_t stream) {
+int stream_norm_bwd(const DeviceInfo& dev, NormBwdParams p, bool drop, int* blocks, bool* done,
+                    cudaStream_t stream) {
   constexpr int kGroups = kNormBwdStreamMost / kLanes;
   auto kernel = drop ? layer_norm_bwd_stream_kernel<kT, kS, kLanes, kCluster, true>
                      : layer_norm_bwd_stream_kernel<kT, kS, kLanes, kCluster, false>;
@@ -490,14 +560,17 @@ int stream_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, in
                                   p.A != nullptr ? static_cast<int>(elem_size(kS)) : 0};
   *done = most > 0 && plan_stream(dev, cols, sizes, kGroups, &st);
   if (!*done) return IGC_OK;
-  if (most > kMaxPartials) most = kMaxPartials;
-  const int64_t all = (static_cast<int64_t>(p.M) + kGroups - 1) / kGroups;
-  *blocks = static_cast<int>(all < most ? all : most);
-  return launch_stream(kernel, dev, *blocks * kCluster, kCluster, kGroups * kLanes, kGroups,
-                       static_cast<size_t>(kGroups) * (cols + 8) * 8, stream, p, st);
+  bool join = false;
+  *blocks = norm_bwd_blocks(p, kGroups, kGroups, most, kCluster == 1 ? &join : nullptr);
+  p.join = join;
+  const int rc = launch_stream(kernel, dev, *blocks * kCluster, join ? *blocks : kCluster,
+                               kGroups * kLanes, kGroups,
+                               static_cast<size_t>(kGroups) * (cols + 8) * 8, stream, p, st);
+  if (join) *blocks = 0;
+  return rc;
 }
 
-// *blocks: rows of partial sums that it leaves.
+// *blocks: rows of partial sums that it leaves (0: it has written dw and db).
 template <int kT, int kS>
 int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
                  cudaStream_t stream) {

@@ -6,7 +6,7 @@
 
 namespace igc {
 
-constexpr int kStreamStatic = 3072;  // bytes for the kernels' static shared memory
+constexpr int kStreamStatic = 2560;  // bytes for the kernels' static shared memory
 
 // The ring for rows of which a block has at most N columns (whole units), of inputs whose elements
 // have sizes[i] bytes (0: absent), with `groups` rings to a block: false where rows are too long
@@ -31,6 +31,30 @@ inline bool plan_stream(const DeviceInfo& dev, int64_t N, const int (&sizes)[kSt
   return true;
 }
 
+// Blocks in clusters of `cluster` (1: none), which may start while the kernel before them ends.
+template <typename... Params, typename... Args>
+int launch_clusters(void (*kernel)(Params...), int blocks, int cluster, int threads, size_t smem,
+                    cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return IGC_ERR_CUDA;
+  }
+  return IGC_OK;
+}
+
 // least: bytes of dynamic shared memory that the kernel uses whatever the ring takes.
 template <typename P>
 int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int blocks, int cluster,
@@ -44,24 +68,8 @@ int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int block
   }
   const size_t bytes = static_cast<size_t>(2) * s.plane +
                        static_cast<size_t>(groups) * s.slots * s.slot_bytes;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = bytes < least ? least : bytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p, s) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return IGC_ERR_CUDA;
-  }
-  return IGC_OK;
+  return launch_clusters(kernel, blocks, cluster, threads, bytes < least ? least : bytes, stream, p,
+                         s);
 }
 
 // Clusters of `cluster` streaming blocks (one to an SM) that the device runs at once, of any

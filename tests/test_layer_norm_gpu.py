@@ -143,6 +143,16 @@ def test_any_stride_and_alignment(dtype, stream, pad, shift):
         backward(6, N, dtype, stream, True, 0.1, pad, shift)
 
 
+@pytest.mark.parametrize("M,N", [(1, 9), (2048, 64), (2049, 64), (512, 250), (513, 250), (128, 510),
+                                 (129, 510), (64, 1000), (65, 1000), (40, 1530), (41, 1530),
+                                 (16, 4096), (17, 4096), (7, 8191), (8, 8192), (9, 8192)])
+def test_few_rows_joined_in_a_cluster(M, N):
+    """On either side of the rows up to which one cluster adds its blocks' column sums."""
+    backward(M, N, BF16, BF16, False, 0.0, wtype=BF16, dwtype=BF16)
+    backward(M, N, F16, F32, True, 0.1, outputs=("dX", "db"))
+    backward(M, N, F32, F32, True, 0.1, outputs=("dw",))
+
+
 @pytest.mark.parametrize("outputs", [("dS",), ("dX",), ("dw",), ("db",), ("dS", "db"),
                                      ("dX", "dw", "db")])
 def test_some_of_the_gradients(outputs):
