@@ -12,6 +12,8 @@
 // token's sum; the sums of a token that crosses a chunk's border go to the workspace, and a last
 // kernel adds them in order.  No atomics on sums.  32768 positions of 131072 x 4096 bf16: 208 us,
 // 1.34 GB at 6.5 TB/s, 21 us of it the sort.
+#include <mutex>
+
 #include "layers_host.h"
 
 namespace igc {
@@ -577,8 +579,25 @@ EmbedLayout layout(int64_t M, int64_t V, int64_t D) {
   return l;
 }
 
+// The sort's kernels may have their shared memory, on this device.
+int sort_setup(const DeviceInfo& dev) {
+  static std::once_flag once[64];
+  static int rc[64];
+  std::call_once(once[dev.device], [&] {
+    rc[dev.device] = IGC_OK;
+    for (auto kernel : {embed_count_kernel, embed_move_kernel}) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (kSortThreads / 32) * kMaxDigit * 4) != cudaSuccess) {
+        (void)cudaGetLastError();
+        rc[dev.device] = IGC_ERR_CUDA;
+      }
+    }
+  });
+  return rc[dev.device];
+}
+
 template <int kY, int kW>
-int run(EmbedParams p, cudaStream_t stream) {
+int run(const DeviceInfo& dev, EmbedParams p, cudaStream_t stream) {
   const long long zero_blocks = p.accumulate ? 0 : (p.V + p.zero_rows - 1) / p.zero_rows;
   p.zero_blocks = static_cast<unsigned>(zero_blocks);
   if (p.M <= kSmallM) {
@@ -595,16 +614,10 @@ int run(EmbedParams p, cudaStream_t stream) {
                                 ((static_cast<long long>(p.D) + 255) / 256);
   if (blocks > 0x7fffffff || join_blocks > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
   const int smem = (kSortThreads / 32) * (1 << p.digit_bits) * 4;
-  for (auto kernel : {embed_count_kernel, embed_move_kernel}) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (kSortThreads / 32) * kMaxDigit * 4) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return IGC_ERR_CUDA;
-    }
-  }
+  int rc = sort_setup(dev);
+  if (rc != IGC_OK) return rc;
   const int run = kSortThreads * p.sort_steps;
   const dim3 sort_grid(static_cast<unsigned>((p.M + static_cast<long long>(run) - 1) / run));
-  int rc = IGC_OK;
   for (int pass = 0; pass < p.passes; ++pass) {
     for (auto kernel : {embed_count_kernel, embed_move_kernel}) {
       rc = launch_pdl(kernel, sort_grid, dim3(kSortThreads), static_cast<size_t>(smem), stream, p,
@@ -681,12 +694,12 @@ int embedding_backward(int64_t M, int64_t V, int64_t D, const void* tokens, int 
   while ((static_cast<int64_t>(1) << bits) <= V) ++bits;  // keys are 0 .. V
   p.passes = (bits + 8) / 9;
   p.digit_bits = (bits + p.passes - 1) / p.passes;
-  if (y_dtype == IGC_F32) return run<IGC_F32, IGC_F32>(p, stream);
+  if (y_dtype == IGC_F32) return run<IGC_F32, IGC_F32>(dev, p, stream);
   if (y_dtype == IGC_F16)
-    return dw_dtype == IGC_F32 ? run<IGC_F16, IGC_F32>(p, stream)
-                               : run<IGC_F16, IGC_F16>(p, stream);
-  return dw_dtype == IGC_F32 ? run<IGC_BF16, IGC_F32>(p, stream)
-                             : run<IGC_BF16, IGC_BF16>(p, stream);
+    return dw_dtype == IGC_F32 ? run<IGC_F16, IGC_F32>(dev, p, stream)
+                               : run<IGC_F16, IGC_F16>(dev, p, stream);
+  return dw_dtype == IGC_F32 ? run<IGC_BF16, IGC_F32>(dev, p, stream)
+                             : run<IGC_BF16, IGC_BF16>(dev, p, stream);
 }
 
 }  // extern "C"

@@ -11,8 +11,6 @@
 // blocks' in order (no atomics).  16384 x 4096 bf16 with dropout and A: 106 us, 671 MB at 6.3 TB/s.
 #pragma once
 
-#include <mutex>
-
 #include "row_stream_host.h"
 
 namespace igc {
@@ -545,29 +543,22 @@ int stream_norm_bwd(const DeviceInfo& dev, NormBwdParams p, bool drop, int* bloc
   constexpr int kGroups = kNormBwdStreamMost / kLanes;
   auto kernel = drop ? layer_norm_bwd_stream_kernel<kT, kS, kLanes, kCluster, true>
                      : layer_norm_bwd_stream_kernel<kT, kS, kLanes, kCluster, false>;
-  int64_t most = dev.sm_count;
-  if constexpr (kCluster > 1) {
-    static std::once_flag once[64];
-    static int clusters[64];
-    std::call_once(once[dev.device], [&] {
-      clusters[dev.device] = stream_clusters(kernel, dev, kCluster, kGroups * kLanes);
-    });
-    most = clusters[dev.device];
-  }
+  static StreamSetup setup[2];
+  const int rc = stream_setup(setup[drop], kernel, dev, kCluster, kGroups * kLanes);
+  if (rc != IGC_OK) return rc;
   RowStream st;
   const int64_t cols = (p.N / 8 + kCluster - 1) / kCluster * 8;
   const int sizes[kStreamMats] = {static_cast<int>(elem_size(kT)), static_cast<int>(elem_size(kS)),
                                   p.A != nullptr ? static_cast<int>(elem_size(kS)) : 0};
-  *done = most > 0 && plan_stream(dev, cols, sizes, kGroups, &st);
+  *done = plan_stream(dev, cols, sizes, kGroups, &st);
   if (!*done) return IGC_OK;
   bool join = false;
-  *blocks = norm_bwd_blocks(p, kGroups, kGroups, most, kCluster == 1 ? &join : nullptr);
+  const int rows = norm_bwd_blocks(p, kGroups, kGroups, setup[drop].clusters[dev.device],
+                                   kCluster == 1 ? &join : nullptr);
   p.join = join;
-  const int rc = launch_stream(kernel, dev, *blocks * kCluster, join ? *blocks : kCluster,
-                               kGroups * kLanes, kGroups,
-                               static_cast<size_t>(kGroups) * (cols + 8) * 8, stream, p, st);
-  if (join) *blocks = 0;
-  return rc;
+  *blocks = join ? 0 : rows;
+  return launch_stream(kernel, rows * kCluster, join ? rows : kCluster, kGroups * kLanes, kGroups,
+                       static_cast<size_t>(kGroups) * (cols + 8) * 8, stream, p, st);
 }
 
 // *blocks: rows of partial sums that it leaves (0: it has written dw and db).
@@ -600,7 +591,7 @@ int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* 
     rc = stream_norm_bwd<kT, kS, 256, 4>(dev, p, drop, blocks, &done, stream);
   else if (units <= 4096)
     rc = stream_norm_bwd<kT, kS, 256, 8>(dev, p, drop, blocks, &done, stream);
-  if (done) return rc;
+  if (done || rc != IGC_OK) return rc;
   if (p.dS != nullptr || p.dX != nullptr) {
     const int rc = launch_pdl(drop ? layer_norm_bwd_any_kernel<kT, kS, true>
                                    : layer_norm_bwd_any_kernel<kT, kS, false>,

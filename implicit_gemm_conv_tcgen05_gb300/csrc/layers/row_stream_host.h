@@ -1,6 +1,8 @@
 // Host side of the rows streamed through shared memory: the ring's plan and its launch.
 #pragma once
 
+#include <mutex>
+
 #include "layers_host.h"
 #include "row_stream.cuh"
 
@@ -57,45 +59,53 @@ int launch_clusters(void (*kernel)(Params...), int blocks, int cluster, int thre
 
 // least: bytes of dynamic shared memory that the kernel uses whatever the ring takes.
 template <typename P>
-int launch_stream(void (*kernel)(P, RowStream), const DeviceInfo& dev, int blocks, int cluster,
+int launch_stream(void (*kernel)(P, RowStream), int blocks, int cluster,
                   int threads, int groups, size_t least, cudaStream_t stream, const P& p, const RowStream& s) {
-  // (the attribute belongs to the function: set by every call, which costs less than to look
-  // whether it is)
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(dev.smem_optin) - kStreamStatic) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return IGC_ERR_CUDA;
-  }
   const size_t bytes = static_cast<size_t>(2) * s.plane +
                        static_cast<size_t>(groups) * s.slots * s.slot_bytes;
   return launch_clusters(kernel, blocks, cluster, threads, bytes < least ? least : bytes, stream, p,
                          s);
 }
 
-// Clusters of `cluster` streaming blocks (one to an SM) that the device runs at once, of any
-// streaming kernel; 0 if that cannot be found out.
+// What a launch of a streaming kernel needs to know of it on a device, found out once.
+struct StreamSetup {
+  std::once_flag once[64];
+  int rc[64];
+  int clusters[64];  // clusters of streaming blocks (one to an SM) that the device runs at once
+};
+
 template <typename P>
-int stream_clusters(void (*kernel)(P, RowStream), const DeviceInfo& dev, int cluster,
-                    int threads) {
-  const int smem = static_cast<int>(dev.smem_optin) - kStreamStatic;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / cluster * cluster));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-          cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  return n;
+int stream_setup(StreamSetup& s, void (*kernel)(P, RowStream), const DeviceInfo& dev, int cluster,
+                 int threads) {
+  const int d = dev.device;
+  std::call_once(s.once[d], [&] {
+    const int smem = static_cast<int>(dev.smem_optin) - kStreamStatic;
+    s.rc[d] = IGC_ERR_CUDA;
+    s.clusters[d] = dev.sm_count;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return;
+    }
+    if (cluster > 1) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / cluster * cluster));
+      cfg.blockDim = dim3(static_cast<unsigned>(threads));
+      cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&s.clusters[d], kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return;
+      }
+    }
+    s.rc[d] = s.clusters[d] > 0 ? IGC_OK : IGC_ERR_UNSUPPORTED;
+  });
+  return s.rc[d];
 }
 
 }  // namespace igc
