@@ -10,9 +10,9 @@
 The branch of a block joins the residual stream inside the next block's layer_norm, which drops,
 adds and normalises in one pass; its backward pass sends the gradient on along the stream and,
 through the same dropout, into the branch.  No mask is stored: a step has an offset, each block a
-seed.  The stream is fp32, everything that feeds a product bf16.  The table's gradient is the sum of
-the output product's and the lookup's (embedding_backward with accumulate).  The stack learns to name the
-token that a fixed permutation sends each token to.
+seed.  The stream is fp32, everything that feeds a product bf16.  The table's gradient is the sum
+of the output product's and the lookup's (embedding_backward with accumulate).  The stack learns to
+name the token that a fixed permutation sends each token to.
 """
 
 import argparse

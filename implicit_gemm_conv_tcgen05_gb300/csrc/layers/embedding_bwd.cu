@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kSmallThreads, 4) embed_small_kernel(const Emb
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const uint32_t same = __ballot_sync(0xffffffffu, held[k] == v);
-    if (threadIdx.x % 32 == 0) bits[(k * kSmallThreads + static_cast<int>(threadIdx.x)) / 32] = same;
+    if (threadIdx.x % 32 == 0)
+      bits[(k * kSmallThreads + static_cast<int>(threadIdx.x)) / 32] = same;
   }
   __syncthreads();
   uint32_t earlier = 0;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kSmallThreads, 4) embed_small_kernel(const Emb
   const int sub = static_cast<int>(threadIdx.x) / kSmallUnits;
   const int n =
       (static_cast<int>((blockIdx.x - p.zero_blocks) % p.slabs) * kSmallUnits + unit) * 8;
-  // of the token's positions in order, each share has every kSmallSubs-th; it loads kSmallAhead rows
+  // of the token's positions in order, each share has every kSmallSubs-th; it loads a few rows
   // before it adds the first
   float acc[8] = {};
   int k = i / 32, count = 0;

@@ -3,9 +3,10 @@
 
 namespace igc {
 
-int layer_norm_bf16(const NormParams& p, int s_dtype, bool drop, cudaStream_t stream) {
-  return s_dtype == IGC_F32 ? run_norm<IGC_BF16, IGC_F32>(p, drop, stream)
-                            : run_norm<IGC_BF16, IGC_BF16>(p, drop, stream);
+int layer_norm_bf16(const DeviceInfo& dev, const NormParams& p, int s_dtype, bool drop,
+                    cudaStream_t stream) {
+  return s_dtype == IGC_F32 ? run_norm<IGC_BF16, IGC_F32>(dev, p, drop, stream)
+                            : run_norm<IGC_BF16, IGC_BF16>(dev, p, drop, stream);
 }
 
 }  // namespace igc

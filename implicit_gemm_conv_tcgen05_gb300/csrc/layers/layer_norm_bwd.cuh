@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
     walk_rows(std::false_type{});
   if (t == 0 && stopped >= 0)
     drain_slots(st, walk.bars, stopped, min(walk.count, stopped + st.slots));
-  if constexpr (kCluster > 1) cluster_sync();  // no block may exit before what is sent to it is there
+  // (no block may exit before what is sent to it is there)
+  if constexpr (kCluster > 1) cluster_sync();
   if (p.partial == nullptr) return;
   // one row of sums per block or cluster: the groups' go over their rings, and are added in order
   float* tot = reinterpret_cast<float*>(ring);

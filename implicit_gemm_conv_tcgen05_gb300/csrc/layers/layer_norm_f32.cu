@@ -3,8 +3,8 @@
 
 namespace igc {
 
-int layer_norm_f32(const NormParams& p, bool drop, cudaStream_t stream) {
-  return run_norm<IGC_F32, IGC_F32>(p, drop, stream);
+int layer_norm_f32(const DeviceInfo& dev, const NormParams& p, bool drop, cudaStream_t stream) {
+  return run_norm<IGC_F32, IGC_F32>(dev, p, drop, stream);
 }
 
 }  // namespace igc

@@ -35,8 +35,8 @@ enum : uint32_t { kSiteNormBwdRow = 0x4c01, kSiteNormBwdMeet = 0x4c02, kSiteRowD
 __device__ __forceinline__ void bulk_load(uint32_t dst_smem, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst_smem),
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1], %2, [%3];" ::"r"(dst_smem),
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
@@ -59,10 +59,10 @@ __device__ __forceinline__ void fill_slot(const RowStream& s, char* slot, uint64
 // Eight bytes into the shared memory of a block of the cluster, counted by a barrier there
 // (addresses in the cluster's shared window).
 __device__ __forceinline__ void store_async_u64(uint32_t to, uint64_t v, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
-                   to),
-               "l"(v), "r"(bar)
-               : "memory");
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(to),
+      "l"(v), "r"(bar)
+      : "memory");
 }
 
 // The whole block: the weights of its columns (whole units; fp32, or of type kT; 1 for none) into

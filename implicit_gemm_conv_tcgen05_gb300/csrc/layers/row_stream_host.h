@@ -59,8 +59,8 @@ int launch_clusters(void (*kernel)(Params...), int blocks, int cluster, int thre
 
 // least: bytes of dynamic shared memory that the kernel uses whatever the ring takes.
 template <typename P>
-int launch_stream(void (*kernel)(P, RowStream), int blocks, int cluster,
-                  int threads, int groups, size_t least, cudaStream_t stream, const P& p, const RowStream& s) {
+int launch_stream(void (*kernel)(P, RowStream), int blocks, int cluster, int threads, int groups,
+                  size_t least, cudaStream_t stream, const P& p, const RowStream& s) {
   const size_t bytes = static_cast<size_t>(2) * s.plane +
                        static_cast<size_t>(groups) * s.slots * s.slot_bytes;
   return launch_clusters(kernel, blocks, cluster, threads, bytes < least ? least : bytes, stream, p,

@@ -82,7 +82,7 @@ def test_mask_is_the_same_in_every_type_stride_and_operator():
 
 
 def test_in_place_and_the_gradient():
-    X, R = torch.randn(33, 400, device="cuda").bfloat16(), torch.randn(33, 400, device="cuda").bfloat16()
+    X, R = (torch.randn(33, 400, device="cuda").bfloat16() for _ in range(2))
     want = igc.dropout_add(X, 0.1, seed=2, residual=R)
     over = R.clone()
     assert igc.dropout_add(X, 0.1, seed=2, residual=over, Y=over) is over

@@ -69,8 +69,8 @@ def backward(M, N, dtype, stream, add, p, pad=None, shift=0, wtype=None, affine=
     if dX is not None:
         dx = ref.drop64(ds, p, SEED, OFFSET)
         scale = 65536 / max(ref.threshold(p), 1)
-        check(dX, dx, rounded(dx, dtype, torch.where(dx == 0, 0, err * scale + 3 * ref.E32 * dx.abs())),
-              "dX")
+        off = torch.where(dx == 0, 0, err * scale + 3 * ref.E32 * dx.abs())
+        check(dX, dx, rounded(dx, dtype, off), "dX")
         assert bool((around(dX) == 77.0).all())
     if dw is not None:
         check(dw, dw64, rounded(dw64, dwtype, ew), "dw")
@@ -325,8 +325,7 @@ def test_offsets_past_32_bits():
     A.copy_(vals[2])
     m, r = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
     y = igc.layer_norm(X, p=0.1, seed=1, S=S, mean=m, rstd=r)
-    dS, dXs = torch.empty(M, N, device="cuda", dtype=BF16), torch.empty(M, N, device="cuda", dtype=BF16)
-    Ss = torch.empty(M, N, device="cuda", dtype=BF16)
+    dS, dXs, Ss = (torch.empty(M, N, device="cuda", dtype=BF16) for _ in range(3))
     y2 = igc.layer_norm(vals[0], p=0.1, seed=1, S=Ss)
     assert torch.equal(y, y2) and torch.equal(S, Ss)
     igc.layer_norm_backward(vals[1], Ss, m, r, dS_add=vals[2], p=0.1, seed=1, dS=dS, dX=dXs)

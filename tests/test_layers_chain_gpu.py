@@ -43,7 +43,8 @@ def stack64(stack, leaves, tokens, offset):
     return h @ leaves["E"].t()
 
 
-@pytest.mark.parametrize("M,V,width,hidden,blocks", [(300, 200, 136, 264, 2), (1500, 1000, 256, 512, 1)])
+@pytest.mark.parametrize("M,V,width,hidden,blocks", [(300, 200, 136, 264, 2),
+                                                     (1500, 1000, 256, 512, 1)])
 def test_gradients_of_the_stack(example, M, V, width, hidden, blocks):
     gen = generator(M, V)
     stack = example.Stack(V, width, hidden, blocks, gen)
