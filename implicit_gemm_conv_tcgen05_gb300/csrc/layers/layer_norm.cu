@@ -40,7 +40,11 @@ extern "C" int layer_norm(int64_t M, int64_t N, int dtype, const void* X, int64_
   a.ldx = ldx, a.ldr = ldr, a.lds = lds, a.ldy = ldy;
   a.w = w, a.b = b, a.mean = mean, a.rstd = rstd, a.eps = eps;
   active = active && X != nullptr;
+  const bool wide = s_dtype == IGC_F32;
   if (dtype == IGC_F32) return layer_norm_f32(dev, a, active, stream);
-  return dtype == IGC_F16 ? layer_norm_f16(dev, a, s_dtype, active, stream)
-                          : layer_norm_bf16(dev, a, s_dtype, active, stream);
+  if (dtype == IGC_F16)
+    return wide ? layer_norm_f16_f32(dev, a, active, stream)
+                : layer_norm_f16(dev, a, active, stream);
+  return wide ? layer_norm_bf16_f32(dev, a, active, stream)
+              : layer_norm_bf16(dev, a, active, stream);
 }

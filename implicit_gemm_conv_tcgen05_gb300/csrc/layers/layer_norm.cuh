@@ -87,8 +87,15 @@ __device__ __forceinline__ void joined8(const NormParams& p, uint64_t offset, lo
                                         bool vec, float (&s)[8]) {
   Raw8<kT> x;
   Raw8<kS> r;
-  if (p.X != nullptr) x = load8<kT>(row_at<kT>(p.X, row, p.ldx), n, p.N, vec);
-  if (p.R != nullptr) r = load8<kS>(row_at<kS>(p.R, row, p.ldr), n, p.N, vec);
+  const char* x_row = row_at<kT>(p.X, row, p.ldx);
+  const char* r_row = row_at<kS>(p.R, row, p.ldr);
+  if (vec) {
+    if (p.X != nullptr) x = load8<kT>(x_row, n, p.N, true);
+    if (p.R != nullptr) r = load8<kS>(r_row, n, p.N, true);
+  } else {
+    if (p.X != nullptr) x = load8_shifted<kT>(x_row, n, p.N);
+    if (p.R != nullptr) r = load8_shifted<kS>(r_row, n, p.N);
+  }
   join8<kT, kS, kDrop>(p, offset, row, n, x, r, s);
 }
 
@@ -98,10 +105,54 @@ __device__ __forceinline__ float rsqrt_step(float x) {
   return y > 0.0f && y < INFINITY ? fmaf(0.5f * y, fmaf(-x * y, y, 1.0f), y) : y;
 }
 
+// Rows off 16-byte boundaries (load8_shifted, store8_warp), one to a block, four units to a thread.
+template <int kT, int kS, int kLanes, bool kDrop>
+__global__ void __launch_bounds__(kLanes) layer_norm_shifted_kernel(const NormParams p) {
+  constexpr int kUnits = 4;
+  __shared__ __align__(16) float red[2][kLanes / 32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long row = blockIdx.x;
+  const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
+  const float inv = 1.0f / static_cast<float>(p.N);
+  const int n0 = static_cast<int>(threadIdx.x) * 8;
+  float s[kUnits][8] = {};
+  uint64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    if (n0 + i * kLanes * 8 >= p.N) continue;
+    joined8<kT, kS, kDrop>(p, offset, row, n0 + i * kLanes * 8, false, s[i]);
+    total = add2(total, add2(add2(pair(s[i][0], s[i][1]), pair(s[i][2], s[i][3])),
+                             add2(pair(s[i][4], s[i][5]), pair(s[i][6], s[i][7]))));
+  }
+  const float mean = row_sum<kLanes>(sum2(total), red[0]) * inv;
+  float squares = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int n = n0 + i * kLanes * 8;
+    if (p.S != nullptr)
+      store8_warp<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, false, n < p.N, s[i]);
+    if (n < p.N) squares += center8(s[i], mean, n, p.N);
+  }
+  const float var = row_sum<kLanes>(squares, red[1]) * inv;
+  const float rstd = rsqrt_step(var + p.eps);
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int n = n0 + i * kLanes * 8;
+    if (n < p.N) affine8<kT>(p, rstd, n, s[i]);
+    store8_warp<kT>(row_at<kT>(p.Y, row, p.ldy), n, p.N, false, n < p.N, s[i]);
+  }
+  if (threadIdx.x == 0) {
+    if (p.mean != nullptr) p.mean[row] = mean;
+    if (p.rstd != nullptr) p.rstd[row] = rstd;
+  }
+}
+
 // Rows of any length and alignment: S is formed again for each of the three passes.  (S may be
 // R: it is stored in the last.)
-template <int kT, int kS, int kThreads, bool kDrop>
-__global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(const NormParams p) {
+template <int kT, int kS, bool kDrop>
+__global__ void __launch_bounds__(1024) layer_norm_any_kernel(const NormParams p) {
+  constexpr int kThreads = 1024;
   __shared__ __align__(16) float red[2][kThreads / 32];
   grid_dependency_wait();
   grid_dependents_launch();
@@ -121,13 +172,17 @@ __global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(const NormPara
   }
   const float var = row_sum<kThreads>(sum, red[1]) / static_cast<float>(p.N);
   const float rstd = rsqrt_step(var + p.eps);
-  for (long long m = threadIdx.x * 8; m < p.N; m += kThreads * 8) {
-    const int n = static_cast<int>(m);
-    joined8<kT, kS, kDrop>(p, offset, row, n, vec, s);
-    if (p.S != nullptr) store8<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec, s);
-    (void)center8(s, mean, n, p.N);
-    affine8<kT>(p, rstd, n, s);
-    store8<kT>(row_at<kT>(p.Y, row, p.ldy), n, p.N, vec, s);
+  // (the lanes of a warp stay together for the stores)
+  for (long long m = threadIdx.x / 32 * 256; m < p.N; m += kThreads * 8) {
+    const int n = static_cast<int>(m) + static_cast<int>(threadIdx.x) % 32 * 8;
+    const bool there = n < p.N;
+    if (there) joined8<kT, kS, kDrop>(p, offset, row, n, vec, s);
+    if (p.S != nullptr) store8_warp<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec, there, s);
+    if (there) {
+      (void)center8(s, mean, n, p.N);
+      affine8<kT>(p, rstd, n, s);
+    }
+    store8_warp<kT>(row_at<kT>(p.Y, row, p.ldy), n, p.N, vec, there, s);
   }
   if (threadIdx.x == 0) {
     if (p.mean != nullptr) p.mean[row] = mean;
@@ -305,19 +360,28 @@ int run_norm(const DeviceInfo& dev, const NormParams& p, bool drop, cudaStream_t
   }
   const dim3 grid(static_cast<unsigned>(p.M));
   if (units <= 512)
-    return launch_pdl(drop ? layer_norm_any_kernel<kT, kS, 128, true>
-                           : layer_norm_any_kernel<kT, kS, 128, false>,
+    return launch_pdl(drop ? layer_norm_shifted_kernel<kT, kS, 128, true>
+                           : layer_norm_shifted_kernel<kT, kS, 128, false>,
                       grid, dim3(128), 0, stream, p);
-  return launch_pdl(drop ? layer_norm_any_kernel<kT, kS, 1024, true>
-                         : layer_norm_any_kernel<kT, kS, 1024, false>,
+  if (units <= 1024)
+    return launch_pdl(drop ? layer_norm_shifted_kernel<kT, kS, 256, true>
+                           : layer_norm_shifted_kernel<kT, kS, 256, false>,
+                      grid, dim3(256), 0, stream, p);
+  if (units <= 2048)
+    return launch_pdl(drop ? layer_norm_shifted_kernel<kT, kS, 512, true>
+                           : layer_norm_shifted_kernel<kT, kS, 512, false>,
+                      grid, dim3(512), 0, stream, p);
+  return launch_pdl(drop ? layer_norm_any_kernel<kT, kS, true>
+                         : layer_norm_any_kernel<kT, kS, false>,
                     grid, dim3(1024), 0, stream, p);
 }
 
-// By type (layer_norm_f32.cu, layer_norm_f16.cu, layer_norm_bf16.cu).
+// By type of X and of the residual stream (a file each: they compile side by side).
 int layer_norm_f32(const DeviceInfo& dev, const NormParams& p, bool drop, cudaStream_t stream);
-int layer_norm_f16(const DeviceInfo& dev, const NormParams& p, int s_dtype, bool drop,
-                   cudaStream_t stream);
-int layer_norm_bf16(const DeviceInfo& dev, const NormParams& p, int s_dtype, bool drop,
-                    cudaStream_t stream);
+int layer_norm_f16(const DeviceInfo& dev, const NormParams& p, bool drop, cudaStream_t stream);
+int layer_norm_f16_f32(const DeviceInfo& dev, const NormParams& p, bool drop, cudaStream_t stream);
+int layer_norm_bf16(const DeviceInfo& dev, const NormParams& p, bool drop, cudaStream_t stream);
+int layer_norm_bf16_f32(const DeviceInfo& dev, const NormParams& p, bool drop,
+                        cudaStream_t stream);
 
 }  // namespace igc

@@ -100,12 +100,15 @@ int layer_norm_backward(int64_t M, int64_t N, int dtype, const void* dY, int64_t
     a.partial = sums ? static_cast<float*>(workspace) : nullptr;
     a.dw = dw, a.db = db, a.dw_f32 = dw_dtype == IGC_F32;
     active = active && dX != nullptr;
+    const bool wide = s_dtype == IGC_F32;
     if (dtype == IGC_F32)
       rc = layer_norm_bwd_f32(dev, a, active, &blocks, stream);
     else if (dtype == IGC_F16)
-      rc = layer_norm_bwd_f16(dev, a, s_dtype, active, &blocks, stream);
+      rc = wide ? layer_norm_bwd_f16_f32(dev, a, active, &blocks, stream)
+                : layer_norm_bwd_f16(dev, a, active, &blocks, stream);
     else
-      rc = layer_norm_bwd_bf16(dev, a, s_dtype, active, &blocks, stream);
+      rc = wide ? layer_norm_bwd_bf16_f32(dev, a, active, &blocks, stream)
+                : layer_norm_bwd_bf16(dev, a, active, &blocks, stream);
     if (rc != IGC_OK) return rc;
   }
   if (!sums || (M > 0 && blocks == 0)) return IGC_OK;

@@ -39,25 +39,18 @@ constexpr int kJoinBlocks = 8;
 
 constexpr int kMaxPartials = 512;  // rows of partial sums that the workspace has room for
 
-// dS and dX of eight columns from g, h and the row's sums; ds_row and dx_row are where the
-// row's dS and dX start.
-template <int kT, int kS, bool kDrop>
-__device__ __forceinline__ void grads8(const NormBwdParams& p, uint64_t offset, long long row,
-                                       char* ds_row, char* dx_row, int n, bool vec, float rstd,
-                                       float c1, float c2, const Raw8<kS>& a, const float (&g)[8],
-                                       const float (&h)[8]) {
-  float d[8], f[8] = {};
+// dS of eight columns from g, h and the row's sums.
+template <int kS>
+__device__ __forceinline__ void slopes8(const NormBwdParams& p, float rstd, float c1, float c2,
+                                        const Raw8<kS>& a, const float (&g)[8],
+                                        const float (&h)[8], float (&d)[8]) {
+  float f[8] = {};
   if (p.A != nullptr) unpack8<kS>(a, f);
   const uint64_t r = pair(rstd, rstd), m1 = pair(-c1, -c1), m2 = pair(-c2, -c2);
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const uint64_t x = fma2(pair(h[j], h[j + 1]), m2, add2(pair(g[j], g[j + 1]), m1));
     unpair(fma2(x, r, pair(f[j], f[j + 1])), d[j], d[j + 1]);
-  }
-  if (p.dS != nullptr) store8<kS>(ds_row, n, p.N, vec, d);
-  if (p.dX != nullptr) {
-    if constexpr (kDrop) drop8(p.drop, drop_bits(p.drop, offset, row, n), d);
-    store8<kT>(dx_row, n, p.N, vec, d);
   }
 }
 
@@ -351,9 +344,9 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
 }
 
 // Rows of any length and alignment, without the column sums: the row is read twice.
-template <int kT, int kS, bool kDrop>
-__global__ void __launch_bounds__(512) layer_norm_bwd_any_kernel(const NormBwdParams p) {
-  __shared__ __align__(16) float2 red[16];
+template <int kT, int kS, int kThreads, bool kDrop>
+__global__ void __launch_bounds__(kThreads) layer_norm_bwd_any_kernel(const NormBwdParams p) {
+  __shared__ __align__(16) float2 red[kThreads / 32];
   grid_dependency_wait();
   grid_dependents_launch();
   const long long row = blockIdx.x;
@@ -361,31 +354,46 @@ __global__ void __launch_bounds__(512) layer_norm_bwd_any_kernel(const NormBwdPa
   const uint64_t offset = kDrop ? drop_offset(p.drop) : 0;
   const float mean = p.mean[row], rstd = p.rstd[row];
   uint64_t p1 = 0, p2 = 0;
-  float g[8], h[8], none[8];
+  float g[8] = {}, h[8] = {}, none[8];
+  auto load = [&](auto type, const char* at, int n) {
+    constexpr int kType = decltype(type)::value;
+    return vec ? load8<kType>(at, n, p.N, true) : load8_shifted<kType>(at, n, p.N);
+  };
+  using T = std::integral_constant<int, kT>;
+  using S = std::integral_constant<int, kS>;
   auto terms = [&](int n) {
-    const Raw8<kT> y = load8<kT>(row_at<kT>(p.dY, row, p.lddy), n, p.N, vec);
-    const Raw8<kS> s = load8<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec);
     float w[8];
     load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, w);
-    unpack8<kT>(y, g);
-    unpack8<kS>(s, h);
+    unpack8<kT>(load(T{}, row_at<kT>(p.dY, row, p.lddy), n), g);
+    unpack8<kS>(load(S{}, row_at<kS>(p.S, row, p.lds), n), h);
     terms8<false>(mean, rstd, w, g, h, p1, p2, none, none);
   };
-  for (long long n = threadIdx.x * 8; n < p.N; n += 512 * 8) terms(static_cast<int>(n));
+  for (long long n = threadIdx.x * 8; n < p.N; n += kThreads * 8) terms(static_cast<int>(n));
   float c1 = sum2(p1), c2 = sum2(p2);
   const float inv = 1.0f / static_cast<float>(p.N);
-  leave_sums<512>(c1, c2, red);
+  leave_sums<kThreads>(c1, c2, red);
   __syncthreads();
-  take_sums<512>(c1, c2, red);
+  take_sums<kThreads>(c1, c2, red);
   c1 *= inv;
   c2 *= inv;
-  for (long long m = threadIdx.x * 8; m < p.N; m += 512 * 8) {
-    const int n = static_cast<int>(m);
-    terms(n);
+  char* ds_row = row_at<kS>(p.dS, row, p.ldds);
+  char* dx_row = row_at<kT>(p.dX, row, p.lddx);
+  // (the lanes of a warp stay together for the stores)
+  for (long long m = threadIdx.x / 32 * 256; m < p.N; m += kThreads * 8) {
+    const int n = static_cast<int>(m) + static_cast<int>(threadIdx.x) % 32 * 8;
+    const bool there = n < p.N;
     Raw8<kS> a = {};
-    if (p.A != nullptr) a = load8<kS>(row_at<kS>(p.A, row, p.lda), n, p.N, vec);
-    grads8<kT, kS, kDrop>(p, offset, row, row_at<kS>(p.dS, row, p.ldds),
-                          row_at<kT>(p.dX, row, p.lddx), n, vec, rstd, c1, c2, a, g, h);
+    if (there) {
+      terms(n);
+      if (p.A != nullptr) a = load(S{}, row_at<kS>(p.A, row, p.lda), n);
+    }
+    float d[8];
+    slopes8<kS>(p, rstd, c1, c2, a, g, h, d);
+    if (p.dS != nullptr) store8_warp<kS>(ds_row, n, p.N, vec, there, d);
+    if (p.dX != nullptr) {
+      if constexpr (kDrop) drop8(p.drop, drop_bits(p.drop, offset, row, n), d);
+      store8_warp<kT>(dx_row, n, p.N, vec, there, d);
+    }
   }
 }
 
@@ -407,8 +415,10 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const NormBwdPa
     const int n = static_cast<int>(n0);
 #pragma unroll 4
     for (long long row = r0 + sub; row < r1; row += 8) {
-      const Raw8<kT> y = load8<kT>(row_at<kT>(p.dY, row, p.lddy), n, p.N, vec);
-      const Raw8<kS> s = load8<kS>(row_at<kS>(p.S, row, p.lds), n, p.N, vec);
+      const char* y_row = row_at<kT>(p.dY, row, p.lddy);
+      const char* s_row = row_at<kS>(p.S, row, p.lds);
+      const Raw8<kT> y = vec ? load8<kT>(y_row, n, p.N, true) : load8_shifted<kT>(y_row, n, p.N);
+      const Raw8<kS> s = vec ? load8<kS>(s_row, n, p.N, true) : load8_shifted<kS>(s_row, n, p.N);
       const float mean = p.mean[row], rstd = p.rstd[row];
       float g[8], h[8];
       unpack8<kT>(y, g);
@@ -483,10 +493,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       terms8<true>(mean[r], rstd[r], w, g, h, p1, p2, sw, sb);
       float c1 = sum2(p1), c2 = sum2(p2);
       lane_sums<kLanes>(c1, c2);
-      if (row < p.M && n < p.N)
-        grads8<kT, kS, kDrop>(p, offset, row, row_at<kS>(p.dS, row, p.ldds),
-                              row_at<kT>(p.dX, row, p.lddx), n, vec, rstd[r], c1 * inv, c2 * inv,
-                              a[r], g, h);
+      if (row >= p.M || n >= p.N) continue;
+      float d[8];
+      slopes8<kS>(p, rstd[r], c1 * inv, c2 * inv, a[r], g, h, d);
+      if (p.dS != nullptr) store8<kS>(row_at<kS>(p.dS, row, p.ldds), n, p.N, vec, d);
+      if (p.dX != nullptr) {
+        if constexpr (kDrop) drop8(p.drop, drop_bits(p.drop, offset, row, n), d);
+        store8<kT>(row_at<kT>(p.dX, row, p.lddx), n, p.N, vec, d);
+      }
     }
   }
   if (p.partial == nullptr) return;
@@ -594,9 +608,13 @@ int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* 
     rc = stream_norm_bwd<kT, kS, 256, 8>(dev, p, drop, blocks, &done, stream);
   if (done || rc != IGC_OK) return rc;
   if (p.dS != nullptr || p.dX != nullptr) {
-    const int rc = launch_pdl(drop ? layer_norm_bwd_any_kernel<kT, kS, true>
-                                   : layer_norm_bwd_any_kernel<kT, kS, false>,
-                              dim3(static_cast<unsigned>(p.M)), dim3(512), 0, stream, p);
+    const dim3 grid(static_cast<unsigned>(p.M));
+    rc = units <= 1024 ? launch_pdl(drop ? layer_norm_bwd_any_kernel<kT, kS, 128, true>
+                                         : layer_norm_bwd_any_kernel<kT, kS, 128, false>,
+                                    grid, dim3(128), 0, stream, p)
+                       : launch_pdl(drop ? layer_norm_bwd_any_kernel<kT, kS, 512, true>
+                                         : layer_norm_bwd_any_kernel<kT, kS, 512, false>,
+                                    grid, dim3(512), 0, stream, p);
     if (rc != IGC_OK) return rc;
   }
   if (p.partial == nullptr) return IGC_OK;
@@ -611,12 +629,16 @@ int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* 
                     dim3(256), 0, stream, p, static_cast<int>(rows));
 }
 
-// By type (layer_norm_bwd_f32.cu, layer_norm_bwd_f16.cu, layer_norm_bwd_bf16.cu).
+// By type of dY and of the residual stream (a file each: they compile side by side).
 int layer_norm_bwd_f32(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
                        cudaStream_t stream);
-int layer_norm_bwd_f16(const DeviceInfo& dev, const NormBwdParams& p, int s_dtype, bool drop,
-                       int* blocks, cudaStream_t stream);
-int layer_norm_bwd_bf16(const DeviceInfo& dev, const NormBwdParams& p, int s_dtype, bool drop,
-                        int* blocks, cudaStream_t stream);
+int layer_norm_bwd_f16(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
+                       cudaStream_t stream);
+int layer_norm_bwd_f16_f32(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
+                           cudaStream_t stream);
+int layer_norm_bwd_bf16(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
+                        cudaStream_t stream);
+int layer_norm_bwd_bf16_f32(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* blocks,
+                            cudaStream_t stream);
 
 }  // namespace igc

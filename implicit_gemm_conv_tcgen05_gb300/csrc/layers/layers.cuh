@@ -133,6 +133,112 @@ __device__ __forceinline__ void store1(char* row, int n, float v) {
     store16(row, n, v, kT == IGC_BF16);
 }
 
+// w moved up by `bytes` (a multiple of 4, less than 16) of its kN words: what lies past its end is
+// undefined.
+template <int kN>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[kN], uint32_t bytes) {
+#pragma unroll
+  for (int i = 0; i + 2 < kN; ++i) w[i] = bytes & 8u ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i + 1 < kN; ++i) w[i] = bytes & 4u ? w[i + 1] : w[i];
+}
+
+// load8 for a row off 16-byte boundaries: the 16-byte pieces that hold the unit, where they lie
+// within the row, are loaded and shifted into place (what neighbours hold in them is not used);
+// the units at the ends of a row are loaded one by one.  (Of use where a kernel has few registers
+// to lose: beside the other loads of the dropout and the lookup it made their aligned rows slower
+// by a sixth to a quarter, and rows off boundaries no faster.)
+template <int kT>
+__device__ __forceinline__ Raw8<kT> load8_shifted(const char* row, int n, int N) {
+  if (n < 8 || n > N - 16) return load8<kT>(row, n, N, false);
+  constexpr int kPieces = kT == IGC_F32 ? 3 : 2;
+  const char* at = row + static_cast<long long>(n) * (kT == IGC_F32 ? 4 : 2);
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
+  const uint4* p = reinterpret_cast<const uint4*>(at - off);
+  uint32_t w[4 * kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const uint4 q = p[i];
+    w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+  }
+  shift_words(w, off);
+  Raw8<kT> r;
+  if constexpr (kT == IGC_F32) {
+    r.q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    r.q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    const uint32_t s = (off & 3u) * 8u;
+    r.q[0] = make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
+                        __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+  }
+  return r;
+}
+
+// store8 by a whole warp whose lanes hold adjacent units of a row.  `there`: whether the lane has
+// one.  Rows off 16-byte boundaries are written in aligned 16-byte pieces all the same: a lane writes
+// the piece that its unit begins in, together with what the lane before it has of that piece.
+template <int kT>
+__device__ __forceinline__ void store8_warp(char* row, int n, int N, bool vec, bool there,
+                                            const float (&v)[8]) {
+  if (vec) {
+    if (there) store8<kT>(row, n, N, true, v);
+    return;
+  }
+  constexpr int kSize = kT == IGC_F32 ? 4 : 2, kWords = 2 * kSize;
+  uint32_t w[kWords + 4];  // the last 16 bytes of the lane before, then this lane's
+  if constexpr (kT == IGC_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[4 + i] = __float_as_uint(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[4 + i] = pack16(v[2 * i], v[2 * i + 1], kT == IGC_BF16);
+  }
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, w[kWords + i], 1);
+  const bool whole = there && n + 8 <= N;
+  const uint32_t wholes = __ballot_sync(0xffffffffu, whole);
+  if (!there) return;
+  if (!whole) {
+    store8<kT>(row, n, N, false, v);
+    return;
+  }
+  char* at = row + static_cast<long long>(n) * kSize;
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
+  if (off == 0) {
+    store_unit<kT>(at, v);
+    return;
+  }
+  const bool before = lane > 0 && (wholes >> (lane - 1) & 1u);
+  const bool after = lane < 31 && (wholes >> (lane + 1) & 1u);
+  const uint32_t from = 16u - off;  // bytes of this lane in the piece that it begins in
+  if (!before || !after) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool first = static_cast<uint32_t>(i * kSize) < from;
+      // (an fp32 unit has a whole piece between its ends)
+      const bool last = static_cast<uint32_t>(i * kSize) >= 8 * kSize - off;
+      if ((first && !before) || (last && !after)) {
+        if constexpr (kT == IGC_F32)
+          reinterpret_cast<float*>(at)[i] = v[i];
+        else
+          store16(at, i, v[i], kT == IGC_BF16);
+      }
+    }
+  }
+  shift_words(w, from);
+  uint4* to = reinterpret_cast<uint4*>(at - off);
+  if constexpr (kT == IGC_F32) {
+    if (before) to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    const uint32_t s = (from & 3u) * 8u;
+    if (before)
+      to[0] = make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
+                         __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
+  }
+}
+
 // Elements [n, n + 8) of a vector of N that is fp32 (f32) or of type kT; `none` for no vector
 // and past its end.  (Vectors may start anywhere: 16-byte loads where they can.)
 template <int kT>
