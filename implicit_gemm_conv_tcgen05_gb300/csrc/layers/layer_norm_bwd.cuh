@@ -115,13 +115,15 @@ __device__ __forceinline__ void terms8(float mean, float rstd, const float (&w)[
 
 constexpr int kNormBwdStreamMost = 512;  // 128 registers each
 
-// Rows streamed through shared memory (row_stream.cuh), two units to a thread.  Rows of more
-// columns than a block has are shared by the kCluster blocks of a cluster, which exchange their
-// sums through distributed shared memory.
-template <int kT, int kS, int kLanes, int kCluster, bool kDrop>
+// Rows streamed through shared memory (row_stream.cuh), two or three units to a thread (three:
+// dY and S are taken from the slot again after the sums, their registers go to the column sums).
+// Rows of more columns than a block has are shared by the kCluster blocks of a cluster, which
+// exchange their sums through distributed shared memory.
+template <int kT, int kS, int kLanes, int kUnits, int kCluster, bool kDrop>
 __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
     layer_norm_bwd_stream_kernel(const NormBwdParams p, const RowStream st) {
-  constexpr int kGroups = kNormBwdStreamMost / kLanes, kUnits = 2;
+  constexpr int kGroups = kNormBwdStreamMost / kLanes;
+  constexpr bool kAgain = kUnits > 2;  // g and h are formed again after the sums
   constexpr int kSizeT = kT == IGC_F32 ? 4 : 2, kSizeS = kS == IGC_F32 ? 4 : 2;
   extern __shared__ __align__(128) char ring[];
   __shared__ uint64_t full[kGroups][kMaxSlots];
@@ -202,17 +204,17 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       if (!mbar_wait(walk.bars + slot, phase, st.wait_limit, &abort_flag, st.status,
                      kSiteNormBwdRow) && stopped < 0)
         stopped = k;
-      float g[kUnits][8], h[kUnits][8];
+      float g[kAgain ? 1 : kUnits][8], h[kAgain ? 1 : kUnits][8];
       uint64_t p1 = 0, p2 = 0;
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const int n = (i * kLanes + t) * 8;
+        const int n = (i * kLanes + t) * 8, q = kAgain ? 0 : i;
         if (!decltype(whole)::value && n >= cols) continue;
         float wv[8];
         kept_weights(ring, st.plane, n, wv);
-        load_unit<kT>(at + st.at[0] + n * kSizeT, g[i]);
-        load_unit<kS>(at + st.at[1] + n * kSizeS, h[i]);
-        terms8<true>(mean, rstd, wv, g[i], h[i], p1, p2, sw[i], sb[i]);
+        load_unit<kT>(at + st.at[0] + n * kSizeT, g[q]);
+        load_unit<kS>(at + st.at[1] + n * kSizeS, h[q]);
+        terms8<true>(mean, rstd, wv, g[q], h[q], p1, p2, sw[i], sb[i]);
       }
       float c1 = sum2(p1), c2 = sum2(p2), g_last = 0.0f, h_last = 0.0f, f_last = a_last;
       if (last >= 0) {
@@ -225,8 +227,8 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
         if (k + 1 < walk.count) load_last(row + walk.step);
       }
       // the bits of the dropout are made here, among the shuffles of the sums
-      [[maybe_unused]] uint4 bits[kDrop ? kUnits : 1];
-      if constexpr (kDrop) {
+      [[maybe_unused]] uint4 bits[kDrop && !kAgain ? kUnits : 1];
+      if constexpr (kDrop && !kAgain) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
           bits[i] = drop_bits(p.drop, offset, row, col0 + (i * kLanes + t) * 8);
@@ -265,19 +267,28 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       const uint64_t r2 = pair(rstd, rstd), m1 = pair(-c1, -c1), m2 = pair(-c2, -c2);
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const int n = (i * kLanes + t) * 8;
+        const int n = (i * kLanes + t) * 8, q = kAgain ? 0 : i;
         if (!decltype(whole)::value && n >= cols) continue;
+        if constexpr (kAgain) {
+          float wv[8], none[8];
+          kept_weights(ring, st.plane, n, wv);
+          load_unit<kT>(at + st.at[0] + n * kSizeT, g[q]);
+          load_unit<kS>(at + st.at[1] + n * kSizeS, h[q]);
+          terms8<false>(mean, rstd, wv, g[q], h[q], p1, p2, none, none);
+        }
         float d[8], f[8] = {};
         if (has_a) load_unit<kS>(at + st.at[2] + n * kSizeS, f);
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const uint64_t x =
-              fma2(pair(h[i][j], h[i][j + 1]), m2, add2(pair(g[i][j], g[i][j + 1]), m1));
+              fma2(pair(h[q][j], h[q][j + 1]), m2, add2(pair(g[q][j], g[q][j + 1]), m1));
           unpair(fma2(x, r2, pair(f[j], f[j + 1])), d[j], d[j + 1]);
         }
         if (has_s) store_unit<kS>(ds_row + n * kSizeS, d);
         if (has_x) {
-          if constexpr (kDrop) drop8(p.drop, bits[i], d);
+          if constexpr (kDrop)
+            drop8(p.drop,
+                  kAgain ? drop_bits(p.drop, offset, row, col0 + n) : bits[kAgain ? 0 : i], d);
           store_unit<kT>(dx_row + n * kSizeT, d);
         }
       }
@@ -552,12 +563,12 @@ int launch_narrow(const DeviceInfo& dev, NormBwdParams p, bool drop, int* blocks
 }
 
 // *done: whether a block's shared memory holds two rows of every group.
-template <int kT, int kS, int kLanes, int kCluster>
+template <int kT, int kS, int kLanes, int kUnits, int kCluster>
 int stream_norm_bwd(const DeviceInfo& dev, NormBwdParams p, bool drop, int* blocks, bool* done,
                     cudaStream_t stream) {
   constexpr int kGroups = kNormBwdStreamMost / kLanes;
-  auto kernel = drop ? layer_norm_bwd_stream_kernel<kT, kS, kLanes, kCluster, true>
-                     : layer_norm_bwd_stream_kernel<kT, kS, kLanes, kCluster, false>;
+  auto kernel = drop ? layer_norm_bwd_stream_kernel<kT, kS, kLanes, kUnits, kCluster, true>
+                     : layer_norm_bwd_stream_kernel<kT, kS, kLanes, kUnits, kCluster, false>;
   static StreamSetup setup[2];
   const int rc = stream_setup(setup[drop], kernel, dev, kCluster, kGroups * kLanes);
   if (rc != IGC_OK) return rc;
@@ -589,23 +600,34 @@ int run_norm_bwd(const DeviceInfo& dev, const NormBwdParams& p, bool drop, int* 
   if (!p.vec)
     done = false;
   else if (units <= 64)
-    rc = stream_norm_bwd<kT, kS, 32, 1>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 32, 2, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 128)
-    rc = stream_norm_bwd<kT, kS, 64, 1>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 64, 2, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 192)  // (32768 x 1536 bf16: five rows at once, 88 us; four of 128 threads 108)
-    rc = stream_norm_bwd<kT, kS, 96, 1>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 96, 2, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 256)
-    rc = stream_norm_bwd<kT, kS, 128, 1>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 128, 2, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 320)  // (16384 x 2500: three at once, 93 us; two of 256 threads 125)
-    rc = stream_norm_bwd<kT, kS, 160, 1>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 160, 2, 1>(dev, p, drop, blocks, &done, stream);
   else if (units <= 512)
-    rc = stream_norm_bwd<kT, kS, 256, 1>(dev, p, drop, blocks, &done, stream);
-  else if (units <= 1024)
-    rc = stream_norm_bwd<kT, kS, 512, 1>(dev, p, drop, blocks, &done, stream);
-  else if (units <= 2048)
-    rc = stream_norm_bwd<kT, kS, 256, 4>(dev, p, drop, blocks, &done, stream);
-  else if (units <= 4096)
-    rc = stream_norm_bwd<kT, kS, 256, 8>(dev, p, drop, blocks, &done, stream);
+    rc = stream_norm_bwd<kT, kS, 256, 2, 1>(dev, p, drop, blocks, &done, stream);
+  // Three units to a thread where two rows at once then fit a block's or cluster's shared memory
+  // and a wider form would leave a quarter of its threads without work (8192 x 6000: 94 us, one row
+  // of 512 threads 108; 4096 x 12000: 102, clusters of four 125).
+  else if (units <= 768)
+    rc = stream_norm_bwd<kT, kS, 256, 3, 1>(dev, p, drop, blocks, &done, stream);
+  else if (units > 1024 && units <= 1536)
+    rc = stream_norm_bwd<kT, kS, 256, 3, 2>(dev, p, drop, blocks, &done, stream);
+  else if (units > 2048 && units <= 12 * 256)
+    rc = stream_norm_bwd<kT, kS, 256, 3, 4>(dev, p, drop, blocks, &done, stream);
+  if (p.vec && !done && rc == IGC_OK && units > 512) {
+    if (units <= 1024)
+      rc = stream_norm_bwd<kT, kS, 512, 2, 1>(dev, p, drop, blocks, &done, stream);
+    else if (units <= 2048)
+      rc = stream_norm_bwd<kT, kS, 256, 2, 4>(dev, p, drop, blocks, &done, stream);
+    else if (units <= 4096)
+      rc = stream_norm_bwd<kT, kS, 256, 2, 8>(dev, p, drop, blocks, &done, stream);
+  }
   if (done || rc != IGC_OK) return rc;
   if (p.dS != nullptr || p.dX != nullptr) {
     const dim3 grid(static_cast<unsigned>(p.M));

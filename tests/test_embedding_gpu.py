@@ -128,6 +128,7 @@ def test_many_positions(M):
     """The sort's blocks hold one, several and many runs of positions."""
     backward(M, 90000, 9, F32, F32, "frequent")
     backward(M, 1000, 4, BF16, F32, "any", itype=torch.int32)
+    backward(M, 300, 8, F32, F32, "any")        # (one pass of the sort)
 
 
 @pytest.mark.parametrize("D", [8, 16, 40, 64, 100, 128, 500, 520])

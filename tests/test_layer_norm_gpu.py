@@ -111,8 +111,9 @@ def test_row_counts(M):
 # every width of work to a thread, whole units of eight columns and not, with so many rows that
 # each group of threads walks down several
 @pytest.mark.parametrize("M,N", [(15000, 64), (7500, 71), (15000, 250), (9000, 512), (8000, 777),
-                                 (7400, 1024), (4000, 1030), (4000, 1536), (2500, 2048), (2400, 2510), (2300, 3500),
-                                 (2000, 4096), (1000, 8000), (800, 8192), (700, 12001),
+                                 (7400, 1024), (4000, 1030), (4000, 1536), (2500, 2048),
+                                 (2400, 2510), (2300, 3500),
+                                 (2000, 4096), (1000, 6001), (1000, 8000), (800, 8192), (700, 12001),
                                  (700, 16384), (300, 20001), (150, 32768)])
 @pytest.mark.parametrize("dtype,stream", TYPES)
 def test_many_rows(M, N, dtype, stream):
