@@ -10,8 +10,7 @@
  *  - Matrices are row-major with a row stride (ld*) in elements, at least their number
  *    of columns, and may start at any multiple of their element's size.  Rows that start
  *    on 16-byte boundaries (of every matrix of the call) are read and written 16 bytes at
- *    a time; others element by element, at a fraction of the speed.  Anything else is
- *    IGC_ERR_MISALIGNED.
+ *    a time; others take two to four times as long.  Anything else is IGC_ERR_MISALIGNED.
  *  - Sizes: anything that fits 32 bits; what would need more than 2^31 - 1 blocks is
  *    IGC_ERR_UNSUPPORTED.  An empty output is a no-op.
  *  - Aliasing: outputs must not overlap inputs or each other, but for the pairs that an
@@ -151,8 +150,7 @@ int embedding_lookup(int64_t M, int64_t V, int64_t D, const void *tokens, int to
  *           it is written, zeros where no token points; with it (1) only the rows that a
  *           token points to are read and written.
  *
- *  The sum of a row runs over the positions in ascending order, in groups whose bounds
- *  depend on the tokens and sizes alone.
+ *  The sum of a row is formed in an order that depends on the tokens and sizes alone.
  */
 size_t embedding_backward_workspace_size(int64_t M, int64_t V, int64_t D);
 int embedding_backward(int64_t M, int64_t V, int64_t D, const void *tokens, int token_bytes,
