@@ -202,6 +202,31 @@ def test_in_place_streams():
         assert torch.equal(A, dS) and torch.equal(dX2, dX)
 
 
+@pytest.mark.parametrize("N,pad,shift", [(100, 0, 1), (777, 0, 0), (4097, 3, 5), (12001, 0, 3),
+                                         (20003, 2, 7)])
+@pytest.mark.parametrize("stream", [BF16, F32])
+def test_in_place_streams_off_boundaries(N, pad, shift, stream):
+    """The same where a 16-byte piece holds what two lanes, warps or rows write."""
+    gen = generator(N, str(stream))
+    X, R = matrix(gen, 65, N, BF16, pad=pad, shift=shift), \
+        matrix(gen, 65, N, stream, pad=pad, shift=shift)
+    S, Y = (matrix(gen, 65, N, t, pad=pad, shift=shift) for t in (stream, BF16))
+    m, r = torch.empty(65, device="cuda"), torch.empty(65, device="cuda")
+    drop = dict(p=0.1, seed=3)
+    igc.layer_norm(X, residual=R, Y=Y, S=S, mean=m, rstd=r, **drop)
+    Y2 = matrix(gen, 65, N, BF16, pad=pad, shift=shift)
+    igc.layer_norm(X, residual=R, S=R, Y=Y2, **drop)
+    assert torch.equal(R, S) and torch.equal(Y2, Y)
+    assert bool((around(R) == 77.0).all()) and bool((around(Y2) == 77.0).all())
+    A, dS = (matrix(gen, 65, N, stream, pad=pad, shift=shift) for _ in range(2))
+    dX, dX2 = (matrix(gen, 65, N, BF16, pad=pad, shift=shift) for _ in range(2))
+    igc.layer_norm_backward(Y, S, m, r, dS_add=A, dS=dS, dX=dX, **drop)
+    igc.layer_norm_backward(Y, S, m, r, dS_add=A, dS=A, dX=dX2, **drop)
+    check_device_ok()
+    assert torch.equal(A, dS) and torch.equal(dX2, dX)
+    assert bool((around(A) == 77.0).all()) and bool((around(dX2) == 77.0).all())
+
+
 def test_rows_far_from_zero_and_constant_rows():
     """A mean that is 4096 times the spread cancels nothing but its own rounding; a row of one
     value has variance 0 and gives b."""
