@@ -209,6 +209,9 @@ __global__ void __launch_bounds__(NormRows<kLanes, kUnits>::kBlock,
     layer_norm_rows_kernel(const NormParams p) {
   constexpr int kGroups = NormRows<kLanes, kUnits>::kGroups;
   constexpr int kSizeT = kT == IGC_F32 ? 4 : 2, kSizeS = kS == IGC_F32 ? 4 : 2;
+  // few rows: w and b are loaded with the row, not after its sums (1 x 4096: 1.9 us, 2.1 after;
+  // where rows fill the SMs their registers cost more: 65536 x 200 with dropout 31 instead of 27)
+  constexpr bool kEarly = kUnits == 1 && kLanes >= 128;
   __shared__ __align__(16) float red[kGroups][2][(kLanes + 127) / 128 * 4];
   const int t = threadIdx.x % kLanes, group = threadIdx.x / kLanes, N8 = p.N / 8 * 8;
   const long long row = static_cast<long long>(blockIdx.x) * kGroups + group;
@@ -235,6 +238,11 @@ __global__ void __launch_bounds__(NormRows<kLanes, kUnits>::kBlock,
       if (!decltype(whole)::value && (n >= N8 || !there)) continue;
       if (has_x) x[i] = load8<kT>(x_row, n, n + 8, true);
       if (has_r) r[i] = load8<kS>(r_row, n, n + 8, true);
+    }
+    float w_early[8], b_early[8];
+    if constexpr (kEarly) {
+      load_vec8<kT>(p.w, t * 8, p.N, p.w_f32, 1.0f, w_early);
+      load_vec8<kT>(p.b, t * 8, p.N, p.w_f32, 0.0f, b_early);
     }
     uint64_t sum = 0;
 #pragma unroll
@@ -294,8 +302,13 @@ __global__ void __launch_bounds__(NormRows<kLanes, kUnits>::kBlock,
       const int n = (i * kLanes + t) * 8;
       if (!decltype(whole)::value && (n >= N8 || !there)) continue;
       float wv[8], bv[8];
-      load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, wv);
-      load_vec8<kT>(p.b, n, p.N, p.w_f32, 0.0f, bv);
+      if constexpr (kEarly) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wv[j] = w_early[j], bv[j] = b_early[j];
+      } else {
+        load_vec8<kT>(p.w, n, p.N, p.w_f32, 1.0f, wv);
+        load_vec8<kT>(p.b, n, p.N, p.w_f32, 0.0f, bv);
+      }
 #pragma unroll
       for (int j = 0; j < 8; j += 2)
         unpair(fma2(mul2(pair(s[i][j], s[i][j + 1]), r2), pair(wv[j], wv[j + 1]),
@@ -339,9 +352,13 @@ int launch_long_rows(const NormParams& p, bool drop, cudaStream_t stream) {
 template <int kT, int kS>
 int run_norm(const DeviceInfo& dev, const NormParams& p, bool drop, cudaStream_t stream) {
   const long long units = (static_cast<long long>(p.N) + 7) / 8;
-  // Two rows to an SM or fewer: a unit or two to a thread, so that a row is done sooner (on the
-  // device 1 x 1024 bf16 1.6 us, 1 x 4096 2.1, 1 x 8192 2.8; with four units 2.6, 2.7 and 3.0).
-  if (p.vec && units > 32 && p.M <= 2 * dev.sm_count) {
+  // Few rows: a unit or two to a thread, so that a row is done sooner (on the device 1 x 1024 bf16
+  // 1.4 us, 1 x 4096 1.9, 1 x 8192 2.8; with four units 2.6, 2.7 and 3.0).  As long as an SM holds
+  // all its rows at once: 16 of 128 threads (600 x 1000: 2.0 us, 3.2 with four units; 2400 x 1000:
+  // 4.6, 4.9), 8 of 256 (600 x 2048: 2.7, 3.2; 2400: 7.4, 8.1; 4800: 13.7, 11.7), two of 512 (333 x
+  // 4096: 4.0, 3.5), and 4 where half of a row's threads have nothing (1200 x 512: 2.3, 2.3).
+  const int at_once = units <= 64 ? 4 : units <= 128 ? 16 : units <= 256 ? 8 : 2;
+  if (p.vec && units > 32 && p.M <= static_cast<long long>(at_once) * dev.sm_count) {
     if (units <= 128) return launch_rows<kT, kS, 128, 1>(p, drop, stream);
     if (units <= 256) return launch_rows<kT, kS, 256, 1>(p, drop, stream);
     if (units <= 512) return launch_rows<kT, kS, 512, 1>(p, drop, stream);
