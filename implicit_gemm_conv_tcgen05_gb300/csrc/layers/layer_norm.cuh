@@ -4,8 +4,9 @@
 // Bound by memory: X and R are read once, S and Y written once.  A row's S stays in the
 // registers of its threads (units of eight columns), so that mean and variance are two sums
 // over registers; the variance is that of the differences from the mean, which a large mean
-// does not cancel (16384 x 4096 bf16 with dropout and residual: 87 us, 537 MB at 6.2 TB/s).  Rows
-// that no block's registers hold are read three times.
+// does not cancel: only the roundings of its sum are left in them (16384 x 4096 bf16 with dropout
+// and residual: 87 us, 537 MB at 6.2 TB/s).  Rows that no block's registers hold are read three
+// times.
 #pragma once
 
 #include "layers_host.h"
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kLanes) layer_norm_shifted_kernel(const NormPa
     total = add2(total, add2(add2(pair(s[i][0], s[i][1]), pair(s[i][2], s[i][3])),
                              add2(pair(s[i][4], s[i][5]), pair(s[i][6], s[i][7]))));
   }
-  const float mean = row_sum<kLanes>(sum2(total), red[0]) * inv;
+  const float mean = quotient(row_sum<kLanes>(sum2(total), red[0]), p.N, inv);
   float squares = 0.0f;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(NormRows<kLanes, kUnits>::kBlock,
       s_last = kDrop ? drop1(p.drop, offset, row, last, x_last, r_last) : x_last + r_last;
       total += s_last;
     }
-    const float mean = row_sum<kLanes>(total, red[group][0], group) * inv;
+    const float mean = quotient(row_sum<kLanes>(total, red[group][0], group), p.N, inv);
     const uint64_t m = pair(-mean, -mean);
     uint64_t squares = 0;
 #pragma unroll

@@ -84,7 +84,8 @@ int dropout_add(int64_t M, int64_t N, const void *X, int64_t ldx, int x_dtype,
  *  mean, rstd  device fp32 vectors of M elements; either may be NULL: not stored.
  *
  *  dtype: any; s_dtype: dtype or IGC_F32 (a residual stream kept in fp32).  N >= 1.  The
- *  statistics and Y are those of the fp32 S, before it is rounded where it is stored.  The
+ *  statistics and Y are those of the fp32 S, before it is rounded where it is stored.  The mean
+ *  is an fp32 sum divided by N: a row of one value whose sums fp32 holds gives Y = b.  The
  *  variance is a sum of squared differences from the mean in fp32: a row whose values differ by
  *  more than 2^63 has an infinite one (rstd 0, Y = b), one whose sum overflows a mean that is not
  *  finite (Y NaN).

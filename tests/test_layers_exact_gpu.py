@@ -1,0 +1,37 @@
+"""Layer operators on values whose fp32 sums are exact in any order, so that the results are those
+of the definition to the last bit."""
+
+import pytest
+import torch
+
+import implicit_gemm_conv_tcgen05_gb300 as igc
+from gpu_helpers import check_device_ok
+from layers_reference import generator, matrix
+
+pytestmark = pytest.mark.gpu
+
+
+def constant_rows(M, N, pad):
+    """Row i holds i + 1 throughout: every sum over it is a whole number under 2^24."""
+    assert M * N < 2 ** 24
+    X = matrix(generator(M, N), M, N, torch.float32, pad=pad)
+    X.copy_(torch.arange(1, M + 1, device="cuda", dtype=torch.float32)[:, None].expand(M, N))
+    return X
+
+
+# widths of every kernel, for which a rounded 1/N times N i is often not i; pad None: rows on 16-byte boundaries
+@pytest.mark.parametrize("N", [61, 122, 241, 488, 749, 1000, 1498, 2021, 2996, 4067, 5992, 8163,
+                               12037, 16268, 20002])
+@pytest.mark.parametrize("pad", [None, 1])
+def test_rows_of_one_value_have_their_mean(N, pad):
+    """The mean is the sum divided by N, not multiplied by a rounded 1/N (which puts it one step of
+    fp32 off at 1000 columns of 1000.0, and Y there 0.02 off): a row of one value gives b."""
+    for M in (5, 800):
+        X = constant_rows(M, N, pad)
+        gen = generator(N)
+        w, b = (torch.randn(N, generator=gen, device="cuda") for _ in range(2))
+        mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        y = igc.layer_norm(X, w, b, eps=2.0 ** -20, mean=mean, rstd=rstd)
+        check_device_ok()
+        assert torch.equal(mean, X[:, 0]) and bool((rstd == 1024.0).all())
+        assert torch.equal(y, b.expand(M, N))
