@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       }
       if (kBehind && t == 0 && stopped < 0 && k + st.slots - 1 < walk.count)
         fill(k + st.slots - 1);
-      c1 *= inv;
+      c1 = quotient(c1, p.N, inv);
       c2 *= inv;
       const uint64_t r2 = pair(rstd, rstd), m1 = pair(-c1, -c1), m2 = pair(-c2, -c2);
 #pragma unroll
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) layer_norm_bwd_any_kernel(const Norm
   leave_sums<kThreads>(c1, c2, red);
   __syncthreads();
   take_sums<kThreads>(c1, c2, red);
-  c1 *= inv;
+  c1 = quotient(c1, p.N, inv);
   c2 *= inv;
   char* ds_row = row_at<kS>(p.dS, row, p.ldds);
   char* dx_row = row_at<kT>(p.dX, row, p.lddx);
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       lane_sums<kLanes>(c1, c2);
       if (row >= p.M || n >= p.N) continue;
       float d[8];
-      slopes8<kS>(p, rstd[r], c1 * inv, c2 * inv, a[r], g, h, d);
+      slopes8<kS>(p, rstd[r], quotient(c1, p.N, inv), c2 * inv, a[r], g, h, d);
       if (p.dS != nullptr) store8<kS>(row_at<kS>(p.dS, row, p.ldds), n, p.N, vec, d);
       if (p.dX != nullptr) {
         if constexpr (kDrop) drop8(p.drop, drop_bits(p.drop, offset, row, n), d);

@@ -401,9 +401,9 @@ __device__ __forceinline__ float row_sum(float v, float* red, int group = 0) {
   return v;
 }
 
-// a / n, rounded to nearest, from inv = 1 / n (rounded to nearest), n < 2^24: the product a * inv
-// alone is a step off for many a even where n divides a, and a row of one value would not have it
-// as its mean.  The remainder of the product, which is exact, corrects it (Markstein, "Computation
+// a / n, rounded to nearest, from inv = 1 / n (rounded to nearest); fp32 holds n up to 2^24.  The
+// product a * inv alone is a step off for many a even where n divides a, and a row of one value
+// would not have it as its mean.  The remainder of the product, which is exact, corrects it (Markstein, "Computation
 // of elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990).  (A
 // division there took 1 to 5 % of a pass over rows: its branch for extreme values holds registers.)
 __device__ __forceinline__ float quotient(float a, int n, float inv) {

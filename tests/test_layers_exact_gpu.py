@@ -35,3 +35,22 @@ def test_rows_of_one_value_have_their_mean(N, pad):
         check_device_ok()
         assert torch.equal(mean, X[:, 0]) and bool((rstd == 1024.0).all())
         assert torch.equal(y, b.expand(M, N))
+
+
+# widths of every kernel of the backward pass
+@pytest.mark.parametrize("N", [61, 122, 241, 488, 1000, 1498, 2021, 2500, 4067, 5992, 8163, 12037,
+                               16268, 20400, 32001, 40001])
+@pytest.mark.parametrize("pad", [None, 1])
+def test_gradients_of_one_value_to_a_row_cancel(N, pad):
+    """A norm does not change with a shift of its row: where h is 0 the gradient of the row's sum
+    is 0, which asks for the mean of g as exactly as the forward pass does for that of S."""
+    for M in (5, 400):
+        dY = constant_rows(M, N, pad)
+        S, dS = (matrix(generator(N), M, N, torch.float32, pad=pad) for _ in range(2))
+        S.zero_()
+        dw, db = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+        igc.layer_norm_backward(dY, S, torch.zeros(M, device="cuda"),
+                                torch.full((M,), 2.0, device="cuda"), dS=dS, dw=dw, db=db)
+        check_device_ok()
+        assert not bool(dS.any()) and not bool(dw.any())
+        assert bool((db == M * (M + 1) // 2).all())
