@@ -51,12 +51,7 @@ __device__ __forceinline__ void join8(const NormParams& p, uint64_t offset, long
 
 // s less the mean; returns the sum of the squares.
 __device__ __forceinline__ float center8(float (&s)[8], float mean, int n, int N) {
-  if (n + 8 > N) {
-    // (what lies past the row's end is to differ by nothing)
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (n + j >= N) s[j] = mean;
-  }
+  fill_past(s, n, N, mean);  // (what lies past the row's end is to differ by nothing)
   const uint64_t m = pair(-mean, -mean);
   uint64_t q = 0;
 #pragma unroll

@@ -239,6 +239,14 @@ __device__ __forceinline__ void store8_warp(char* row, int n, int N, bool vec, b
   }
 }
 
+// Of a unit of columns [n, n + 8) those past the row's end become v.
+__device__ __forceinline__ void fill_past(float (&s)[8], int n, int N, float v) {
+  if (n + 8 <= N) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (n + j >= N) s[j] = v;
+}
+
 // Elements [n, n + 8) of a vector of N that is fp32 (f32) or of type kT; `none` for no vector
 // and past its end.  (Vectors may start anywhere: 16-byte loads where they can.)
 template <int kT>

@@ -6,7 +6,7 @@ import torch
 
 import implicit_gemm_conv_tcgen05_gb300 as igc
 from gpu_helpers import check_device_ok
-from layers_reference import generator, matrix
+from layers_reference import check, generator, matrix, norm_backward64, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,27 @@ def test_gradients_of_one_value_to_a_row_cancel(N, pad):
         check_device_ok()
         assert not bool(dS.any()) and not bool(dw.any())
         assert bool((db == M * (M + 1) // 2).all())
+
+
+@pytest.mark.parametrize("N,pad", [(9, 7), (100, 4), (249, 7), (9, 0), (100, 1), (513, 0), (1001, 0),
+                                   (7001, 2), (9001, 0)])
+@pytest.mark.parametrize("add", [False, True])
+def test_rows_far_from_zero_with_a_part_of_a_unit(N, pad, add):
+    """Rows of 2^110 whose last unit of eight columns is not whole: what lies past a row's end has
+    no part in its sums, also where 2^110 rstd is past fp32's range."""
+    M = 70
+    X = matrix(generator(N), M, N, torch.float32, pad=pad)
+    X.fill_(2.0 ** 110)
+    mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    igc.layer_norm(X, eps=2.0 ** -60, mean=mean, rstd=rstd)
+    check_device_ok()
+    assert bool((mean == 2.0 ** 110).all()) and bool((rstd == 2.0 ** 30).all())
+    dY, A, dS = (matrix(generator(N, k), M, N, torch.float32, pad=pad) for k in range(3))
+    dY.copy_(torch.randint(-8, 9, (M, N), device="cuda"))
+    A = A if add else None
+    dw, db = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    igc.layer_norm_backward(dY, X, mean, rstd, dS_add=A, dS=dS, dw=dw, db=db)
+    check_device_ok()
+    assert not bool(dw.any()) and torch.equal(db, dY.sum(0))
+    want, err = norm_backward64(dY, X, mean, rstd, None, A)[:2]
+    check(dS, want, rounded(want, torch.float32, err))
