@@ -131,8 +131,9 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   // the cluster's sums, by block, and the barriers that count their arrival: two of each, for
   // alternate rows
   __shared__ __align__(16) uint64_t met[kGroups][2][kCluster], met_bar[kGroups][2];
-  __shared__ int abort_flag;
-  const RowWalk walk = row_walk<kLanes, kGroups, kCluster>(st, ring, full, &abort_flag, p.M);
+  __shared__ int abort_flag, lost;
+  const RowWalk walk =
+      row_walk<kLanes, kGroups, kCluster>(st, ring, full, &abort_flag, &lost, p.M);
   if constexpr (kCluster > 1) {
     if (walk.t == 0) {
       mbar_init(&met_bar[walk.group][0], 1);
@@ -312,8 +313,9 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
     walk_rows(std::true_type{});
   else
     walk_rows(std::false_type{});
-  if (t == 0 && stopped >= 0)
-    drain_slots(st, walk.bars, stopped, min(walk.count, stopped + st.slots));
+  if (t == 0 && stopped >= 0 &&
+      !drain_slots(st, walk.bars, stopped, min(walk.count, stopped + st.slots - kBehind)))
+    lost = 1;
   // (no block may exit before what is sent to it is there)
   if constexpr (kCluster > 1) cluster_sync();
   if (p.partial == nullptr) return;
@@ -321,8 +323,10 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   float* tot = reinterpret_cast<float*>(ring);
   const int width = (rank == kCluster - 1 ? p.N : col0 + cols) - col0;
   __syncthreads();
+  const bool ring_free = lost == 0;  // (else a copy may land in it yet, and the sums are no use)
 #pragma unroll
   for (int v = 0; v < 2; ++v) {
+    if (!ring_free) break;
     const float(&acc)[kUnits][8] = v ? sb : sw;
     float* to = tot + (walk.group * 2 + v) * width;
 #pragma unroll
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       db += tot[(2 * r + 1) * width + n];
     }
     if (p.join) {
-      tot[n] = dw, tot[width + n] = db;
+      if (ring_free) tot[n] = dw, tot[width + n] = db;
     } else {
       out[n] = dw;
       out[static_cast<long long>(rows) * p.N + n] = db;

@@ -29,6 +29,10 @@ struct RowStream {
   unsigned long long* status = nullptr;
 };
 
+// What is on its way to a block after a wait gave up is waited for as long as this, whatever the
+// limit of the waits is: a copy or a store takes microseconds.
+constexpr uint64_t kLandNs = 1000000000;
+
 // Sites of waits that gave up (device status word).
 enum : uint32_t { kSiteNormBwdRow = 0x4c01, kSiteNormBwdMeet = 0x4c02, kSiteRowDrain = 0x4c03 };
 
@@ -87,14 +91,18 @@ __device__ __forceinline__ void kept_weights(const char* from, uint32_t plane, i
   w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
 }
 
-// After a wait gave up, the group's leader: the copies in flight (of its rows next, next + 1, ...
-// last - 1) are waited for, again with a limit, so that none lands after the block has gone.
-__device__ __forceinline__ void drain_slots(const RowStream& s, uint64_t* bars, int next,
-                                            int last) {
-  volatile int none = 0;
-  for (int k = next; k < last; ++k)
-    (void)mbar_wait(bars + k % s.slots, static_cast<uint32_t>(k / s.slots) & 1u, s.wait_limit,
-                    &none, s.status, kSiteRowDrain);
+// After a wait gave up, the group's leader: the copies of its rows next, next + 1, ... filled - 1,
+// all that may be in flight, are waited for, each for kLandNs, so that none lands after the block
+// has gone or the ring has another use.  False: one never landed.
+__device__ __forceinline__ bool drain_slots(const RowStream& s, uint64_t* bars, int next,
+                                            int filled) {
+  bool landed = true;
+  for (int k = next; k < filled; ++k) {
+    int none = 0;
+    landed = mbar_wait(bars + k % s.slots, static_cast<uint32_t>(k / s.slots) & 1u, kLandNs, &none,
+                       s.status, kSiteRowDrain) && landed;
+  }
+  return landed;
 }
 
 // A group's walk: rows first, first + step, ... (count of them), its slots and barriers.
@@ -111,7 +119,7 @@ struct RowWalk {
 template <int kLanes, int kGroups, int kCluster>
 __device__ __forceinline__ RowWalk row_walk(const RowStream& st, char* ring,
                                             uint64_t (&full)[kGroups][kMaxSlots],
-                                            int* abort_flag, int M) {
+                                            int* abort_flag, int* lost, int M) {
   RowWalk w;
   w.t = threadIdx.x % kLanes;
   w.group = threadIdx.x / kLanes;
@@ -121,7 +129,7 @@ __device__ __forceinline__ RowWalk row_walk(const RowStream& st, char* ring,
     for (int i = 0; i < st.slots; ++i) mbar_init(w.bars + i, 1);
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) *abort_flag = 0;
+  if (threadIdx.x == 0) *abort_flag = *lost = 0;
   w.first = static_cast<long long>(blockIdx.x / kCluster) * kGroups + w.group;
   w.step = static_cast<long long>(gridDim.x / kCluster) * kGroups;
   w.count = w.first < M ? static_cast<int>((M - w.first + w.step - 1) / w.step) : 0;

@@ -1,0 +1,47 @@
+"""The backward pass of layer norm with waits that may give up: nothing that is on its way to a
+block's shared memory arrives after the block has gone, so that the worst that a wait's limit can do
+is a reported timeout."""
+
+import pytest
+import torch
+
+import implicit_gemm_conv_tcgen05_gb300 as igc
+from gpu_helpers import check_device_ok
+from layers_reference import BF16, generator, matrix
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M,N", [(9000, 500), (3000, 1500), (1500, 4100), (1000, 6000),
+                                 (1000, 8192)])
+def test_the_shortest_limit_gives_a_result_or_a_timeout(M, N):
+    gen = generator(M, N)
+    dY, S, A = (matrix(gen, M, N, BF16) for _ in range(3))
+    w = torch.randn(N, generator=gen, device="cuda")
+    mean, rstd = torch.zeros(M, device="cuda"), torch.ones(M, device="cuda")
+
+    def call():
+        dX = torch.empty_like(dY)
+        dS, _, dw, db = igc.layer_norm_backward(
+            dY, S, mean, rstd, w, dS_add=A, p=0.1, seed=1, dS=torch.empty_like(S), dX=dX,
+            dw=torch.empty_like(w), db=torch.empty_like(w))
+        return dS, dX, dw, db
+
+    want = call()
+    check_device_ok()
+    old = igc.igc_set_wait_limit_ns(1)         # (raised to the least, 1 us)
+    try:
+        for _ in range(5):
+            got = call()
+            rc = igc.igc_check_device_status()
+            assert rc in (igc.IGC_OK, igc.IGC_ERR_DEVICE_TIMEOUT)
+            if rc == igc.IGC_OK:
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+            else:                              # a row's copy or the cluster's sums
+                site = igc.igc_last_device_status() >> 32 & 0xFFFFFF
+                assert site in (0x4C01, 0x4C02), hex(site)
+    finally:
+        igc.igc_set_wait_limit_ns(old)
+    got = call()
+    check_device_ok()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
