@@ -128,17 +128,18 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   extern __shared__ __align__(128) char ring[];
   __shared__ uint64_t full[kGroups][kMaxSlots];
   __shared__ __align__(16) float2 red[kGroups][2][(kLanes / 32 + 1) / 2 * 2];
-  // the cluster's sums, by block, and the barriers that count their arrival: two of each, for
-  // alternate rows
-  __shared__ __align__(16) uint64_t met[kGroups][2][kCluster], met_bar[kGroups][2];
+  __shared__ __align__(16) Meeting<kCluster> meet[kCluster > 1 ? kGroups : 1];
   __shared__ int abort_flag, lost;
   const RowWalk walk =
       row_walk<kLanes, kGroups, kCluster>(st, ring, full, &abort_flag, &lost, p.M);
   if constexpr (kCluster > 1) {
     if (walk.t == 0) {
-      mbar_init(&met_bar[walk.group][0], 1);
-      mbar_init(&met_bar[walk.group][1], 1);
+      Meeting<kCluster>& m = meet[walk.group];
+      mbar_init(&m.bar[0], 1);
+      mbar_init(&m.bar[1], 1);
       fence_mbar_init();
+#pragma unroll
+      for (int r = 0; r < kCluster; ++r) m.sent[r] = walk.count;
     }
     cluster_sync();
   }
@@ -188,7 +189,9 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   char* ds_row = row_at<kS>(p.dS, walk.first, p.ldds) + col0 * kSizeS;
   char* dx_row = row_at<kT>(p.dX, walk.first, p.lddx) + col0 * kSizeT;
   const long long ds_step = walk.step * p.ldds * kSizeS, dx_step = walk.step * p.lddx * kSizeT;
-  int stopped = -1;  // the row whose wait gave up
+  // A wait that gave up is reported; the group goes on to its end, without further copies, waits
+  // and sums sent.
+  int stop = -1;  // twice the row whose wait gave up, plus 1 where that was for the cluster's sums
   int slot = 0;
   uint32_t phase = 0;
   // whole: every lane of the warp has all its units, so that no branch keeps the loads and the
@@ -201,10 +204,10 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       float mean_next = 0.0f, rstd_next = 0.0f;
       if (k + 1 < walk.count)
         mean_next = p.mean[row + walk.step], rstd_next = p.rstd[row + walk.step];
-      // (a wait that gave up is reported; the group goes on to its end, without further copies)
-      if (!mbar_wait(walk.bars + slot, phase, st.wait_limit, &abort_flag, st.status,
-                     kSiteNormBwdRow) && stopped < 0)
-        stopped = k;
+      if (!mbar_try_wait(smem_u32(walk.bars + slot), phase) && stop < 0 &&
+          !mbar_wait(walk.bars + slot, phase, st.wait_limit, &abort_flag, st.status,
+                     kSiteNormBwdRow))
+        stop = 2 * k;
       float g[kAgain ? 1 : kUnits][8], h[kAgain ? 1 : kUnits][8];
       uint64_t p1 = 0, p2 = 0;
 #pragma unroll
@@ -244,24 +247,25 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       if constexpr (kCluster > 1) {
         // (the bytes of the row after the next go to this row's barrier: they are sent by a block
         // that has met the next row's, which this block sends after all of it has met this row's)
-        uint64_t* bar = &met_bar[walk.group][k & 1];
-        uint64_t* sums = met[walk.group][k & 1];
-        if (t == 0) {
+        uint64_t* bar = &meet[walk.group].bar[k & 1];
+        uint64_t* sums = meet[walk.group].sums[k & 1];
+        if (t == 0 && stop < 0) {
           mbar_arrive_expect_tx(bar, 8 * kCluster);
 #pragma unroll
           for (int r = 0; r < kCluster; ++r)
             store_async_u64(mapa_shared(smem_u32(sums + rank), r), pair(c1, c2),
                             mapa_shared(smem_u32(bar), r));
         }
-        if (!mbar_wait<true>(bar, static_cast<uint32_t>(k / 2) & 1u, st.wait_limit, &abort_flag,
-                             st.status, kSiteNormBwdMeet) && stopped < 0)
-          stopped = k;
+        const uint32_t parity = static_cast<uint32_t>(k / 2) & 1u;
+        if (!mbar_try_wait_cluster(smem_u32(bar), parity) && stop < 0 &&
+            !mbar_wait<true>(bar, parity, st.wait_limit, &abort_flag, st.status, kSiteNormBwdMeet))
+          stop = 2 * k + 1;
         uint64_t both = sums[0];
 #pragma unroll
         for (int r = 1; r < kCluster; ++r) both = add2(both, sums[r]);
         unpair(both, c1, c2);
       }
-      if (kBehind && t == 0 && stopped < 0 && k + st.slots - 1 < walk.count)
+      if (kBehind && t == 0 && stop < 0 && k + st.slots - 1 < walk.count)
         fill(k + st.slots - 1);
       c1 = quotient(c1, p.N, inv);
       c2 *= inv;
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
       }
       if constexpr (!kBehind) {
         __syncwarp();
-        if (t == 0 && stopped < 0 && k + st.slots < walk.count) fill(k + st.slots);
+        if (t == 0 && stop < 0 && k + st.slots < walk.count) fill(k + st.slots);
       }
       mean = mean_next, rstd = rstd_next;
       ds_row += ds_step;
@@ -313,11 +317,21 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
     walk_rows(std::true_type{});
   else
     walk_rows(std::false_type{});
-  if (t == 0 && stopped >= 0 &&
-      !drain_slots(st, walk.bars, stopped, min(walk.count, stopped + st.slots - kBehind)))
+  if (t == 0 && stop >= 0 &&
+      !drain_slots(st, walk.bars, stop / 2, min(walk.count, stop / 2 + st.slots - kBehind)))
     lost = 1;
-  // (no block may exit before what is sent to it is there)
-  if constexpr (kCluster > 1) cluster_sync();
+  if constexpr (kCluster > 1) {
+    Meeting<kCluster>& m = meet[walk.group];
+    if (t == 0 && stop >= 0) {
+#pragma unroll
+      for (int r = 0; r < kCluster; ++r)
+        st_shared_cluster_u32(mapa_shared(smem_u32(m.sent + rank), r),
+                              static_cast<uint32_t>(stop + 1) / 2);
+    }
+    cluster_sync();
+    // (a leader that met all its rows has had all that is sent to it)
+    if (t == 0 && stop >= 0) drain_meeting(m, rank, st.status);
+  }
   if (p.partial == nullptr) return;
   // one row of sums per block or cluster: the groups' go over their rings, and are added in order
   float* tot = reinterpret_cast<float*>(ring);

@@ -12,8 +12,10 @@ from layers_reference import BF16, generator, matrix
 pytestmark = pytest.mark.gpu
 
 
+# single blocks; clusters of two, four and eight of them, by two and three units to a thread
 @pytest.mark.parametrize("M,N", [(9000, 500), (3000, 1500), (1500, 4100), (1000, 6000),
-                                 (1000, 8192)])
+                                 (1000, 8192), (700, 12000), (700, 16384), (500, 24000),
+                                 (500, 32001), (40, 16384)])
 def test_the_shortest_limit_gives_a_result_or_a_timeout(M, N):
     gen = generator(M, N)
     dY, S, A = (matrix(gen, M, N, BF16) for _ in range(3))
