@@ -983,6 +983,18 @@ def _type_code(t, name):
     return code
 
 
+def _new_rows(rows, cols, dtype, like, stream):
+    """An uninitialised rows x cols matrix and its row stride.  Its rows follow one another closely
+    unless those of `like`, the call's input, are padded so that each starts on a 16-byte boundary:
+    then so are these, or the result's alone would send the call to the slow kernels."""
+    size, step = dtype.itemsize, like.stride(0) * like.element_size()
+    if cols * size % 16 == 0 or rows < 2 or like.shape[0] < 2 or step % 16 != 0 or \
+            like.data_ptr() % 16 != 0:
+        return _new((rows, cols), dtype, like.device, stream), cols
+    ld = -(-cols * size // 16) * 16 // size
+    return _new((rows, ld), dtype, like.device, stream)[:, :cols], ld
+
+
 _or_f32 = {}
 
 
@@ -1030,7 +1042,8 @@ def dropout_add(X, p, seed=None, offset=0, step=None, residual=None, Y=None, str
     the kernel runs (for captured graphs).  X, Y and residual (M,N) fp32, fp16 or bf16;
     residual has Y's type, which is X's unless one of them is fp32.  Y may be X or residual.
     The gradient of X is dropout_add(dY, p, seed, offset, step), that of residual dY.
-    Returns Y (allocated if None, of residual's type, else X's)."""
+    Returns Y (allocated if None, of residual's type, else X's; its rows are padded to 16 bytes
+    where X's are)."""
     xt = _type_code(X, "X")
     M, N = _two_dims(X, "X")
     dev = X.get_device()
@@ -1044,8 +1057,8 @@ def dropout_add(X, p, seed=None, offset=0, step=None, residual=None, Y=None, str
     p, seed, offset, step = _drop_args(p, seed, offset, step, dev)
     _check_device(dev, "X")
     if Y is None:
-        Y = _new((M, N), like.dtype, X.device, stream)
-        y, ldy = Y.data_ptr(), N
+        Y, ldy = _new_rows(M, N, like.dtype, X, stream)
+        y = Y.data_ptr()
     _check(lib().dropout_add(M, N, x, ldx, xt, r, ldr, p, seed, offset, step, y, ldy, yt,
                              _handle(stream, dev)), "dropout_add")
     return Y
@@ -1059,7 +1072,8 @@ def layer_norm(X, w=None, b=None, eps=1e-5, residual=None, p=0.0, seed=None, off
     dropout_add.  Without residual and dropout S is X, which may then be fp32 whatever Y is.
     S, mean and rstd (M, fp32), if given, receive what layer_norm_backward needs, which is to
     be called for the gradients: the result has no autograd history.  S may be residual
-    itself.  Returns Y (allocated if None, of X's type)."""
+    itself.  Returns Y (allocated if None, of X's type, its rows padded to 16 bytes where X's
+    are)."""
     M, N = _two_dims(X, "X")
     _type_code(X, "X")
     dev = X.get_device()
@@ -1086,8 +1100,8 @@ def layer_norm(X, w=None, b=None, eps=1e-5, residual=None, p=0.0, seed=None, off
     m, rs = _floats(mean, "mean", M, dev), _floats(rstd, "rstd", M, dev)
     _check_device(dev, "X")
     if Y is None:
-        Y = _new((M, N), dtype, X.device, stream)
-        y, ldy = Y.data_ptr(), N
+        Y, ldy = _new_rows(M, N, dtype, X, stream)
+        y = Y.data_ptr()
     _check(lib().layer_norm(M, N, dt, x, ldx, r, ldr, _dtype_code(s_dtype), *drop, wp, bp,
                             wt if w is not None else bt, float(eps), s, lds, y, ldy, m, rs,
                             _handle(stream, dev)), "layer_norm")
@@ -1105,7 +1119,7 @@ def layer_norm_backward(dY, S, mean, rstd, w=None, dS_add=None, p=0.0, seed=None
     dS (M,N), that of S and so of the residual, with dS_add (the gradient that reaches S past
     the norm) added; dX (M,N), that of X, through the dropout of the same (p, seed, offset,
     step); dw and db (N).  The ones given are computed; with none given, dS, dw and db are
-    allocated (dw and db in fp32).  dX has dY's type; S, dS_add and dS are of that type or
+    allocated (dw and db in fp32, dS with rows padded to 16 bytes where S's are).  dX has dY's type; S, dS_add and dS are of that type or
     fp32, all the same; w, dw and db of dY's type or fp32.  dS may be dS_add itself.  No
     tensor's .grad is touched.  Returns (dS, dX, dw, db)."""
     dt = _type_code(dY, "dY")
@@ -1123,7 +1137,7 @@ def layer_norm_backward(dY, S, mean, rstd, w=None, dS_add=None, p=0.0, seed=None
         raise ValueError("mean and rstd are needed")
     wp, wt = _vector(w, "w", either, N, dev)
     if dS is None and dX is None and dw is None and db is None:
-        dS = _new((M, N), S.dtype, dY.device, stream)
+        dS, _ = _new_rows(M, N, S.dtype, S, stream)
         dw, db = (_new((N,), torch.float32, dY.device, stream) for _ in range(2))
     ds, ldds = _mat(dS, "dS", stream_type, M, N, dev)
     dx, lddx = _mat(dX, "dX", own, M, N, dev)
@@ -1159,7 +1173,8 @@ def _tokens(tokens, dev):
 def embedding_lookup(tokens, W, scale=1.0, Y=None, stream=None):
     """Y[i] = scale W[tokens[i]]: tokens (M) int32 or int64, W (V,D) fp32, fp16 or bf16, Y (M,D)
     of that type or fp32.  A token outside [0, V) gives a row of zeros.  The result has no
-    autograd history (embedding_backward).  Returns Y (allocated if None, of W's type)."""
+    autograd history (embedding_backward).  Returns Y (allocated if None, of W's type, its rows
+    padded to 16 bytes where W's are)."""
     wt = _type_code(W, "W")
     V, D = _two_dims(W, "W")
     dev = W.get_device()
@@ -1168,8 +1183,8 @@ def embedding_lookup(tokens, W, scale=1.0, Y=None, stream=None):
     y, ldy = _mat(Y, "Y", _type_or_f32(W.dtype), M, D, dev)
     _check_device(dev, "W")
     if Y is None:
-        Y = _new((M, D), W.dtype, W.device, stream)
-        y, ldy = Y.data_ptr(), D
+        Y, ldy = _new_rows(M, D, W.dtype, W, stream)
+        y = Y.data_ptr()
     _check(lib().embedding_lookup(M, V, D, tp, size, w, ldw, wt, float(scale), y, ldy,
                                   _dtype_code(Y.dtype), _handle(stream, dev)),
            "embedding_lookup")
@@ -1183,9 +1198,9 @@ def embedding_backward_workspace_size(M: int, V: int, D: int) -> int:
 def embedding_backward(tokens, dY, V=None, scale=1.0, dW=None, accumulate=False, workspace=None,
                        stream=None):
     """dW[v] = scale * sum of dY[i] over the positions i with tokens[i] = v: dY (M,D) fp32, fp16
-    or bf16, dW (V,D) of that type or fp32 (allocated in dY's type for V rows if None).  All of
-    dW is written, or with accumulate the sums are added to the rows that tokens point to.
-    Returns dW."""
+    or bf16, dW (V,D) of that type or fp32 (allocated in dY's type for V rows if None, padded to
+    16 bytes where dY's are).  All of dW is written, or with accumulate the sums are added to
+    the rows that tokens point to.  Returns dW."""
     yt = _type_code(dY, "dY")
     M, D = _two_dims(dY, "dY")
     dev = dY.get_device()
@@ -1204,8 +1219,8 @@ def embedding_backward(tokens, dY, V=None, scale=1.0, dW=None, accumulate=False,
     w, ldw = _mat(dW, "dW", _type_or_f32(dY.dtype), V, D, dev)
     _check_device(dev, "dY")
     if dW is None:
-        dW = _new((V, D), dY.dtype, dY.device, stream)
-        w, ldw = dW.data_ptr(), D
+        dW, ldw = _new_rows(V, D, dY.dtype, dY, stream)
+        w = dW.data_ptr()
     L = lib()
     need = L.embedding_backward_workspace_size(M, V, D)
     ws, nbytes = None, 0

@@ -113,7 +113,8 @@ extern "C" int dropout_add(int64_t M, int64_t N, const void* X, int64_t ldx, int
   a.per_row = FastDiv(static_cast<uint32_t>((N + 7) / 8));
   a.units = M * ((N + 7) / 8);
   a.N = static_cast<int>(N);
-  a.vec = rows_vec(X, ldx, x_dtype) && rows_vec(R, ldr, y_dtype) && rows_vec(Y, ldy, y_dtype);
+  a.vec = rows_vec(M, X, ldx, x_dtype) && rows_vec(M, R, ldr, y_dtype) &&
+          rows_vec(M, Y, ldy, y_dtype);
   a.X = X, a.R = R, a.Y = Y;
   a.ldx = ldx, a.ldr = ldr, a.ldy = ldy;
   switch (x_dtype * 3 + y_dtype) {

@@ -102,7 +102,7 @@ extern "C" int embedding_lookup(int64_t M, int64_t V, int64_t D, const void* tok
   p.per_row = FastDiv(static_cast<uint32_t>((D + 7) / 8));
   p.units = M * ((D + 7) / 8);
   p.D = static_cast<int>(D);
-  p.vec = rows_vec(W, ldw, w_dtype) && rows_vec(Y, ldy, y_dtype);
+  p.vec = rows_vec(V, W, ldw, w_dtype) && rows_vec(M, Y, ldy, y_dtype);
   p.token64 = token_bytes == 8;
   p.V = V;
   p.tokens = tokens, p.W = W, p.Y = Y;

@@ -670,7 +670,7 @@ int embedding_backward(int64_t M, int64_t V, int64_t D, const void* tokens, int 
     return IGC_ERR_WORKSPACE;
   EmbedParams p = {};
   p.M = static_cast<int>(M), p.D = static_cast<int>(D), p.V = V;
-  p.vec = rows_vec(dY, lddy, y_dtype) && rows_vec(dW, lddw, dw_dtype);
+  p.vec = rows_vec(M, dY, lddy, y_dtype) && rows_vec(V, dW, lddw, dw_dtype);
   p.token64 = token_bytes == 8;
   p.accumulate = accumulate != 0;
   const int64_t slab = (M <= kSmallM ? kSmallUnits : kThreads) * 8;

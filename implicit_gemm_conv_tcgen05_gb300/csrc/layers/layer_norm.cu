@@ -33,8 +33,8 @@ extern "C" int layer_norm(int64_t M, int64_t N, int dtype, const void* X, int64_
   const int rc = current_device(&dev);
   if (rc != IGC_OK) return rc;
   a.M = static_cast<int>(M), a.N = static_cast<int>(N);
-  a.vec = rows_vec(X, ldx, dtype) && rows_vec(R, ldr, s_dtype) && rows_vec(S, lds, s_dtype) &&
-          rows_vec(Y, ldy, dtype);
+  a.vec = rows_vec(M, X, ldx, dtype) && rows_vec(M, R, ldr, s_dtype) &&
+          rows_vec(M, S, lds, s_dtype) && rows_vec(M, Y, ldy, dtype);
   a.w_f32 = w_dtype == IGC_F32;
   a.X = X, a.R = R, a.S = S, a.Y = Y;
   a.ldx = ldx, a.ldr = ldr, a.lds = lds, a.ldy = ldy;

@@ -91,8 +91,9 @@ int layer_norm_backward(int64_t M, int64_t N, int dtype, const void* dY, int64_t
   int blocks = 0;
   if (M > 0) {
     a.M = static_cast<int>(M), a.N = static_cast<int>(N);
-    a.vec = rows_vec(dY, lddy, dtype) && rows_vec(S, lds, s_dtype) && rows_vec(A, lda, s_dtype) &&
-            rows_vec(dS, ldds, s_dtype) && rows_vec(dX, lddx, dtype);
+    a.vec = rows_vec(M, dY, lddy, dtype) && rows_vec(M, S, lds, s_dtype) &&
+            rows_vec(M, A, lda, s_dtype) && rows_vec(M, dS, ldds, s_dtype) &&
+            rows_vec(M, dX, lddx, dtype);
     a.w_f32 = w_dtype == IGC_F32;
     a.dY = dY, a.S = S, a.A = A, a.dS = dS, a.dX = dX;
     a.lddy = lddy, a.lds = lds, a.lda = lda, a.ldds = ldds, a.lddx = lddx;

@@ -30,9 +30,10 @@ inline bool make_drop(double p, uint64_t seed, uint64_t offset, const uint64_t* 
   return true;
 }
 
-// Whether the rows of a matrix start on 16-byte boundaries (a null one's do).
-inline bool rows_vec(const void* p, int64_t ld, int dtype) {
-  return p == nullptr || rows_aligned(p, ld, elem_size(dtype), 16);
+// Whether the rows of a matrix of M rows start on 16-byte boundaries (a null one's do).  A single
+// row's stride says nothing.
+inline bool rows_vec(int64_t M, const void* p, int64_t ld, int dtype) {
+  return p == nullptr || rows_aligned(p, M > 1 ? ld : 0, elem_size(dtype), 16);
 }
 
 // Division of 32-bit numbers by a fixed d >= 1 as a product and shifts (Granlund and
