@@ -1037,9 +1037,10 @@ def _floats(v, name, n, dev):
 def dropout_add(X, p, seed=None, offset=0, step=None, residual=None, Y=None, stream=None):
     """Y = residual + drop(X): each element of X (M,N) is kept and scaled with probability
     1 - p (to a multiple of 1/65536), else 0.  Which ones follows from (seed, offset, row,
-    column) and is computed again where it is needed, never stored; calls with other seeds or
-    offsets are independent.  step, a one-element int64 CUDA tensor, is added to offset when
-    the kernel runs (for captured graphs).  X, Y and residual (M,N) fp32, fp16 or bf16;
+    column) and is computed again where it is needed, never stored.  step, a one-element int64
+    CUDA tensor, is added to offset when the kernel runs (for captured graphs).  Calls are
+    independent where (seed, offset + step) differ: layers that share a seed and have offsets 0,
+    1, 2, ... repeat one another's masks a step later, so give each a seed of its own.  X, Y and residual (M,N) fp32, fp16 or bf16;
     residual has Y's type, which is X's unless one of them is fp32.  Y may be X or residual.
     The gradient of X is dropout_add(dY, p, seed, offset, step), that of residual dY.
     Returns Y (allocated if None, of residual's type, else X's; its rows are padded to 16 bytes

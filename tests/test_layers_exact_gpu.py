@@ -78,3 +78,15 @@ def test_rows_far_from_zero_with_a_part_of_a_unit(N, pad, add):
     assert not bool(dw.any()) and torch.equal(db, dY.sum(0))
     want, err = norm_backward64(dY, X, mean, rstd, None, A)[:2]
     check(dS, want, rounded(want, torch.float32, err))
+
+
+def test_offset_and_step_add_up():
+    """Calls differ where offset + step does: a neighbour's offset is the next step's."""
+    X = torch.ones(64, 512, device="cuda")
+    step = torch.tensor(6, device="cuda")
+    a = igc.dropout_add(X, 0.5, seed=3, offset=1, step=step)
+    step.add_(1)
+    b = igc.dropout_add(X, 0.5, seed=3, offset=0, step=step)
+    c = igc.dropout_add(X, 0.5, seed=4, offset=0, step=step)
+    check_device_ok()
+    assert torch.equal(a, b) and not torch.equal(b, c)
