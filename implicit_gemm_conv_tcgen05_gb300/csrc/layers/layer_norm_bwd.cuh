@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(stream_threads(kLanes, kNormBwdStreamMost), 1)
   int slot = 0;
   uint32_t phase = 0;
   // whole: every lane of the warp has all its units, so that no branch keeps the loads and the
-  // arithmetic of different units apart (16384 x 4096 bf16 with dropout: 111 us, with a branch
-  // for each unit 122)
+  // arithmetic of different units apart (16384 x 4096 bf16 with dropout: 106 us, with a branch
+  // for each unit 119)
   auto walk_rows = [&](auto whole) {
     for (int k = 0; k < walk.count; ++k) {
       const long long row = walk.first + k * walk.step;
@@ -563,8 +563,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 
 // Blocks of a launch whose blocks have `rows` rows side by side: as many as there is work for, at
 // most `most`.  *join (if not null): whether they are one cluster that adds its blocks' sums, as
-// where none then takes more than `once` rows, which take as long as one (64 x 1000 bf16: 15.0 us
-// a call, 6.6 on the device, as two launches 17.4 and 6.6; with four times the rows 15.0 and 10.0).
+// where none then takes more than `once` rows, which take as long as one (64 x 1000 bf16: 12.9 us
+// a call, 6.9 on the device, as two launches 15.2 and 6.5; with four times the rows 10 on the
+// device).
 inline int norm_bwd_blocks(const NormBwdParams& p, int64_t rows, int64_t once, int64_t most,
                            bool* join) {
   if (join != nullptr && p.partial != nullptr && p.M <= kJoinBlocks * once) {

@@ -10,7 +10,7 @@
  *  - Matrices are row-major with a row stride (ld*) in elements, at least their number
  *    of columns, and may start at any multiple of their element's size (anything else is
  *    IGC_ERR_MISALIGNED).  Rows that start on 16-byte boundaries (of every matrix of the call)
- *    are read and written 16 bytes at a time.  Others take two to eight times as long (most at
+ *    are read and written 16 bytes at a time.  Others take up to eight times as long (most at
  *    257 to 512 columns), and layer_norm on rows of up to 256 columns, which then has a block to
  *    each row, 9 to 28 times: 65536 rows of 63 bf16 columns 167 us, of 64 columns 6; of 201
  *    columns 196, of 208 22.
