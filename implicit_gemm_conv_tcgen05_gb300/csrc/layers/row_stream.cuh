@@ -96,7 +96,7 @@ struct Meeting {
 // A group's leader that stopped, once all blocks are at the end and have told the rows they sent:
 // waits for the bytes on their way here.  (The closing barrier of a cluster waits for no st.async,
 // and none may arrive in a block that has gone.  Ordinary stores it would wait for, but they queue
-// behind the rows' own stores: 4096 x 16384 bf16 took 140 to 160 us with them, 134 with these.)
+// behind the rows' own stores: 4096 x 16384 bf16 took 140 to 160 us with them, 131 with these.)
 template <int kCluster>
 __device__ __noinline__ void drain_meeting(Meeting<kCluster>& m, int rank,
                                               unsigned long long* status) {
